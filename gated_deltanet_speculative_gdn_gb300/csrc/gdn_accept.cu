@@ -1,0 +1,400 @@
+// gdn_accept.cu - acceptance of drafted token trees on the device: rejection
+// sampling of the draft against the target's probabilities, from given uniforms.
+// It takes the place of the host's decision between verify and commit.
+//
+// Mathematics.  At node t with children x_1, x_2, ... drawn from q without
+// replacement, child x (token y) is accepted with probability p'(y) / q'(y), and
+// on rejection p' <- norm(max(p' - q', 0)), q' <- norm(q' without y).  Written
+// out, every p' along the way is max(p - c q, 0) / W for a number c: with
+// p' = max(p - c q, 0) / W and q' = q / Z off the rejected tokens,
+//     max(p' - q', 0) = max(p - c q - (W / Z) q, 0) / W,
+// since max(max(a, 0) - b, 0) = max(a - b, 0) for b >= 0; and the rejected token
+// itself drops out, as u >= (p - c q) Z / (q W) makes p - (c + W / Z) q <= 0.  So
+// a rejection costs one sum W = sum_v max(p_v - c q_v, 0) over a row of p and one
+// of q and nothing is rewritten, and an accepted first child costs no row at all.
+//
+// Precision.  The decisions and the place in the cumulative sum stand next to
+// borders, so p - c q is formed as an unevaluated pair of floats (Dekker's and
+// Knuth's error-free product and sum; c as a pair too) and summed as one: 2^-48
+// relative, at ~16 fp32 operations an element, where fp64 arithmetic would run at
+// 1/64 of that rate.  The few scalars are fp64.
+//
+// Mapping.  A cluster of CTAs takes a sequence, each CTA a contiguous slice of
+// the vocabulary.  Thread 0 of every CTA walks the tree with the same numbers (so
+// the CTAs agree without exchange) and calls for a pass when it needs a sum; a
+// pass sums each warp's contiguous range, and the CTAs' sums are exchanged
+// through distributed shared memory in rank order.  The last pass's sums are the
+// coarse cumulative sum: the CTA and the warp whose range holds the threshold
+// scan it, 128 elements at a time.  Bound by the rows it reads (1 MB a pass at
+// 131072 tokens) for many sequences, by the passes' latency for one.
+//
+// It does not release its dependent kernel early: the commits read `accepted`
+// before their own wait.
+#include <cooperative_groups.h>
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+
+namespace {
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarpsA = kThreads / 32, kMaxCluster = 8;
+
+struct AcceptArgs {
+    const float *__restrict__ p, *__restrict__ q;
+    int64_t p_stride, q_stride;
+    const int32_t *__restrict__ tokens, *__restrict__ parents, *__restrict__ node_off;
+    const float *__restrict__ u, *__restrict__ u_next;
+    int32_t *accepted, *next_token, *n_accepted, *status;
+    int S, N, V, max_nodes, replacement;
+};
+
+struct Pair {
+    float h, l;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+// max(p - (ch + cl) q, 0) as a pair
+__device__ __forceinline__ Pair residual(float p, float q, float ch, float cl) {
+    const float ph = __fmul_rn(ch, q), pl = __fmaf_rn(ch, q, -ph);
+    const Pair s = two_sum(p, -ph);
+    const float l = __fsub_rn(s.l, __fmaf_rn(cl, q, pl));
+    const float h = __fadd_rn(s.h, l);
+    if (!(h > 0.f)) return {0.f, 0.f};
+    return {h, __fsub_rn(l, __fsub_rn(h, s.h))};
+}
+__device__ __forceinline__ void add(Pair &acc, const Pair &v) {
+    const Pair s = two_sum(acc.h, v.h);
+    acc.h = s.h;
+    acc.l = __fadd_rn(acc.l, __fadd_rn(s.l, v.l));
+}
+
+// What a pass computes: rows of a node, c, and the tokens that are taken out.
+struct Pass {
+    const float *p, *q;  // q NULL: the residual is p
+    float ch, cl;
+    int n_out;
+    int last;  // the pass is the one that the next token comes from
+};
+
+// The four residuals of vector i of the row (elements 4 i ..; zero past V)
+__device__ __forceinline__ void load4(const Pass &ps, const int *out, int i, int V, Pair (&r)[4]) {
+    const float4 p4 = *reinterpret_cast<const float4 *>(ps.p + 4 * int64_t(i));
+    float pv[4] = {p4.x, p4.y, p4.z, p4.w};
+    if (ps.q) {
+        const float4 q4 = *reinterpret_cast<const float4 *>(ps.q + 4 * int64_t(i));
+        const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = residual(pv[e], qv[e], ps.ch, ps.cl);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = {pv[e] > 0.f ? pv[e] : 0.f, 0.f};
+    }
+    for (int k = 0; k < ps.n_out; ++k)
+        if ((out[k] >> 2) == i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if ((out[k] & 3) == e) r[e] = {0.f, 0.f};
+        }
+    if (4 * i + 3 >= V) {  // the row's last vector: what lies behind the row is not read as values
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (4 * i + e >= V) r[e] = {0.f, 0.f};
+    }
+}
+
+// Sum over the warp (lane 0's result is the one that is used).
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Pair w = {__shfl_down_sync(0xffffffffu, v.h, o), __shfl_down_sync(0xffffffffu, v.l, o)};
+        add(v, w);
+    }
+    return v;
+}
+
+// Sum of vectors [lo, hi) of the row, lanes side by side (lane 0's result).
+__device__ __forceinline__ Pair sum_range(const Pass &ps, const int *out, int lo, int hi, int V) {
+    Pair acc = {0.f, 0.f};
+#pragma unroll 4
+    for (int i = lo + (threadIdx.x & 31); i < hi; i += 32) {
+        Pair r[4];
+        load4(ps, out, i, V, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add(acc, r[e]);
+    }
+    return warp_sum(acc);
+}
+
+// Warp-collective: the first of `count` consecutive parts (lane k holds part k's
+// sum) whose cumulative sum, from b on, passes thr; b becomes the sum before it.
+// When none does (rounding at the very end, or no distribution) the last part
+// that is not empty, and thr becomes infinite, so that finer selections take the
+// last one too.
+__device__ __forceinline__ int select_part(double v, int count, double &b, double &thr) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= count) v = 0.0;
+    double inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, v > 0.0 && b + inc > thr);
+    const unsigned some = __ballot_sync(0xffffffffu, v > 0.0);
+    int k;
+    if (hit) {
+        k = __ffs(hit) - 1;
+    } else {
+        k = some ? 31 - __clz(some) : 0;
+        thr = __longlong_as_double(0x7ff0000000000000ll);
+    }
+    b += __shfl_sync(0xffffffffu, inc - v, k);
+    return k;
+}
+
+__global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs a) {
+    __shared__ Pair warp_tot[kWarpsA];
+    __shared__ Pair cta_tot[2][kMaxCluster];  // [pass parity][rank], written by every CTA of the cluster
+    __shared__ int par[gdn::kMaxSeqNodes], tok[gdn::kMaxSeqNodes], out[gdn::kMaxSeqNodes];
+    __shared__ float pc[gdn::kMaxSeqNodes], qc[gdn::kMaxSeqNodes], uc[gdn::kMaxSeqNodes];  // p, q at the parent's row
+    __shared__ Pass pass_s;
+    __shared__ int err_s, step_s;              // what follows the pass: another, the selection, nothing
+    __shared__ double base_s, thr_s;           // of the selection
+    __shared__ int lo_s, hi_s;
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+    const int s = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) err_s = 0;
+    __syncthreads();
+
+    // the tree and the drafted tokens' probabilities, all nodes at once
+    const int n0 = a.node_off[s], n1 = a.node_off[s + 1], n = n1 - n0;
+    if (n0 < 0 || n1 < n0 || n1 > a.N || (s == 0 && n0 != 0) || (s == a.S - 1 && n1 != a.N) || n > a.max_nodes) {
+        if (tid == 0) err_s = GDN_DEV_BAD_NODE_OFF;
+    } else if (tid < n) {
+        const int p = a.parents[n0 + tid];
+        par[tid] = p;
+        if (p >= tid || (tid == 0 ? p != -1 : p < 0)) atomicCAS(&err_s, 0, GDN_DEV_BAD_PARENT);
+    }
+    gdn::grid_dep_wait();  // the drafted tokens, the rows and the uniforms may come from kernels before this one
+    __syncthreads();
+    const bool tree_ok = err_s == 0;
+    __syncthreads();
+    if (tree_ok && tid > 0 && tid < n) {
+        const int y = a.tokens[n0 + tid];
+        tok[tid] = y;
+        uc[tid] = a.u[n0 + tid];
+        if (y < 0 || y >= a.V) {
+            atomicCAS(&err_s, 0, GDN_DEV_BAD_TOKEN);
+        } else {
+            const int64_t row = n0 + par[tid];
+            pc[tid] = a.p[row * a.p_stride + y];
+            qc[tid] = a.q ? a.q[row * a.q_stride + y] : 1.f;
+        }
+    }
+    cl.sync();  // also: every CTA of the cluster runs before another writes its shared memory
+    if (err_s || n == 0) {  // the whole cluster: every CTA has found the same
+        if (rank == 0 && tid == 0) {
+            if (err_s) gdn::record_status(a.status, err_s);
+            a.accepted[s] = -1;
+            a.next_token[s] = -1;
+            a.n_accepted[s] = 0;
+        }
+        return;
+    }
+
+    // vectors of the row: CTA `rank` takes [v0, v1), its warp w [w0, w1), in order
+    const int nvec = (a.V + 3) / 4;
+    const int per = (nvec + C - 1) / C, v0 = min(nvec, rank * per), v1 = min(nvec, v0 + per);
+    const int perw = (v1 - v0 + kWarpsA - 1) / kWarpsA, w0 = min(v1, v0 + warp * perw), w1 = min(v1, w0 + perw);
+
+    // thread 0's walk
+    int cur = 0, t = 1, depth = 1, n_out = 0, parity = 0;
+    double c = 0.0, W = 1.0, Z = 1.0;
+    bool fallback = false;
+    Pass ps;
+    for (;;) {
+        if (tid == 0) {
+            bool need = false;
+            while (t < n && !need) {
+                if (par[t] == cur && Z > 0.0) {
+                    const int y = tok[t];
+                    bool was_out = false;
+                    for (int k = 0; k < n_out; ++k) was_out |= out[k] == y;
+                    const double qx = was_out && a.q ? 0.0 : double(qc[t]);
+                    double px = was_out ? 0.0 : double(pc[t]) - (a.q ? c * double(qc[t]) : 0.0);
+                    px = px > 0.0 ? px : 0.0;
+                    if (double(uc[t]) * qx * W < px * Z) {
+                        cur = t;
+                        ++depth;
+                        n_out = 0;
+                        c = 0.0;
+                        W = Z = 1.0;
+                    } else {
+                        if (!(a.q && a.replacement) && !was_out) out[n_out++] = y;
+                        if (a.q) {
+                            c += W / Z;
+                            if (!a.replacement) Z = Z > qx ? Z - qx : 0.0;
+                            // the sum is wanted only if another child is tried
+                            for (int x = t + 1; x < n; ++x) need |= par[x] == cur;
+                            need = need && Z > 0.0;
+                        } else {
+                            W = W > px ? W - px : 0.0;
+                        }
+                    }
+                }
+                ++t;
+            }
+            const int64_t row = n0 + cur;
+            pass_s.p = a.p + row * a.p_stride;
+            pass_s.q = a.q && c > 0.0 && !fallback ? a.q + row * a.q_stride : nullptr;
+            pass_s.ch = float(c);
+            pass_s.cl = float(c - double(float(c)));
+            pass_s.n_out = fallback ? 0 : n_out;
+            pass_s.last = !need;
+        }
+        __syncthreads();
+        ps = pass_s;
+        const Pair wt = sum_range(ps, out, w0, w1, a.V);
+        if (lane == 0) warp_tot[warp] = wt;
+        __syncthreads();
+        if (warp == 0) {
+            Pair v = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
+            v = warp_sum(v);
+            v.h = __shfl_sync(0xffffffffu, v.h, 0);
+            v.l = __shfl_sync(0xffffffffu, v.l, 0);
+            if (lane < C) cl.map_shared_rank(&cta_tot[0][0], lane)[parity * kMaxCluster + rank] = v;
+        }
+        cl.sync();
+        if (warp == 0) {
+            const Pair mine = lane < C ? cta_tot[parity][lane] : Pair{0.f, 0.f};
+            const Pair sum = warp_sum(mine);
+            double total = double(sum.h) + double(sum.l);
+            total = __shfl_sync(0xffffffffu, total, 0);
+            int step = 0;
+            if (ps.last) {
+                const bool empty = !(total > 0.0) && !__shfl_sync(0xffffffffu, int(fallback), 0);
+                if (empty) {
+                    fallback = true;  // nothing is left: the target's own row
+                } else {
+                    double b = 0.0, thr = double(a.u_next[s]) * total;
+                    const bool owner = select_part(double(mine.h) + double(mine.l), C, b, thr) == rank;
+                    step = owner ? 2 : 1;
+                    if (owner) {
+                        const Pair w = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
+                        const int k = select_part(double(w.h) + double(w.l), kWarpsA, b, thr);
+                        if (lane == 0) {
+                            base_s = b;
+                            thr_s = thr;
+                            lo_s = min(v1, v0 + k * perw);
+                            hi_s = min(v1, v0 + (k + 1) * perw);
+                        }
+                    }
+                }
+            }
+            if (lane == 0) {
+                W = total;
+                step_s = step;
+            }
+        }
+        parity ^= 1;
+        __syncthreads();
+        if (step_s) break;
+    }
+
+    // ---- the next token: the owner narrows its warp's range down to 32 vectors
+    if (rank == 0 && tid == 0) {
+        a.accepted[s] = cur;
+        a.n_accepted[s] = depth;
+    }
+    if (step_s != 2) return;
+    while (hi_s - lo_s > 32) {
+        const int lo = lo_s, hi = hi_s, part = (hi - lo + kWarpsA - 1) / kWarpsA;
+        const Pair wt = sum_range(ps, out, min(hi, lo + warp * part), min(hi, lo + (warp + 1) * part), a.V);
+        if (lane == 0) warp_tot[warp] = wt;
+        __syncthreads();
+        if (warp == 0) {
+            const Pair w = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
+            double b = base_s, thr = thr_s;
+            const int k = select_part(double(w.h) + double(w.l), kWarpsA, b, thr);
+            if (lane == 0) {
+                base_s = b;
+                thr_s = thr;
+                lo_s = min(hi, lo + k * part);
+                hi_s = min(hi, lo + (k + 1) * part);
+            }
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+        Pair r[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+        const int i = lo_s + lane;
+        if (i < hi_s) load4(ps, out, i, a.V, r);
+        double e[4], run = 0.0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            run += double(r[k].h) + double(r[k].l);
+            e[k] = run;
+        }
+        double b = base_s, thr = thr_s;
+        const int src = select_part(run, 32, b, thr);
+        if (lane == src) {
+            int k = 0;
+            while (k < 3 && !(r[k].h > 0.f && b + e[k] > thr)) ++k;
+            while (k > 0 && !(r[k].h > 0.f)) --k;  // rounding: the lane's last element that is not 0
+            a.next_token[s] = min(max(4 * i + k, 0), a.V - 1);
+        }
+    }
+}
+
+}  // namespace
+
+extern "C" int gdn_tree_accept(const gdn_dims *dims, int vocab, const float *p, int64_t p_stride, const float *q,
+                               int64_t q_stride, int replacement, const int32_t *tokens, const int32_t *parents,
+                               const int32_t *node_off, const float *u, const float *u_next, int32_t *accepted,
+                               int32_t *next_token, int32_t *n_accepted, int32_t *status, void *stream) {
+    int rc = gdn::check_dims(dims);
+    if (rc) return rc;
+    if (!status) return GDN_ERR_NULL;
+    if (vocab < 1 || vocab > (1 << 28) || (replacement != 0 && replacement != 1)) return GDN_ERR_ARG;
+    const int64_t S = dims->n_seqs, N = dims->n_nodes;
+    if (S == 0) return GDN_OK;
+    if (!node_off || !accepted || !next_token || !n_accepted || !u_next ||
+        (N > 0 && (!p || !tokens || !parents || !u)))
+        return GDN_ERR_NULL;
+    const int64_t row = (int64_t(vocab) + 3) / 4 * 4;
+    if (N > 0 && (p_stride < row || p_stride % 4 || (q && (q_stride < row || q_stride % 4)))) return GDN_ERR_STRIDE;
+    if (!gdn::aligned16(p) || !gdn::aligned16(q)) return GDN_ERR_ALIGN;
+    const gdn::Span outs[] = {{accepted, size_t(S * 4)}, {next_token, size_t(S * 4)}, {n_accepted, size_t(S * 4)}};
+    const gdn::Span ins[] = {{p, gdn::strided_bytes(N, p_stride, row)},
+                             {q, gdn::strided_bytes(N, q_stride, row)},
+                             {tokens, size_t(N * 4)},
+                             {parents, size_t(N * 4)},
+                             {node_off, size_t((S + 1) * 4)},
+                             {u, size_t(N * 4)},
+                             {u_next, size_t(S * 4)},
+                             {status, 4}};
+    if ((rc = gdn::check_alias(outs, 3, ins, 8))) return rc;
+
+    AcceptArgs a{p, q, p_stride, q_stride, tokens, parents, node_off, u, u_next, accepted, next_token, n_accepted,
+                 status, int(S), int(N), vocab, dims->max_seq_nodes, replacement};
+    // a CTA's slice is at least 2048 elements (one vector a thread)
+    int C = 1;
+    while (C < kMaxCluster && int64_t(vocab) / (2 * C) >= 2048) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(S * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = unsigned(C);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, tree_accept_kernel, a) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}

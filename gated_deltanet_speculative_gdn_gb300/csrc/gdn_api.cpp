@@ -20,6 +20,10 @@ extern "C" const char *gdn_status_str(int code) {
         case GDN_DEV_BAD_ACCEPTED: return "GDN_DEV_BAD_ACCEPTED";
         case GDN_DEV_TIMEOUT: return "GDN_DEV_TIMEOUT";
         case GDN_DEV_BAD_WINDOW: return "GDN_DEV_BAD_WINDOW";
+        case GDN_DEV_BAD_PAGE: return "GDN_DEV_BAD_PAGE";
+        case GDN_DEV_BAD_LEN: return "GDN_DEV_BAD_LEN";
+        case GDN_DEV_BAD_AXIS: return "GDN_DEV_BAD_AXIS";
+        case GDN_DEV_BAD_TOKEN: return "GDN_DEV_BAD_TOKEN";
         default: return "unknown";
     }
 }

@@ -1,0 +1,238 @@
+// gdn_rope.cu - q/k RMS norm, rotary positions with several axes, and the append
+// of the new tokens' keys and values to the paged cache: what a full-attention
+// layer of a hybrid model does before its attention.
+//
+// Mathematics.  A pair (y_a, y_b) is turned by phi = pos * f.  Far positions need
+// phi mod 2 pi to more than fp32: with f / (2 pi) mod 1 as a 64-bit fraction F,
+// the product pos * F wraps modulo 2^64, which is the reduction modulo one turn
+// itself, exact but for F's own rounding (2^-53 relative).  The top 32 bits, as a
+// signed fraction, go to sincospif.
+//
+// Mapping.  A warp takes one token and a share of its rows (q heads, k heads, v
+// heads); a lane holds 8 elements (128-bit loads and stores), so a row of d takes
+// d / 8 lanes and 256 / d rows go at a time.  The pair partner of a lane's 8
+// elements is a whole lane away (rot_dim is a multiple of 16), fetched by
+// shuffles.  The sines and cosines are formed once per token and warp and stay in
+// registers over its rows.  Bound by HBM: each row is read and written once.
+#include "gdn_attn.h"
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr double kInv2Pi = 0.15915494309189533576888376337251;
+
+struct RopeArgs {
+    const void *__restrict__ q, *__restrict__ k, *__restrict__ v;
+    int64_t q_stride, k_stride, v_stride, qo_stride;
+    const float *__restrict__ qw, *__restrict__ kw;
+    float eps;
+    const int32_t *__restrict__ pos;
+    const double *__restrict__ inv_freq;
+    const int32_t *__restrict__ axis;
+    int n_axes, rot, interleaved;
+    const int32_t *__restrict__ node_off, *__restrict__ ctx_len;
+    gdn::PagedLayout pl;
+    void *qo;
+    void *k_pool, *v_pool;
+    int32_t *status;
+    int S, N, max_tokens, Hq, Hkv, shares;  // shares: warps of a token
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs a) {
+    constexpr int LH = D / 8, RW = 32 / LH;  // lanes of a row, rows of a warp
+    const unsigned full = 0xffffffffu;
+    gdn::grid_dep_launch();
+    const int lane = threadIdx.x & 31, sub = lane / LH, l = lane % LH;
+    const int64_t wid = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    if (blockIdx.x == 0) {
+        const int err = gdn::check_node_off(a.node_off, a.S, a.N, a.max_tokens, threadIdx.x, kWarps * 32);
+        gdn::grid_dep_wait();
+        if (err) gdn::record_status(a.status, err);
+    } else {
+        gdn::grid_dep_wait();
+    }
+    const int n = int(wid / a.shares), share = int(wid % a.shares);
+    if (n >= a.N) return;
+    const int s = gdn::find_sequence(a.node_off, a.S, n);
+    const int n0 = a.node_off[s], ctx = a.ctx_len[s];
+    const int i = n - n0;
+    int64_t place = -1;  // element offset of the token in the pools
+    {
+        int err = 0;
+        const int64_t x = int64_t(ctx) + i;
+        if (i < 0 || i >= a.max_tokens || n >= a.node_off[s + 1]) {
+            err = GDN_DEV_BAD_NODE_OFF;
+        } else if (ctx < 0 || x >= (int64_t(a.pl.width) << a.pl.shift)) {
+            err = GDN_DEV_BAD_LEN;
+        } else {
+            place = gdn::position_offset(a.pl, s, int(x));
+            if (place < 0) err = GDN_DEV_BAD_PAGE;
+        }
+        if (err && lane == 0) gdn::record_status(a.status, err);
+    }
+
+    // the lane's cosines and sines: element e of the lane is column 8 l + e
+    const int half = a.rot / 2, col = 8 * l;
+    const bool turned = col < a.rot;
+    const bool upper = !a.interleaved && col >= half;  // the lane holds second elements of pairs
+    float cs[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+    }
+    if (turned) {
+        const int pairs = a.interleaved ? 4 : 8;
+        const int p0 = a.interleaved ? col / 2 : (upper ? col - half : col);
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e >= pairs) break;
+            int ax = a.axis ? a.axis[p0 + e] : 0;
+            if (ax < 0 || ax >= a.n_axes) {
+                bad = true;
+                ax = 0;
+            }
+            double f = a.inv_freq[p0 + e] * kInv2Pi;  // turns per position
+            f -= floor(f);
+            const unsigned long long frac = __double2ull_rz(f * 18446744073709551616.0);
+            const unsigned long long turns =
+                static_cast<unsigned long long>(static_cast<long long>(a.pos[int64_t(n) * a.n_axes + ax])) * frac;
+            // a signed 32-bit fraction of a turn, in units of half turns
+            sincospif(float(int(turns >> 32)) * (1.0f / 2147483648.0f), &sn[e], &cs[e]);
+        }
+        if (bad) gdn::record_status(a.status, GDN_DEV_BAD_AXIS);
+        if (a.interleaved) {  // pair p of the lane: elements 2 p, 2 p + 1
+#pragma unroll
+            for (int e = 7; e >= 0; --e) {
+                cs[e] = cs[e / 2];
+                sn[e] = sn[e / 2];
+            }
+        }
+    }
+    const int hop = a.rot / 16;  // lanes between the halves of a pair
+    const int partner = turned && !a.interleaved ? (upper ? lane - hop : lane + hop) : lane;
+    const int rows = a.Hq + 2 * a.Hkv, slots = (rows + RW - 1) / RW;
+    float qw[8], kw[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        qw[e] = a.qw ? a.qw[col + e] : 1.f;
+        kw[e] = a.kw ? a.kw[col + e] : 1.f;
+    }
+
+    for (int slot = share; slot < slots; slot += a.shares) {
+        const int r = slot * RW + sub;  // q heads, then k heads, then v heads
+        const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv, live = r < rows;
+        const int h = is_q ? r : is_k ? r - a.Hq : r - a.Hq - a.Hkv;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (live) {
+            const T *src = is_q ? static_cast<const T *>(a.q) + n * a.q_stride
+                                : is_k ? static_cast<const T *>(a.k) + n * a.k_stride
+                                       : static_cast<const T *>(a.v) + n * a.v_stride;
+            raw = *reinterpret_cast<const uint4 *>(src + int64_t(h) * D + col);
+        }
+        float y[8], z[8];
+        gdn::unpack8<T>(raw, y);
+        const bool norm = live && ((is_q && a.qw) || (is_k && a.kw));
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+        for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(full, ss, o);
+        if (norm) {
+            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * (is_q ? qw[e] : kw[e]);
+        }
+        if (a.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = (e & 1) ? y[e] * cs[e] + y[e - 1] * sn[e] : y[e] * cs[e] - y[e + 1] * sn[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float other = __shfl_sync(full, y[e], partner);
+                z[e] = upper ? y[e] * cs[e] + other * sn[e] : y[e] * cs[e] - other * sn[e];
+            }
+        }
+        if (!live) continue;
+        // untouched values are copied, not converted: a NaN keeps its bits
+        const uint4 out = (is_q || is_k) && (turned || norm) ? gdn::pack8<T>(z) : raw;
+        if (is_q) {
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.qo) + n * a.qo_stride + int64_t(h) * D + col) = out;
+        } else if (place >= 0) {
+            T *pool = static_cast<T *>(is_k ? a.k_pool : a.v_pool);
+            *reinterpret_cast<uint4 *>(pool + place + int64_t(h) * a.pl.head_stride + col) = out;
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch(int d, dim3 grid, cudaStream_t st, const RopeArgs &a) {
+    const dim3 block(kWarps * 32);
+    switch (d) {
+        case 64: return gdn::launch_pdl(rope_append_kernel<T, 64>, grid, block, 0, st, a);
+        case 128: return gdn::launch_pdl(rope_append_kernel<T, 128>, grid, block, 0, st, a);
+        default: return gdn::launch_pdl(rope_append_kernel<T, 256>, grid, block, 0, st, a);
+    }
+}
+
+}  // namespace
+
+extern "C" int gdn_rope_append(const gdn_attn_dims *dims, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                               const void *v, int64_t v_stride, const float *q_norm_w, const float *k_norm_w, float eps,
+                               const int32_t *pos, int n_axes, const double *inv_freq, const int32_t *axis, int rot_dim,
+                               int interleaved, const int32_t *node_off, const int32_t *ctx_len, const int32_t *page_table,
+                               void *q_out, int64_t q_out_stride, void *k_pool, void *v_pool, int32_t *status,
+                               void *stream) {
+    int rc = gdn::check_attn_dims(dims);
+    if (rc) return rc;
+    if (!status) return GDN_ERR_NULL;
+    if (rot_dim < 0 || rot_dim > dims->d_head || rot_dim % 16 != 0 || n_axes < 1 || n_axes > 4 ||
+        (interleaved != 0 && interleaved != 1) || !(eps >= 0.0f) || !(eps < 3.0e38f))
+        return GDN_ERR_ARG;
+    const int64_t S = dims->n_seqs, N = dims->n_tokens, Hq = dims->h_q, Hkv = dims->h_kv, D = dims->d_head;
+    if (S == 0 || N == 0) return GDN_OK;
+    if (!q || !k || !v || !node_off || !ctx_len || !page_table || !q_out || !k_pool || !v_pool) return GDN_ERR_NULL;
+    if (rot_dim > 0 && (!pos || !inv_freq)) return GDN_ERR_NULL;
+    if (q_stride < Hq * D || k_stride < Hkv * D || v_stride < Hkv * D || q_out_stride < Hq * D || q_stride % 8 ||
+        k_stride % 8 || v_stride % 8 || q_out_stride % 8)
+        return GDN_ERR_STRIDE;
+    if (!gdn::aligned16(q) || !gdn::aligned16(k) || !gdn::aligned16(v) || !gdn::aligned16(q_out) ||
+        !gdn::aligned16(k_pool) || !gdn::aligned16(v_pool) || !gdn::aligned16(q_norm_w) || !gdn::aligned16(k_norm_w) ||
+        (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+        return GDN_ERR_ALIGN;
+    const size_t pool = gdn::pool_bytes(dims);
+    const gdn::Span qs{q, gdn::rows_bytes16(N, q_stride, Hq * D)}, qos{q_out, gdn::rows_bytes16(N, q_out_stride, Hq * D)};
+    const gdn::Span ins[] = {{k, gdn::rows_bytes16(N, k_stride, Hkv * D)},
+                             {v, gdn::rows_bytes16(N, v_stride, Hkv * D)},
+                             {q_norm_w, size_t(D * 4)},
+                             {k_norm_w, size_t(D * 4)},
+                             {pos, size_t(N * n_axes * 4)},
+                             {inv_freq, size_t(rot_dim * 4)},
+                             {axis, size_t(rot_dim * 2)},
+                             {node_off, size_t((S + 1) * 4)},
+                             {ctx_len, size_t(S * 4)},
+                             {page_table, size_t(S * int64_t(dims->table_width) * 4)},
+                             {status, 4}};
+    // the pools may interleave, so they are not checked against each other
+    const gdn::Span ko[] = {{k_pool, pool}, qos}, vo[] = {{v_pool, pool}, qos};
+    if ((rc = gdn::check_alias(ko, 2, ins, 11)) || (rc = gdn::check_alias(vo, 2, ins, 11))) return rc;
+    if (gdn::overlaps(qs, ko[0]) || gdn::overlaps(qs, vo[0])) return GDN_ERR_ALIAS;
+    if (gdn::overlaps(qs, qos) && !(q == q_out && q_stride == q_out_stride)) return GDN_ERR_ALIAS;
+
+    // a token's rows are shared by as many warps as it takes to fill the GPU
+    // when there are few tokens; a warp with all rows of a token forms the
+    // angles once for all of them
+    const int64_t slots = (Hq + 2 * Hkv + 256 / D - 1) / (256 / D);
+    const int64_t want = 152 * 24;
+    const int64_t shares = N >= want ? 1 : (want / N < slots ? want / N : slots);
+    RopeArgs a{q, k, v, q_stride, k_stride, v_stride, q_out_stride, q_norm_w, k_norm_w, eps, pos, inv_freq, axis,
+               n_axes, rot_dim, interleaved, node_off, ctx_len, gdn::paged_layout(dims, page_table), q_out, k_pool, v_pool,
+               status, int(S), int(N), dims->max_seq_tokens, int(Hq), int(Hkv), int(shares)};
+    const dim3 grid(unsigned((N * shares + kWarps - 1) / kWarps));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dims->dtype == GDN_BF16 ? launch<__nv_bfloat16>(int(D), grid, st, a)
+                                                  : launch<__half>(int(D), grid, st, a);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}

@@ -120,7 +120,11 @@ enum {
     GDN_DEV_DUP_SLOT = 4,      /* two committing sequences share a slot           */
     GDN_DEV_BAD_ACCEPTED = 5,  /* accepted[s] outside [-1, N_s)                   */
     GDN_DEV_TIMEOUT = 6,       /* a bounded wait in a kernel ran out              */
-    GDN_DEV_BAD_WINDOW = 7     /* a window reference outside [-3, N) (compact)    */
+    GDN_DEV_BAD_WINDOW = 7,    /* a window reference outside [-3, N) (compact)    */
+    GDN_DEV_BAD_PAGE = 8,      /* a page index outside [0, n_pages)               */
+    GDN_DEV_BAD_LEN = 9,       /* ctx_len[s] < 0, or the new tokens pass the table */
+    GDN_DEV_BAD_AXIS = 10,     /* axis[i] outside [0, n_axes) (rope)              */
+    GDN_DEV_BAD_TOKEN = 11     /* a drafted token outside [0, vocab)              */
 };
 
 /* Conv tree step (lucebox PR #707, Optimizations: fused convolution
@@ -276,6 +280,153 @@ int gdn_decode_step(const gdn_dims *dims, const float *x, int64_t x_stride, cons
                     float *conv_hist, const float *ba, int64_t ba_stride, const float *dt_bias,
                     const float *A, float *ssm, float q_scale, const int32_t *slot_map, float *xc,
                     float *o, int32_t *status, void *stream);
+
+/* Attention layers of the round
+ * -----------------------------
+ * A hybrid model runs full-attention layers between its GDN layers.  Their keys
+ * and values live in a paged cache: pools of n_pages pages of page_size tokens,
+ * and a page table that names, for each sequence, the page of each run of
+ * page_size positions.  Position x of sequence s is token x % page_size of page
+ * page_table[s][x / page_size].  Sequence s has ctx_len[s] cached positions; the
+ * new token i of this call (tokens node_off[s] .. node_off[s + 1] - 1 of the
+ * batch, as for the trees above) takes position ctx_len[s] + i.
+ *   gdn_rope_append      writes the new tokens' keys and values there
+ *   gdn_paged_attention  reads them together with the context
+ *   gdn_kv_commit        once acceptance is known, moves the accepted path's
+ *                        keys and values to positions ctx_len[s] + 0, 1, ...
+ * 16-bit tensors hold bf16 or fp16 (dims->dtype).  Both pools have the same
+ * strides, in elements, so a cache of [page][token][head][d], of
+ * [page][head][token][d] or one that interleaves keys and values all work. */
+enum { GDN_BF16 = 0, GDN_FP16 = 1 };
+
+typedef struct {
+    int32_t n_seqs;          /* S                                                   */
+    int32_t n_tokens;        /* N, new tokens over all sequences                    */
+    int32_t max_seq_tokens;  /* bound on any sequence's new tokens                  */
+    int32_t h_q;             /* query heads (multiple of h_kv, h_q / h_kv <= 128)   */
+    int32_t h_kv;            /* key/value heads                                     */
+    int32_t d_head;          /* head width, in {64, 128, 256}                       */
+    int32_t dtype;           /* GDN_BF16 or GDN_FP16                                */
+    int32_t n_pages;         /* pages in each pool                                  */
+    int32_t page_size;       /* tokens of a page: a power of two, 8..1024           */
+    int32_t table_width;     /* page-table entries of a sequence                    */
+    int64_t page_stride;     /* elements between pages (multiples of 8, as are ...) */
+    int64_t token_stride;    /* ... between the tokens of a page                    */
+    int64_t head_stride;     /* ... between the heads of a token                    */
+} gdn_attn_dims;
+
+/* q/k RMS norm, rotary positions, and the append to the cache.  For token n and
+ * each head x of q (h_q of them) and k (h_kv):
+ *     y = x                                             without a norm weight
+ *     y = x / sqrt(mean(x^2) + eps) * w                 with one (q_norm_w, k_norm_w)
+ *     phi_i = pos[n][axis[i]] * inv_freq[i]             i = 0 .. rot_dim / 2 - 1
+ *     (z_a, z_b) = (y_a cos phi_i - y_b sin phi_i, y_b cos phi_i + y_a sin phi_i)
+ * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when `interleaved`; the
+ * d_head - rot_dim other elements keep y.  q rows go to q_out, k rows and the
+ * plain v rows to the pools.  A token has n_axes positions (time, height, width
+ * of an image's patches, say); `axis` gives each frequency its axis, so sections
+ * and interleaved layouts are both a table.  Angles are exact to 2^-53 of
+ * inv_freq for any int32 position.
+ *   q [N][q_stride], k [N][k_stride], v [N][v_stride]   in, 16-bit, strides in
+ *            elements, multiples of 8
+ *   q_norm_w, k_norm_w  [d_head] fp32, or NULL
+ *   pos      [N][n_axes] int32;  inv_freq [rot_dim / 2] fp64
+ *   axis     [rot_dim / 2] int32, or NULL (axis 0);  n_axes 1..4
+ *   rot_dim  a multiple of 16, 0 .. d_head (0: no rotation)
+ *   q_out    [N][q_out_stride] out; may be q itself with the same stride
+ * Host errors: GDN_ERR_ARG for eps, n_axes, rot_dim or interleaved.
+ * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_LEN, GDN_DEV_BAD_PAGE (the
+ * token's k and v are not written), GDN_DEV_BAD_AXIS. */
+int gdn_rope_append(const gdn_attn_dims *dims, const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const void *v, int64_t v_stride, const float *q_norm_w,
+                    const float *k_norm_w, float eps, const int32_t *pos, int n_axes,
+                    const double *inv_freq, const int32_t *axis, int rot_dim, int interleaved,
+                    const int32_t *node_off, const int32_t *ctx_len, const int32_t *page_table,
+                    void *q_out, int64_t q_out_stride, void *k_pool, void *v_pool, int32_t *status,
+                    void *stream);
+
+/* Attention of the new tokens over the paged cache.  New token i of sequence s,
+ * query head h, key/value head h / (h_q / h_kv):
+ *     o[n][h] = sum_x p_x v_x,   p = softmax over the positions it sees of
+ *               scale * q[n][h] . k_x
+ * It sees the positions below ctx_len[s], itself, and of the other new tokens
+ * those before it (parents NULL: a prompt's chunk, a chain, one token) or its
+ * ancestors (parents as for the trees, max_seq_tokens <= 64).  What it does not
+ * see has no influence, whatever it holds: NaN and infinities in the rest of a
+ * page or in other branches stay there.
+ *   q [N][q_stride] in (16-byte aligned rows);  o [N][h_q * d_head] out
+ *   k_pool, v_pool, page_table, ctx_len, node_off, parents  in
+ *   scale    finite, > 0
+ *   workspace  at least gdn_attention_workspace_bytes(dims) bytes, 16-byte
+ *            aligned, contents irrelevant before and after the call
+ * Host errors: GDN_ERR_ARG for scale or a workspace too small.
+ * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_PARENT, GDN_DEV_BAD_LEN,
+ * GDN_DEV_BAD_PAGE, GDN_DEV_TIMEOUT. */
+int gdn_paged_attention(const gdn_attn_dims *dims, const void *q, int64_t q_stride,
+                        const void *k_pool, const void *v_pool, const int32_t *page_table,
+                        const int32_t *ctx_len, const int32_t *node_off, const int32_t *parents,
+                        float scale, void *o, void *workspace, int64_t workspace_bytes,
+                        int32_t *status, void *stream);
+
+/* Workspace of gdn_paged_attention on the current device, in bytes (0 for dims
+ * that the call refuses).  It does not depend on the lengths. */
+size_t gdn_attention_workspace_bytes(const gdn_attn_dims *dims);
+
+/* Commit of the accepted path in the cache, the attention layers' part of
+ * gdn_commit, for n_layers layers at once (pool of layer l at k_pool +
+ * l * layer_stride elements, one page table for all).  With p_0 < p_1 < ... the
+ * path root .. accepted[s] (m nodes), for every layer and head
+ *     position ctx_len[s] + j  <-  position ctx_len[s] + p_j        j = 0 .. m - 1
+ * in k_pool and v_pool, and new_len[s] = ctx_len[s] + m.  accepted[s] = -1 moves
+ * nothing (m = 0).  As for gdn_commit, a preflight checks every sequence first;
+ * if a check fails, or *status is already non-zero, nothing is written.
+ *   max_seq_tokens <= 64; h_q is not used (give h_kv)
+ *   accepted [S], parents [N], node_off, ctx_len, page_table in; new_len [S] out
+ *            (must not overlap ctx_len); layer_stride a multiple of 8
+ * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_ACCEPTED,
+ * GDN_DEV_BAD_PARENT, GDN_DEV_BAD_LEN, GDN_DEV_BAD_PAGE. */
+int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
+                  const int32_t *accepted, const int32_t *parents, const int32_t *node_off,
+                  const int32_t *ctx_len, const int32_t *page_table, void *k_pool, void *v_pool,
+                  int32_t *new_len, int32_t *status, void *stream);
+
+/* Acceptance of drafted trees on the device (lucebox PR #707 leaves it to the
+ * host between verify and commit).  Node 0 of a sequence is its last sampled
+ * token, always accepted; the other nodes are drafted, tokens[n] each, children
+ * tried in the order of their index.  p[n] is the target's distribution after
+ * node n, q[n] the one the draft drew n's children from.  At node t, with
+ * c = 0, W = Z = 1 at first, child x with uniform u[x] and token y is
+ *     accepted   if u[x] q[t][y] W < max(p[t][y] - c q[t][y], 0) Z
+ * and the walk goes on at x; otherwise, in this order,
+ *     c <- c + W / Z,  Z <- max(Z - q[t][y], 0),  y is taken out,
+ *     W <- sum over the vocabulary of max(p[t] - c q[t], 0)
+ * so that max(p - c q, 0) / W is the residual distribution of rejection
+ * sampling without replacement (Z = 0, a draft with nothing left: no further
+ * child is tried).  When no child is left the next token is drawn
+ * from that residual (from p[t] itself when its sum is 0): the first y whose
+ * cumulative sum passes u_next[s] times the total.  The tokens that come out are
+ * distributed as the target's.  Sums, c, W and Z carry at least 44 bits.
+ *   replacement  0: as above.  1: the draft draws children independently (Z
+ *            stays 1 and nothing is taken out)
+ *   q        NULL: the children are proposed outright (q[t][y] = 1 for them;
+ *            the residual is p without the rejected tokens, W <- W - p[t][y])
+ *   dims     n_seqs, n_nodes, max_seq_nodes (the GDN layers' dims as they are)
+ *   p [N][p_stride], q [N][q_stride]   fp32 rows of `vocab` probabilities
+ *   tokens [N] (node 0's is not read), parents, node_off, u [N], u_next [S]  in
+ *   accepted [S]   deepest accepted node (-1 for a sequence without nodes): the
+ *                  argument of gdn_commit and gdn_kv_commit
+ *   next_token [S] the token that follows it (-1 for a sequence without nodes)
+ *   n_accepted [S] nodes of the accepted path, node 0 included
+ * Rows that are not distributions give tokens in [0, vocab) of no meaning.
+ * Host errors: GDN_ERR_ARG for vocab or replacement.
+ * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_PARENT (not before its
+ * child, or a root other than node 0), GDN_DEV_BAD_TOKEN; the sequence's
+ * outputs are then -1, -1 and 0. */
+int gdn_tree_accept(const gdn_dims *dims, int vocab, const float *p, int64_t p_stride,
+                    const float *q, int64_t q_stride, int replacement, const int32_t *tokens,
+                    const int32_t *parents, const int32_t *node_off, const float *u,
+                    const float *u_next, int32_t *accepted, int32_t *next_token,
+                    int32_t *n_accepted, int32_t *status, void *stream);
 
 /* Test hook for the device timeout path.  The next call that runs a
  * tensor-core verify kernel (gdn_tree_verify with d = 128 and
