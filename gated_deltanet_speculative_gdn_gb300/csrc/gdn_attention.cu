@@ -1,107 +1,879 @@
-// gdn_attention.cu - attention of a chunk of new tokens over a paged cache.
+// gdn_attention.cu - attention of a chunk of new tokens over a paged cache: the
+// full-attention layers of a speculative round (token trees), of a prompt's chunk
+// and of plain decode, in one kernel.
 //
-// First form: a warp per (token, query head), one pass over the positions it
-// sees with a running maximum and sum.
+// Mathematics.  One pass over the positions with a running reference m and sum l:
+//     p_x = 2^(c s_x - m),  l += p_x,  O += p_x v_x,   c = scale log2(e)
+// where m is the running maximum when it was last moved.  It is moved (l and O
+// scaled by 2^(m - m')) only when the maximum has grown by more than 2^8: until
+// then p stays below 2^8, which costs no precision in a floating type.  Parts of a
+// row's positions are joined by the same rule: o = sum 2^(m_i - M) O_i / sum
+// 2^(m_i - M) l_i.
+//
+// Rounding.  The products run on the tensor cores with 16-bit operands and fp32
+// accumulators, so p is rounded to the cache's type before P V (a relative half
+// step of that type, as the result's own rounding); l sums the unrounded p.
+//
+// Work.  The h_q / h_kv heads that share a key/value head are rows of one tile:
+// row r is (token i0 + r / G, head r % G), 128 / G tokens a tile, so keys and
+// values are read once for all of them.  An item is (sequence, key/value head, row
+// tile); its positions come in tiles of TK.  All items' tiles in a row are cut into
+// equal shares, one per CTA (one CTA per SM): lengths as ragged as they come keep
+// every SM busy to the end, one sequence alone spreads over the GPU, and a CTA has
+// at most one item that began before it and one that ends after it.  Those parts
+// go to the workspace and a second kernel joins them in CTA order, so results do
+// not depend on timing.
+//
+// Mapping (GB300).  Tensor memory holds O (D columns, fp32), Q (D / 2 columns, the
+// A operand of Q K^T: nothing of it is read again from shared memory, which leaves
+// all of that to keys and values) and two score tiles (TK columns each), P taking
+// its scores' place as the A operand of P V.  Shared memory is a ring of 192 KB of
+// key and value tiles, filled by TMA page by page in the 128-byte swizzle: keys as
+// they lie are the K-major B operand, values as they lie the MN-major one.
+//   warps 0-3  row r = 32 w + lane = tensor-memory lane: Q in, scores -> P, moves
+//              of m, results out
+//   warp 4     TMA: K_0 K_1 V_0 K_2 V_1 ...; a lane per (page, 64 columns)
+//   warp 5     tcgen05.mma: S_{i+1} = Q K_{i+1}^T is issued before P_i is awaited,
+//              so the tensor cores run while the softmax does
+//   warps 6-7  values of tiles in which some rows do not see some positions: what
+//              no row sees (the rest of a page) is set to 0, and elements that are
+//              not finite are set to 0 and remembered, since 0 * NaN in P V would
+//              reach rows that do not see them; rows that do get them back at the
+//              end
+// Every mbarrier completes once per use, so a counter gives every wait's phase.
+#include <type_traits>
+
 #include "gdn_attn.h"
+#include "gdn_tma.h"
 
 namespace {
+namespace att {
 
-struct AttnArgs {
-    const void *__restrict__ q;
-    int64_t q_stride;
-    const void *__restrict__ k_pool, *__restrict__ v_pool;
-    gdn::PagedLayout pl;
-    const int32_t *__restrict__ ctx_len, *__restrict__ node_off, *__restrict__ parents;
-    float scale;
-    void *o;
-    int32_t *status;
-    int S, N, max_tokens, Hq, Hkv;
+constexpr int kThreads = 256, kTma = 4, kMma = 5, kClean0 = 6;
+constexpr int kRows = 128;
+constexpr int kNfBufs = 8;  // the ring holds the values of 6 segments at most, and one may still be going out
+
+template <int D_>
+struct Cfg {
+    static constexpr int D = D_;
+    static constexpr int TK = D == 256 ? 64 : 128;        // positions of a tile
+    static constexpr int kChunks = D / 64;                // 128-byte columns of a row
+    static constexpr uint32_t kChunkBytes = TK * 128;
+    static constexpr uint32_t kTile = TK * D * 2;         // 32 KB, 32 KB, 16 KB
+    static constexpr int kStages = 196608 / kTile;
+    static constexpr size_t kSmem = 1024 + 196608;
+    // tensor-memory columns
+    static constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2;
+    static_assert(D + D / 2 + 2 * TK <= 512, "tensor memory");
+    // workspace of a CTA: two parts (0: an item that began before, 1: one that goes on) of m, l and O
+    static constexpr size_t kPartFloats = size_t(kRows) * (D + 2);
 };
 
+struct Args {
+    const void *__restrict__ q;
+    int64_t q_stride;
+    const void *__restrict__ v_pool;  // read directly only for values that are not finite
+    gdn::PagedLayout pl;
+    const int32_t *__restrict__ ctx_len, *__restrict__ node_off, *__restrict__ parents;
+    float c;  // scale * log2(e)
+    void *o;
+    int32_t *status;
+    float *parts;  // [CTA][2][part]
+    int4 *meta;    // [CTA][2]: rows of the part (0: none), ends, token n0 + i0, key/value head
+    int S, N, max_tokens, Hq, Hkv, G, R;  // R: tokens of a row tile
+};
+
+// sum_{j < n} floor((a j + b) / m), a, b >= 0, m > 0: by Euclid's steps on (a, m)
+__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long r = 0;
+    while (n > 0) {
+        r += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const long long t = m;
+        m = a;
+        a = t;
+    }
+    return r;
+}
+
+// A sequence as the schedule sees it; n = 0 when it is empty or refused.
+struct Seq {
+    int n0, n, ctx;
+};
+struct RawSeq {
+    int n0, n1, ctx;
+};
+__device__ __forceinline__ RawSeq load_raw(const Args &a, int s) { return {a.node_off[s], a.node_off[s + 1], a.ctx_len[s]}; }
+__device__ __forceinline__ Seq checked(const Args &a, int s, const RawSeq &r, int *err = nullptr) {
+    Seq q{r.n0, 0, r.ctx};
+    const int n1 = r.n1;
+    int e = 0;
+    if (q.n0 < 0 || n1 < q.n0 || n1 > a.N || (s == 0 && q.n0 != 0) || (s == a.S - 1 && n1 != a.N) ||
+        n1 - q.n0 > a.max_tokens)
+        e = GDN_DEV_BAD_NODE_OFF;
+    else if (q.ctx < 0 || int64_t(q.ctx) + (n1 - q.n0) > (int64_t(a.pl.width) << a.pl.shift))
+        e = GDN_DEV_BAD_LEN;
+    else
+        q.n = n1 - q.n0;
+    if (err) *err = e;
+    return q;
+}
+template <int TK>
+__device__ __forceinline__ int item_tiles(const Seq &q, int j, int R) {
+    return (q.ctx + min((j + 1) * R, q.n) + TK - 1) / TK;
+}
+// tiles of row tiles 0 .. j - 1 (j <= the number of row tiles - 1)
+template <int TK>
+__device__ __forceinline__ long long tiles_before(const Seq &q, int j, int R) {
+    return floor_sum(j, TK, R, (long long)q.ctx + R + TK - 1);
+}
+template <int TK>
+__device__ __forceinline__ long long head_tiles(const Seq &q, int R) {
+    if (q.n == 0) return 0;
+    const int J = (q.n + R - 1) / R;
+    return tiles_before<TK>(q, J - 1, R) + item_tiles<TK>(q, J - 1, R);
+}
+
+struct Start {
+    int s, h, j, off;
+    long long count;  // tiles of this CTA
+};
+
+// A CTA's run through its share, segment by segment (a segment: consecutive tiles
+// of one item).  Every role walks it for itself.
+struct Segment {
+    int s, h, i0, rows, tile0, tile1;  // rows: valid rows of the tile
+    bool starts, ends;
+    int limit;  // positions of the item: ctx + tokens up to the tile's last
+    int safe;   // positions below it are seen by every row
+    Seq q;
+};
+template <int TK>
+struct Walk {
+    const Args &a;
+    int s, h, j, off;
+    long long left;
+    Seq q;
+    RawSeq nx;  // of the next sequence, loaded one ahead and looked at when it is its turn
+    __device__ Walk(const Args &a_, const Start &st) : a(a_), s(st.s), h(st.h), j(st.j), off(st.off), left(st.count) {
+        if (left > 0) {
+            q = checked(a, s, load_raw(a, s));
+            if (s + 1 < a.S) nx = load_raw(a, s + 1);
+        }
+    }
+    __device__ __forceinline__ bool next(Segment &g) {
+        if (left <= 0) return false;
+        const int total = item_tiles<TK>(q, j, a.R);
+        const int take = int(min((long long)(total - off), left));
+        g.s = s;
+        g.h = h;
+        g.i0 = j * a.R;
+        const int toks = min(a.R, q.n - g.i0);
+        g.rows = toks * a.G;
+        g.tile0 = off;
+        g.tile1 = off + take;
+        g.starts = off == 0;
+        g.ends = off + take == total;
+        g.limit = q.ctx + g.i0 + toks;
+        g.safe = a.parents ? q.ctx : q.ctx + g.i0 + 1;
+        g.q = q;
+        left -= take;
+        off += take;
+        if (g.ends) {
+            off = 0;
+            if ((j + 1) * a.R >= q.n) {
+                j = 0;
+                if (++h == a.Hkv) {
+                    h = 0;
+                    while (left > 0 && s + 1 < a.S) {  // the next sequence with tokens
+                        ++s;
+                        q = checked(a, s, nx);
+                        if (s + 1 < a.S) nx = load_raw(a, s + 1);
+                        if (q.n > 0) break;
+                    }
+                }
+            } else {
+                ++j;
+            }
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// D[tmem] (+)= A[tmem] x B[smem], 16-bit operands, fp32 accumulators
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// MN-major operand in the 128-byte swizzle: 64 elements (128 bytes) of MN by 8 of K
+// an atom; `lead` bytes from one atom of MN to the next, 1024 from one of K to the next.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(lead >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int row, int head, int page,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(page), "r"(gdn::smem_addr(bar))
+        : "memory");
+}
+// Warp-collective: thread t writes 32 columns (words) of lane (taddr lane) + t.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(gdn::smem_addr(bar)) : "memory");
+}
+// Warp-collective bounded wait; false (for the whole warp) after a timeout anywhere in the CTA.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    bool ok = gdn::mbar_try_wait(bar, parity);
+    if (!ok && !*abort_flag) ok = gdn::mbar_wait_bounded(bar, parity);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *abort_flag = 1;
+    return ok;
+}
+// Which of the 32 positions from `base` on a row sees: all below `upto` (chain), or
+// all below ctx and the bits of `line` from there (tree).
+__device__ __forceinline__ uint32_t seen32(bool tree, int base, int ctx, int upto, unsigned long long line) {
+    if (!tree) {
+        const int n = upto - base;
+        return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    }
+    const int rel = base - ctx;
+    if (rel >= 0) return rel < 64 ? uint32_t(line >> rel) : 0u;
+    if (rel <= -32) return 0xffffffffu;
+    return uint32_t(line << -rel) | ((1u << -rel) - 1u);
+}
+
+}  // namespace att
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) paged_attention_kernel(const AttnArgs a) {
-    constexpr int E = D / 32;  // elements of a lane
+__global__ void __launch_bounds__(att::kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                           const att::Args a) {
+    using namespace att;
+    using C = Cfg<D>;
+    constexpr int TK = C::TK;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
+    __shared__ uint64_t s_bar[2], p_bar[2], q_bar, pv_bar, go_bar, clean_bar, drain_bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_s;
+    __shared__ Start start_s;
+    __shared__ long long wsum[kThreads / 32];
+    __shared__ int tree_par[4][gdn::kMaxSeqNodes];
+    __shared__ uint32_t nf[2][kNfBufs][4];  // by cleaning warp and segment: positions from `safe` on with values that are not finite
+    volatile int *abort_flag = &abort_s;
+    unsigned char *tiles =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t tb = gdn::smem_addr(tiles);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned full = 0xffffffffu;
+
+    gdn::grid_dep_launch();
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            gdn::mbar_init(full_bar + i, 1);
+            gdn::mbar_init(empty_bar + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            gdn::mbar_init(s_bar + i, 1);
+            gdn::mbar_init(p_bar + i, 4);
+        }
+        gdn::mbar_init(&q_bar, 4);
+        gdn::mbar_init(&pv_bar, 1);
+        gdn::mbar_init(&go_bar, 1);
+        gdn::mbar_init(&clean_bar, 2);
+        gdn::mbar_init(&drain_bar, 1);
+        gdn::fence_mbar_init();
+        abort_s = 0;
+        start_s.count = 0;
+    }
+    if (warp == kMma) {
+        gdn::tmem_alloc(&tmem_slot, 512);
+        gdn::tmem_relinquish();
+    }
+    gdn::grid_dep_wait();  // lengths, q, the pools and the workspace
+
+    // ---- the schedule: tiles of all sequences, cut into equal shares ------------
+    const int per = (a.S + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        if (s >= a.S) break;
+        int err;
+        const Seq q = checked(a, s, load_raw(a, s), &err);
+        if (err && blockIdx.x == 0) gdn::record_status(a.status, err);
+        mine += head_tiles<TK>(q, a.R) * a.Hkv;
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(full, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    gdn::tc_fence_before_sync();
+    __syncthreads();
+    gdn::tc_fence_after_sync();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) before = total;
+        total += wsum[w];
+    }
+    before += inc - mine;
+    {
+        const long long active = min((long long)gridDim.x, total);
+        const int b = blockIdx.x;
+        if (b < active) {
+            const long long t0 = total * b / active, t1 = total * (b + 1) / active;
+            if (mine > 0 && t0 >= before && t0 < before + mine) {  // one thread of the CTA
+                long long x = t0 - before;
+                for (int k = 0; k < per; ++k) {
+                    const int s = tid * per + k;
+                    const Seq q = checked(a, s, load_raw(a, s));
+                    const long long ht = head_tiles<TK>(q, a.R);
+                    if (x >= ht * a.Hkv) {
+                        x -= ht * a.Hkv;
+                        continue;
+                    }
+                    const int h = int(x / ht);
+                    x -= h * ht;
+                    int lo = 0, hi = (q.n + a.R - 1) / a.R;  // the last row tile with tiles_before <= x
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) / 2;
+                        if (tiles_before<TK>(q, mid, a.R) <= x) lo = mid;
+                        else hi = mid;
+                    }
+                    start_s = Start{s, h, lo, int(x - tiles_before<TK>(q, lo, a.R)), t1 - t0};
+                    break;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const Start start = start_s;
+    const uint32_t tmem = tmem_slot;
+    Walk<TK> walk(a, start);
+    Segment g;
+
+    if (warp == kTma) {
+        // ---- keys and values by TMA -------------------------------------------------
+        asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
+        const int bx = min(1 << a.pl.shift, TK);            // rows of a box
+        const int b = lane / C::kChunks, ch = lane % C::kChunks;
+        const uint32_t dst = ch * C::kChunkBytes + uint32_t(b) * bx * 128u;
+        int stage = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        bool ok = true, bad_page = false;
+        // the page of this lane's box of tile t (-1: nothing to load)
+        auto page_of = [&](const Segment &sg, int t) {
+            const int x = t * TK + b * bx;
+            if (b * bx >= TK || x >= sg.limit) return -1;
+            const int p = a.pl.table[int64_t(sg.s) * a.pl.width + (x >> a.pl.shift)];
+            if (p < 0 || p >= a.pl.n_pages) {
+                bad_page = true;
+                return -1;
+            }
+            return p;
+        };
+        auto load = [&](const CUtensorMap *map, int page, int row, int head) {
+            if (!wait_bar(empty_bar + stage, phase ^ 1, abort_flag)) return false;
+            const unsigned m = __ballot_sync(full, page >= 0);
+            if (lane == 0) gdn::mbar_arrive_expect_tx(full_bar + stage, __popc(m) * bx * 128u);
+            __syncwarp();
+            if (page >= 0) tma_load_4d(tb + stage * C::kTile + dst, map, 64 * ch, row, head, page, full_bar + stage);
+            ++issued;
+            if (++stage == C::kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            return true;
+        };
+        while (ok && walk.next(g)) {
+            int page = page_of(g, g.tile0), prev = -1;
+            const int mask = (1 << a.pl.shift) - 1;
+            for (int t = g.tile0; t < g.tile1 && ok; ++t) {
+                const int nextp = t + 1 < g.tile1 ? page_of(g, t + 1) : -1;
+                ok = load(&kmap, page, (t * TK + b * bx) & mask, g.h);
+                if (ok && t > g.tile0) ok = load(&vmap, prev, ((t - 1) * TK + b * bx) & mask, g.h);
+                prev = page;
+                page = nextp;
+            }
+            if (ok) ok = load(&vmap, prev, ((g.tile1 - 1) * TK + b * bx) & mask, g.h);
+        }
+        if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
+        if (!ok) {  // after a timeout copies may be in flight: wait for them (bounded)
+            const int n = int(min(issued, (long long)C::kStages));
+            for (int k = 0; k < n; ++k) {
+                if (stage == 0) {
+                    stage = C::kStages;
+                    phase ^= 1;
+                }
+                --stage;
+                gdn::mbar_wait_bounded(full_bar + stage, phase);
+            }
+        }
+    } else if (warp == kMma) {
+        // ---- the products -------------------------------------------------------------
+        constexpr uint32_t fmt = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+        constexpr uint32_t kIdS = (1u << 4) | (fmt << 7) | (fmt << 10) | (uint32_t(TK >> 3) << 17) | (8u << 24);
+        constexpr uint32_t kIdO = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);
+        int stage = 0;
+        uint32_t phase = 0, seg = 0, masked = 0;
+        long long tile = 0;  // tiles of this CTA so far: buffers and phases of S and P
+        bool ok = true;
+        auto advance = [&] {
+            if (++stage == C::kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        };
+        auto scores = [&](long long i) {  // S_i = Q K_i^T
+            if (!wait_bar(full_bar + stage, phase, abort_flag)) return false;
+            gdn::tc_fence_after_sync();
+            if (elect_one()) {
+                const uint32_t kb = tb + stage * C::kTile, d = tmem + C::kS + uint32_t(i & 1) * TK;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_f16_ta(d, tmem + C::kQ + 8 * k, gdn::desc_sw128(kb + (k >> 2) * C::kChunkBytes) + 2 * (k & 3),
+                               kIdS, k > 0);
+                gdn::mma_commit(empty_bar + stage);
+                gdn::mma_commit(s_bar + (i & 1));
+            }
+            __syncwarp();
+            advance();
+            return true;
+        };
+        while (ok && walk.next(g)) {
+            ok = wait_bar(&q_bar, seg & 1, abort_flag);
+            ++seg;
+            gdn::tc_fence_after_sync();
+            if (ok) ok = scores(tile);
+            for (int t = g.tile0; t < g.tile1 && ok; ++t, ++tile) {
+                if (t + 1 < g.tile1 && !scores(tile + 1)) {
+                    ok = false;
+                    break;
+                }
+                ok = wait_bar(full_bar + stage, phase, abort_flag);
+                const bool clean = (t + 1) * TK > g.safe;  // the cleaning runs beside this tile's softmax
+                if (clean && lane == 0) arrive(&go_bar);
+                ok = ok && wait_bar(p_bar + (tile & 1), uint32_t(tile >> 1) & 1, abort_flag);
+                if (clean) ok = ok && wait_bar(&clean_bar, masked++ & 1, abort_flag);
+                if (!ok) break;
+                gdn::tc_fence_after_sync();
+                if (elect_one()) {
+                    const uint32_t vb = tb + stage * C::kTile, p = tmem + C::kS + uint32_t(tile & 1) * TK;
+#pragma unroll
+                    for (int k = 0; k < TK / 16; ++k)  // O += P V
+                        mma_f16_ta(tmem + C::kO, p + 8 * k, desc_mn_sw128(vb + k * 2048, C::kChunkBytes), kIdO,
+                                   k > 0 || t > g.tile0);
+                    gdn::mma_commit(empty_bar + stage);
+                    gdn::mma_commit(&pv_bar);
+                }
+                __syncwarp();
+                advance();
+            }
+        }
+        if (elect_one()) gdn::mma_commit(&drain_bar);
+        __syncwarp();
+        gdn::mbar_wait_bounded(&drain_bar, 0);
+    } else if (warp >= kClean0) {
+        // ---- values of tiles that not every row sees whole ----------------------------
+        long long loads = 0;  // ring position of the segment's first load
+        uint32_t seg = 0, masked = 0;
+        bool ok = true;
+        constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+        const int ct = tid - kClean0 * 32;
+        while (ok && walk.next(g)) {
+            const int n = g.tile1 - g.tile0;
+            uint32_t bits[4] = {0, 0, 0, 0};
+            for (int t = max(g.tile0, g.safe / TK); t < g.tile1 && ok; ++t) {
+                // V of the segment's tile k is load 2 k + 2, the last one 2 n - 1
+                const int k = t - g.tile0;
+                const long long at = loads + (k + 1 < n ? 2 * k + 2 : 2 * n - 1);
+                const int stage = int(at % C::kStages);
+                ok = wait_bar(&go_bar, masked++ & 1, abort_flag) &&
+                     wait_bar(full_bar + stage, uint32_t(at / C::kStages) & 1, abort_flag);
+                if (!ok) break;
+                const int r0 = max(0, g.safe - t * TK);  // rows (positions) that some rows do not see
+                unsigned char *vt = tiles + size_t(stage) * C::kTile;
+                for (int u = ct; u < (TK - r0) * C::kChunks * 8; u += 64) {
+                    const int r = r0 + u / (C::kChunks * 8), c16 = u % (C::kChunks * 8);
+                    uint4 *w = reinterpret_cast<uint4 *>(vt + (c16 >> 3) * C::kChunkBytes + r * 128 + (c16 & 7) * 16);
+                    const int x = t * TK + r;
+                    if (x >= g.limit) {
+                        *w = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    const uint4 v = *w;
+                    uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if ((e[i] & kExp) == kExp) {
+                            e[i] &= 0xFFFF0000u;
+                            any = true;
+                        }
+                        if (((e[i] >> 16) & kExp) == kExp) {
+                            e[i] &= 0xFFFFu;
+                            any = true;
+                        }
+                    }
+                    if (any) {
+                        *w = make_uint4(e[0], e[1], e[2], e[3]);
+                        const int bit = x - g.safe;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i == bit >> 5) bits[i] |= 1u << (bit & 31);
+                    }
+                }
+                gdn::fence_proxy_async_smem();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    bits[i] = __reduce_or_sync(full, bits[i]);
+                    if (lane == i) nf[warp - kClean0][seg % kNfBufs][i] = bits[i];
+                }
+                __syncwarp();
+                if (lane == 0) arrive(&clean_bar);
+            }
+            loads += 2 * n;
+            ++seg;
+        }
+    } else {
+        // ---- rows ------------------------------------------------------------------------
+        const uint32_t trow = tmem + (uint32_t(warp) << 21);  // this warp's lanes
+        const int row = tid;
+        long long tile = 0;
+        uint32_t seg = 0;
+        bool ok = true;
+        const float c = a.c;
+        int4 *meta = a.meta + 2 * blockIdx.x;
+        bool head_part = false, tail_part = false;
+        int line_s = -1;
+        while (ok && walk.next(g)) {
+            const bool live_warp = warp * 32 < g.rows, live = row < g.rows;
+            const int i = g.i0 + row / a.G, hd = g.h * a.G + row % a.G;
+            // Q rows into tensor memory (the last segment's products are complete)
+            if (live_warp) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
+                                                                   (int64_t(g.q.n0) + i) * a.q_stride + int64_t(hd) * D);
+#pragma unroll
+                for (int cc = 0; cc < C::kChunks; ++cc) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 v = live ? src[8 * cc + k] : make_uint4(0, 0, 0, 0);
+                        w[4 * k] = v.x;
+                        w[4 * k + 1] = v.y;
+                        w[4 * k + 2] = v.z;
+                        w[4 * k + 3] = v.w;
+                    }
+                    tmem_st32(trow + C::kQ + 32 * cc, w);
+                }
+                tmem_wait_st();
+            }
+            gdn::tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive(&q_bar);
+            // the row's ancestors
+            unsigned long long line = 0;
+            if (a.parents && live_warp) {
+                if (line_s != g.s) {
+                    __syncwarp();
+                    for (int x = lane; x < g.q.n; x += 32) tree_par[warp][x] = a.parents[g.q.n0 + x];
+                    __syncwarp();
+                    line_s = g.s;
+                }
+                if (live) {
+                    for (int x = i; x >= 0;) {
+                        line |= 1ull << x;
+                        const int p = tree_par[warp][x];
+                        if (p >= x || p < -1) {
+                            gdn::record_status(a.status, GDN_DEV_BAD_PARENT);
+                            break;
+                        }
+                        x = p;
+                    }
+                }
+            }
+            const int upto = g.q.ctx + i + 1;
+            float m = -INFINITY, l = 0.f;
+            for (int t = g.tile0; t < g.tile1; ++t, ++tile) {
+                ok = wait_bar(s_bar + (tile & 1), uint32_t(tile >> 1) & 1, abort_flag);
+                if (!ok) break;
+                if (live_warp) {
+                    gdn::tc_fence_after_sync();
+                    const uint32_t ts = trow + C::kS + uint32_t(tile & 1) * TK;
+                    float sv[TK / 32][32];
+#pragma unroll
+                    for (int k = 0; k < TK / 32; k += 2) gdn::tmem_ld32x2(ts + 32 * k, ts + 32 * k + 32, sv[k], sv[k + 1]);
+                    if ((t + 1) * TK > g.safe) {
+#pragma unroll
+                        for (int k = 0; k < TK / 32; ++k) {
+                            const uint32_t vis = seen32(a.parents != nullptr, t * TK + 32 * k, g.q.ctx, upto, line);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((vis >> e) & 1)) sv[k][e] = -INFINITY;
+                        }
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < TK / 32; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, sv[k][e]);
+                    mx *= c;
+                    if (t == g.tile0) {
+                        m = mx;
+                    } else {
+                        const bool move = mx > m + 8.f;
+                        if (__any_sync(full, move)) {
+                            // O may be scaled once the product before this one has added to it
+                            ok = wait_bar(&pv_bar, uint32_t(tile - 1) & 1, abort_flag);
+                            if (!ok) break;
+                            gdn::tc_fence_after_sync();
+                            const float f = move ? exp2_approx(m - mx) : 1.f;
+                            if (move) m = mx;
+                            l *= f;
+#pragma unroll 1
+                            for (int cc = 0; cc < D; cc += 32) {
+                                float v[32];
+                                uint32_t w[32];
+                                gdn::tmem_ld32(trow + C::kO + cc, v);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e] * f);
+                                tmem_st32(trow + C::kO + cc, w);
+                            }
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet
+                    const uint64_t c2 = gdn::f2pack(c, c), mu2 = gdn::f2pack(-mu, -mu);
+                    uint64_t sum = gdn::f2pack(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < TK / 64; ++k) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float *x = &sv[2 * k + (e >> 4)][2 * (e & 15)];
+                            const float2 y = gdn::f2unpack(gdn::fma2(gdn::f2pack(x[0], x[1]), c2, mu2));
+                            const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+                            sum = gdn::add2(sum, gdn::f2pack(p0, p1));
+                            w[e] = gdn::Half2<T>::pack(p0, p1);
+                        }
+                        tmem_st32(ts + 32 * k, w);
+                    }
+                    const float2 s2 = gdn::f2unpack(sum);
+                    l += s2.x + s2.y;
+                    tmem_wait_st();
+                    gdn::tc_fence_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0) arrive(p_bar + (tile & 1));
+            }
+            if (!ok) break;
+            // ---- the segment's rows out ---------------------------------------------------
+            // the last product; the one before it first, so that the phase is not mistaken for that of two before
+            if (tile > 1) ok = wait_bar(&pv_bar, uint32_t(tile - 2) & 1, abort_flag);
+            ok = ok && wait_bar(&pv_bar, uint32_t(tile - 1) & 1, abort_flag);
+            if (!ok) break;
+            gdn::tc_fence_after_sync();
+            const bool whole = g.starts && g.ends;
+            const int slot = g.starts ? 1 : 0;
+            float *part = a.parts + (size_t(blockIdx.x) * 2 + slot) * C::kPartFloats;
+            if (!whole) {
+                if (tid == 0) meta[slot] = make_int4(g.rows, g.ends, g.q.n0 + g.i0, g.h);
+                if (slot) tail_part = true;
+                else head_part = true;
+                if (live) {
+                    part[row] = m;
+                    part[kRows + row] = l;
+                }
+            }
+            uint32_t bits[4] = {0, 0, 0, 0};
+            bool odd = false;
+            if (g.tile1 * TK > g.safe) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    bits[k] = *reinterpret_cast<volatile uint32_t *>(&nf[0][seg % kNfBufs][k]) |
+                              *reinterpret_cast<volatile uint32_t *>(&nf[1][seg % kNfBufs][k]);
+                    odd |= bits[k] != 0;
+                }
+            }
+            const float inv = 1.f / l;
+            if (live_warp) {
+                T *orow = static_cast<T *>(a.o) + ((int64_t(g.q.n0) + i) * a.Hq + hd) * D;
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 32) {
+                    float v[32];
+                    gdn::tmem_ld32(trow + C::kO + cc, v);
+                    if (odd && live) {  // values that are not finite, for the rows that see them
+                        for (int k = 0; k < 4; ++k)
+                            for (uint32_t w = bits[k]; w; w &= w - 1) {
+                                const int x = g.safe + 32 * k + __ffs(w) - 1;
+                                if (!(seen32(a.parents != nullptr, x, g.q.ctx, upto, line) & 1)) continue;
+                                const int64_t at = gdn::position_offset(a.pl, g.s, x);
+                                if (at < 0) continue;
+                                const T *vr = static_cast<const T *>(a.v_pool) + at + int64_t(g.h) * a.pl.head_stride + cc;
+                                for (int e = 0; e < 32; ++e) {
+                                    const float y = float(vr[e]);
+                                    if (!(fabsf(y) < INFINITY)) {
+#pragma unroll
+                                        for (int z = 0; z < 32; ++z)
+                                            if (z == e) v[z] += y;
+                                    }
+                                }
+                            }
+                    }
+                    if (!live) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            float y[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) y[z] = v[e + z] * inv;
+                            *reinterpret_cast<uint4 *>(orow + cc + e) = gdn::pack8<T>(y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)  // column group, then row: neighbours side by side
+                            *reinterpret_cast<float4 *>(part + 2 * kRows + (size_t((cc + e) / 4) * kRows + row) * 4) =
+                                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                }
+            }
+            ++seg;
+        }
+        if (tid == 0) {
+            if (!head_part) meta[0] = make_int4(0, 0, 0, 0);
+            if (!tail_part) meta[1] = make_int4(0, 0, 0, 0);
+        }
+    }
+    gdn::tc_fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && abort_s) gdn::record_status(a.status, GDN_DEV_TIMEOUT);
+    if (warp == kMma) gdn::tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of items that more than one CTA worked on: block (b, y) takes
+// the item that begins in CTA b and goes on in b + 1, ..., in that order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(const att::Args a, int ctas) {
+    using C = att::Cfg<D>;
     gdn::grid_dep_launch();
     gdn::grid_dep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t wid = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (blockIdx.x == 0) {
-        const int err = gdn::check_node_off(a.node_off, a.S, a.N, a.max_tokens, threadIdx.x, 128);
-        if (err) gdn::record_status(a.status, err);
-    }
-    const int n = int(wid / a.Hq), h = int(wid % a.Hq), hk = h / (a.Hq / a.Hkv);
-    if (n >= a.N) return;
-    const int s = gdn::find_sequence(a.node_off, a.S, n);
-    const int n0 = a.node_off[s], i = n - n0, ctx = a.ctx_len[s];
-    int err = 0;
-    if (i < 0 || i >= a.max_tokens || n >= a.node_off[s + 1]) err = GDN_DEV_BAD_NODE_OFF;
-    else if (ctx < 0 || int64_t(ctx) + i >= (int64_t(a.pl.width) << a.pl.shift)) err = GDN_DEV_BAD_LEN;
-    unsigned long long line = 0;
-    if (!err && a.parents) {
-        for (int x = i; x >= 0;) {
-            line |= 1ull << x;
-            const int p = a.parents[n0 + x];
-            if (p >= x || p < -1) { err = GDN_DEV_BAD_PARENT; break; }
-            x = p;
+    const int b = blockIdx.x;
+    const int4 me = a.meta[2 * b + 1];
+    if (me.x <= 0 || me.x > att::kRows) return;
+    int last = b + 1;  // the CTA with the item's end
+    while (last < ctas - 1 && a.meta[2 * last].x > 0 && !a.meta[2 * last].y) ++last;
+    if (last >= ctas) return;
+    const int rows = me.x;
+    for (int u = blockIdx.y * 256 + threadIdx.x; u < rows * (D / 4); u += gridDim.y * 256) {
+        const int row = u % rows, c4 = u / rows;
+        float M = -INFINITY;
+        for (int k = b; k <= last; ++k)
+            M = fmaxf(M, a.parts[(size_t(k) * 2 + (k == b)) * C::kPartFloats + row]);
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = b; k <= last; ++k) {
+            const float *part = a.parts + (size_t(k) * 2 + (k == b)) * C::kPartFloats;
+            const float m = part[row], pl = part[att::kRows + row];
+            const float4 v = *reinterpret_cast<const float4 *>(part + 2 * att::kRows + (size_t(c4) * att::kRows + row) * 4);
+            if (m == -INFINITY) continue;  // nothing seen in this part
+            const float w = att::exp2_approx(m - M);
+            l = fmaf(w, pl, l);
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
         }
+        const float inv = 1.f / l;
+        T *out = static_cast<T *>(a.o) + ((int64_t(me.z) + row / a.G) * a.Hq + me.w * a.G + row % a.G) * D + 4 * c4;
+        *reinterpret_cast<uint2 *>(out) =
+            make_uint2(gdn::Half2<T>::pack(o.x * inv, o.y * inv), gdn::Half2<T>::pack(o.z * inv, o.w * inv));
     }
-    if (err) {
-        if (lane == 0) gdn::record_status(a.status, err);
-        return;
-    }
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-    const T *qr = static_cast<const T *>(a.q) + n * a.q_stride + int64_t(h) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = float(qr[e]);
-        o[e] = 0.f;
-    }
-    for (int x = 0; x <= ctx + i; ++x) {
-        if (x >= ctx && a.parents && !((line >> (x - ctx)) & 1)) continue;
-        const int64_t at = gdn::position_offset(a.pl, s, x);
-        if (at < 0) {
-            if (lane == 0) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
-            return;
-        }
-        const T *kr = static_cast<const T *>(a.k_pool) + at + int64_t(hk) * a.pl.head_stride + lane * E;
-        const T *vr = static_cast<const T *>(a.v_pool) + at + int64_t(hk) * a.pl.head_stride + lane * E;
-        float d = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) d = fmaf(q[e], float(kr[e]), d);
-        d = gdn::warp_sum(d) * a.scale;
-        const float mn = fmaxf(m, d);
-        const float al = m == -INFINITY ? 0.f : expf(m - mn), p = expf(d - mn);
-        l = l * al + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(p, float(vr[e]), al == 0.f ? 0.f : o[e] * al);
-        m = mn;
-    }
-    T *orow = static_cast<T *>(a.o) + (int64_t(n) * a.Hq + h) * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) orow[e] = T(o[e] / l);
-    (void)full;
+}
+
+size_t workspace_bytes(const gdn_attn_dims *dims, int ctas) {
+    return size_t(ctas) * (2 * att::kRows * size_t(dims->d_head + 2) * 4 + 2 * sizeof(int4));
+}
+
+template <typename T, int D>
+int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *workspace, int ctas, cudaStream_t st) {
+    using C = att::Cfg<D>;
+    CUtensorMap kmap, vmap;
+    const uint32_t rows = uint32_t(dims->page_size < C::TK ? dims->page_size : C::TK);
+    int rc;
+    if ((rc = gdn::encode_kv_pages(&kmap, k_pool, dims, rows)) || (rc = gdn::encode_kv_pages(&vmap, a.v_pool, dims, rows)))
+        return rc;
+    a.meta = static_cast<int4 *>(workspace);
+    a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);
+    auto k = paged_attention_kernel<T, D>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem)) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    if (gdn::launch_pdl(k, dim3(unsigned(ctas)), dim3(att::kThreads), C::kSmem, st, kmap, vmap, a) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    return gdn::launch_pdl(attention_join_kernel<T, D>, dim3(unsigned(ctas), 8), dim3(256), 0, st, a, ctas) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_LAUNCH;
 }
 
 template <typename T>
-cudaError_t launch(int d, dim3 grid, cudaStream_t st, const AttnArgs &a) {
-    switch (d) {
-        case 64: return gdn::launch_pdl(paged_attention_kernel<T, 64>, grid, dim3(128), 0, st, a);
-        case 128: return gdn::launch_pdl(paged_attention_kernel<T, 128>, grid, dim3(128), 0, st, a);
-        default: return gdn::launch_pdl(paged_attention_kernel<T, 256>, grid, dim3(128), 0, st, a);
+int launch_d(const gdn_attn_dims *dims, const void *k_pool, const att::Args &a, void *workspace, int ctas,
+             cudaStream_t st) {
+    switch (dims->d_head) {
+        case 64: return launch<T, 64>(dims, k_pool, a, workspace, ctas, st);
+        case 128: return launch<T, 128>(dims, k_pool, a, workspace, ctas, st);
+        default: return launch<T, 256>(dims, k_pool, a, workspace, ctas, st);
     }
 }
 
 }  // namespace
 
 extern "C" size_t gdn_attention_workspace_bytes(const gdn_attn_dims *dims) {
-    return gdn::check_attn_dims(dims) == GDN_OK ? 16 : 0;
+    if (gdn::check_attn_dims(dims) != GDN_OK) return 0;
+    const int ctas = gdn::sm_count_current();
+    return workspace_bytes(dims, ctas > 0 ? ctas : 1);
 }
 
 extern "C" int gdn_paged_attention(const gdn_attn_dims *dims, const void *q, int64_t q_stride, const void *k_pool,
                                    const void *v_pool, const int32_t *page_table, const int32_t *ctx_len,
                                    const int32_t *node_off, const int32_t *parents, float scale, void *o, void *workspace,
-                                   int64_t workspace_bytes, int32_t *status, void *stream) {
+                                   int64_t workspace_size, int32_t *status, void *stream) {
     int rc = gdn::check_attn_dims(dims);
     if (rc) return rc;
     if (!status) return GDN_ERR_NULL;
@@ -111,7 +883,7 @@ extern "C" int gdn_paged_attention(const gdn_attn_dims *dims, const void *q, int
     if (S == 0 || N == 0) return GDN_OK;
     if (!q || !k_pool || !v_pool || !page_table || !ctx_len || !node_off || !o || !workspace) return GDN_ERR_NULL;
     const size_t need = gdn_attention_workspace_bytes(dims);
-    if (workspace_bytes < 0 || size_t(workspace_bytes) < need) return GDN_ERR_ARG;
+    if (workspace_size < 0 || size_t(workspace_size) < need) return GDN_ERR_ARG;
     if (q_stride < Hq * D || q_stride % 8) return GDN_ERR_STRIDE;
     if (!gdn::aligned16(q) || !gdn::aligned16(k_pool) || !gdn::aligned16(v_pool) || !gdn::aligned16(o) ||
         !gdn::aligned16(workspace))
@@ -127,11 +899,13 @@ extern "C" int gdn_paged_attention(const gdn_attn_dims *dims, const void *q, int
                              {parents, size_t(N * 4)},
                              {status, 4}};
     if ((rc = gdn::check_alias(outs, 2, ins, 8))) return rc;
-    AttnArgs a{q, q_stride, k_pool, v_pool, gdn::paged_layout(dims, page_table), ctx_len, node_off, parents, scale, o,
-               status, int(S), int(N), dims->max_seq_tokens, int(Hq), dims->h_kv};
-    const dim3 grid(unsigned((N * Hq + 3) / 4));
+    const int ctas = gdn::sm_count_current();
+    if (ctas < 1) return GDN_ERR_LAUNCH;
+    const int G = int(Hq / dims->h_kv);
+    att::Args a{q, q_stride, v_pool, gdn::paged_layout(dims, page_table), ctx_len, node_off, parents,
+                scale * 1.4426950408889634f, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens, int(Hq),
+                dims->h_kv, G, att::kRows / G};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dims->dtype == GDN_BF16 ? launch<__nv_bfloat16>(int(D), grid, st, a)
-                                                  : launch<__half>(int(D), grid, st, a);
-    return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    return dims->dtype == GDN_BF16 ? launch_d<__nv_bfloat16>(dims, k_pool, a, workspace, ctas, st)
+                                   : launch_d<__half>(dims, k_pool, a, workspace, ctas, st);
 }
