@@ -26,21 +26,22 @@
 //
 // Mapping (GB300).  Tensor memory holds O (D columns, fp32), Q (D / 2 columns, the
 // A operand of Q K^T: nothing of it is read again from shared memory, which leaves
-// all of that to keys and values) and two score tiles (TK columns each), P taking
+// all of that to keys and values) and two score tiles (64 columns each), P taking
 // its scores' place as the A operand of P V.  Shared memory is a ring of 192 KB of
 // key and value tiles, filled by TMA page by page in the 128-byte swizzle: keys as
 // they lie are the K-major B operand, values as they lie the MN-major one.
-//   warps 0-3  row r = 32 w + lane = tensor-memory lane: Q in, scores -> P, moves
-//              of m, results out
-//   warp 4     TMA: K_0 K_1 V_0 K_2 V_1 ...; a lane per (page, 64 columns)
-//   warp 5     tcgen05.mma: S_{i+1} = Q K_{i+1}^T is issued before P_i is awaited,
-//              so the tensor cores run while the softmax does
-//   warps 6-7  values of tiles in which some rows do not see some positions: what
-//              no row sees (the rest of a page) is set to 0, and elements that are
-//              not finite are set to 0 and remembered, since 0 * NaN in P V would
-//              reach rows that do not see them; rows that do get them back at the
-//              end
-// Every mbarrier completes once per use, so a counter gives every wait's phase.
+//   rows    four warps, row r = 32 w + lane = tensor-memory lane: Q in, scores -> P,
+//           moves of m, results out.  For D <= 128 the softmax is longer than the
+//           products: two warpgroups take alternate tiles, each with an O, m and l of
+//           its own, joined at the end of a segment.
+//   TMA     K_0 K_1 V_0 K_2 V_1 ...; a lane per (page, 64 columns)
+//   mma     two warps: S_{i+1} = Q K_{i+1}^T runs while P_i is formed
+//   clean   values of tiles in which some rows do not see some positions: what no row
+//           sees (the rest of a page) is set to 0, and elements that are not finite
+//           are set to 0 and remembered, since 0 * NaN in P V would reach rows that
+//           do not see them; rows that do get them back at the end
+// Every mbarrier completes once per use, so a counter gives every wait's phase; a
+// wait is only ever for the next completion that the waiter has not seen.
 #include <type_traits>
 
 #include "gdn_attn.h"
@@ -49,22 +50,31 @@
 namespace {
 namespace att {
 
-constexpr int kThreads = 256, kTma = 4, kMma = 5, kClean0 = 6;
 constexpr int kRows = 128;
-constexpr int kNfBufs = 8;  // the ring holds the values of 6 segments at most, and one may still be going out
+constexpr int TK = 64;       // positions of a tile
+constexpr int kNfBufs = 16;  // the ring holds the values of 12 segments at most, and one may still be going out
 
 template <int D_>
 struct Cfg {
     static constexpr int D = D_;
-    static constexpr int TK = D == 256 ? 64 : 128;        // positions of a tile
+    static constexpr int kStreams = D == 256 ? 1 : 2;     // softmax warpgroups, each with an O of its own
+    static constexpr int kRowWarps = 4 * kStreams;
+    static constexpr int kTma = kRowWarps, kMmaS = kTma + 1, kMmaO = kTma + 2, kClean0 = kTma + 3;
+    // one cleaning warp beside two warpgroups: 12 warps, three to a scheduler, leave 168 registers a thread
+    static constexpr int kCleanWarps = kStreams == 2 ? 1 : 2;
+    static constexpr int kThreads = 32 * (kRowWarps + 3 + kCleanWarps);
     static constexpr int kChunks = D / 64;                // 128-byte columns of a row
     static constexpr uint32_t kChunkBytes = TK * 128;
-    static constexpr uint32_t kTile = TK * D * 2;         // 32 KB, 32 KB, 16 KB
+    static constexpr uint32_t kTile = TK * D * 2;         // 32, 16, 8 KB
     static constexpr int kStages = 196608 / kTile;
     static constexpr size_t kSmem = 1024 + 196608;
     // tensor-memory columns
-    static constexpr uint32_t kO = 0, kQ = D, kS = D + D / 2;
-    static_assert(D + D / 2 + 2 * TK <= 512, "tensor memory");
+    static constexpr uint32_t kO = 0, kQ = kStreams * D, kS = kQ + D / 2;
+    static_assert(kStreams * D + D / 2 + 2 * TK <= 512, "tensor memory");
+    static_assert(kStages / 2 + 2 <= kNfBufs, "flags of the segments in the ring");
+    // place in the ring of a segment's K and V tile k of n: K_0 K_1 V_0 K_2 V_1 ... V_{n-1}
+    static __device__ __forceinline__ int k_at(int k) { return k == 0 ? 0 : 2 * k - 1; }
+    static __device__ __forceinline__ int v_at(int k, int n) { return k + 1 < n ? 2 * k + 2 : 2 * n - 1; }
     // workspace of a CTA: two parts (0: an item that began before, 1: one that goes on) of m, l and O
     static constexpr size_t kPartFloats = size_t(kRows) * (D + 2);
 };
@@ -123,20 +133,17 @@ __device__ __forceinline__ Seq checked(const Args &a, int s, const RawSeq &r, in
     if (err) *err = e;
     return q;
 }
-template <int TK>
 __device__ __forceinline__ int item_tiles(const Seq &q, int j, int R) {
     return (q.ctx + min((j + 1) * R, q.n) + TK - 1) / TK;
 }
 // tiles of row tiles 0 .. j - 1 (j <= the number of row tiles - 1)
-template <int TK>
 __device__ __forceinline__ long long tiles_before(const Seq &q, int j, int R) {
     return floor_sum(j, TK, R, (long long)q.ctx + R + TK - 1);
 }
-template <int TK>
 __device__ __forceinline__ long long head_tiles(const Seq &q, int R) {
     if (q.n == 0) return 0;
     const int J = (q.n + R - 1) / R;
-    return tiles_before<TK>(q, J - 1, R) + item_tiles<TK>(q, J - 1, R);
+    return tiles_before(q, J - 1, R) + item_tiles(q, J - 1, R);
 }
 
 struct Start {
@@ -153,7 +160,6 @@ struct Segment {
     int safe;   // positions below it are seen by every row
     Seq q;
 };
-template <int TK>
 struct Walk {
     const Args &a;
     int s, h, j, off;
@@ -168,7 +174,7 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(Segment &g) {
         if (left <= 0) return false;
-        const int total = item_tiles<TK>(q, j, a.R);
+        const int total = item_tiles(q, j, a.R);
         const int take = int(min((long long)(total - off), left));
         g.s = s;
         g.h = h;
@@ -278,21 +284,22 @@ __device__ __forceinline__ uint32_t seen32(bool tree, int base, int ctx, int upt
 }  // namespace att
 
 template <typename T, int D>
-__global__ void __launch_bounds__(att::kThreads, 1)
+__global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const att::Args a) {
     using namespace att;
     using C = Cfg<D>;
-    constexpr int TK = C::TK;
+    constexpr int kThreads = C::kThreads, kTma = C::kTma, kClean0 = C::kClean0;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
-    __shared__ uint64_t s_bar[2], p_bar[2], q_bar, pv_bar, go_bar, clean_bar, drain_bar;
+    __shared__ uint64_t s_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, go_bar, clean_bar, drain_bar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     __shared__ Start start_s;
     __shared__ long long wsum[kThreads / 32];
-    __shared__ int tree_par[4][gdn::kMaxSeqNodes];
-    __shared__ uint32_t nf[2][kNfBufs][4];  // by cleaning warp and segment: positions from `safe` on with values that are not finite
+    __shared__ int tree_par[C::kRowWarps][gdn::kMaxSeqNodes];
+    __shared__ float2 ml[2][C::kStreams][kRows];  // by segment: m and l of each stream's rows
+    __shared__ uint32_t nf[C::kCleanWarps][kNfBufs][4];  // by cleaning warp and segment: positions from `safe` on with values that are not finite
     volatile int *abort_flag = &abort_s;
     unsigned char *tiles =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -309,17 +316,18 @@ __global__ void __launch_bounds__(att::kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             gdn::mbar_init(s_bar + i, 1);
             gdn::mbar_init(p_bar + i, 4);
+            gdn::mbar_init(pv_bar + i, 1);
+            gdn::mbar_init(drain_bar + i, 1);
         }
-        gdn::mbar_init(&q_bar, 4);
-        gdn::mbar_init(&pv_bar, 1);
+        gdn::mbar_init(&q_bar, C::kRowWarps);
+        gdn::mbar_init(&ml_bar, C::kRowWarps);
         gdn::mbar_init(&go_bar, 1);
-        gdn::mbar_init(&clean_bar, 2);
-        gdn::mbar_init(&drain_bar, 1);
+        gdn::mbar_init(&clean_bar, C::kCleanWarps);
         gdn::fence_mbar_init();
         abort_s = 0;
         start_s.count = 0;
     }
-    if (warp == kMma) {
+    if (warp == C::kMmaS) {
         gdn::tmem_alloc(&tmem_slot, 512);
         gdn::tmem_relinquish();
     }
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(att::kThreads, 1)
         int err;
         const Seq q = checked(a, s, load_raw(a, s), &err);
         if (err && blockIdx.x == 0) gdn::record_status(a.status, err);
-        mine += head_tiles<TK>(q, a.R) * a.Hkv;
+        mine += head_tiles(q, a.R) * a.Hkv;
     }
     long long inc = mine;
 #pragma unroll
@@ -363,7 +371,7 @@ __global__ void __launch_bounds__(att::kThreads, 1)
                 for (int k = 0; k < per; ++k) {
                     const int s = tid * per + k;
                     const Seq q = checked(a, s, load_raw(a, s));
-                    const long long ht = head_tiles<TK>(q, a.R);
+                    const long long ht = head_tiles(q, a.R);
                     if (x >= ht * a.Hkv) {
                         x -= ht * a.Hkv;
                         continue;
@@ -373,10 +381,10 @@ __global__ void __launch_bounds__(att::kThreads, 1)
                     int lo = 0, hi = (q.n + a.R - 1) / a.R;  // the last row tile with tiles_before <= x
                     while (hi - lo > 1) {
                         const int mid = (lo + hi) / 2;
-                        if (tiles_before<TK>(q, mid, a.R) <= x) lo = mid;
+                        if (tiles_before(q, mid, a.R) <= x) lo = mid;
                         else hi = mid;
                     }
-                    start_s = Start{s, h, lo, int(x - tiles_before<TK>(q, lo, a.R)), t1 - t0};
+                    start_s = Start{s, h, lo, int(x - tiles_before(q, lo, a.R)), t1 - t0};
                     break;
                 }
             }
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(att::kThreads, 1)
     __syncthreads();
     const Start start = start_s;
     const uint32_t tmem = tmem_slot;
-    Walk<TK> walk(a, start);
+    Walk walk(a, start);
     Segment g;
 
     if (warp == kTma) {
@@ -446,70 +454,70 @@ __global__ void __launch_bounds__(att::kThreads, 1)
                 gdn::mbar_wait_bounded(full_bar + stage, phase);
             }
         }
-    } else if (warp == kMma) {
-        // ---- the products -------------------------------------------------------------
-        constexpr uint32_t fmt = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    } else if (warp == C::kMmaS || warp == C::kMmaO) {
+        // ---- the products: one warp issues S = Q K^T, one O += P V, so that neither's
+        //      waits keep the tensor cores from the other's work -------------------------
+        constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
         constexpr uint32_t kIdS = (1u << 4) | (fmt << 7) | (fmt << 10) | (uint32_t(TK >> 3) << 17) | (8u << 24);
         constexpr uint32_t kIdO = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);
-        int stage = 0;
-        uint32_t phase = 0, seg = 0, masked = 0;
-        long long tile = 0;  // tiles of this CTA so far: buffers and phases of S and P
+        const bool is_s = warp == C::kMmaS;
+        uint32_t seg = 0, masked = 0;
+        long long loads = 0, tile = 0;  // of the segments before: ring places, tiles (buffers and phases of S, P)
         bool ok = true;
-        auto advance = [&] {
-            if (++stage == C::kStages) {
-                stage = 0;
-                phase ^= 1;
-            }
-        };
-        auto scores = [&](long long i) {  // S_i = Q K_i^T
-            if (!wait_bar(full_bar + stage, phase, abort_flag)) return false;
-            gdn::tc_fence_after_sync();
-            if (elect_one()) {
-                const uint32_t kb = tb + stage * C::kTile, d = tmem + C::kS + uint32_t(i & 1) * TK;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_f16_ta(d, tmem + C::kQ + 8 * k, gdn::desc_sw128(kb + (k >> 2) * C::kChunkBytes) + 2 * (k & 3),
-                               kIdS, k > 0);
-                gdn::mma_commit(empty_bar + stage);
-                gdn::mma_commit(s_bar + (i & 1));
-            }
-            __syncwarp();
-            advance();
-            return true;
-        };
         while (ok && walk.next(g)) {
-            ok = wait_bar(&q_bar, seg & 1, abort_flag);
-            ++seg;
-            gdn::tc_fence_after_sync();
-            if (ok) ok = scores(tile);
-            for (int t = g.tile0; t < g.tile1 && ok; ++t, ++tile) {
-                if (t + 1 < g.tile1 && !scores(tile + 1)) {
-                    ok = false;
-                    break;
-                }
-                ok = wait_bar(full_bar + stage, phase, abort_flag);
-                const bool clean = (t + 1) * TK > g.safe;  // the cleaning runs beside this tile's softmax
-                if (clean && lane == 0) arrive(&go_bar);
-                ok = ok && wait_bar(p_bar + (tile & 1), uint32_t(tile >> 1) & 1, abort_flag);
-                if (clean) ok = ok && wait_bar(&clean_bar, masked++ & 1, abort_flag);
-                if (!ok) break;
-                gdn::tc_fence_after_sync();
-                if (elect_one()) {
-                    const uint32_t vb = tb + stage * C::kTile, p = tmem + C::kS + uint32_t(tile & 1) * TK;
+            const int n = g.tile1 - g.tile0;
+            if (is_s) {
+                ok = wait_bar(&q_bar, seg & 1, abort_flag);
+                for (int k = 0; k < n && ok; ++k) {
+                    const long long at = loads + C::k_at(k), i = tile + k;
+                    const int stage = int(at % C::kStages);
+                    ok = wait_bar(full_bar + stage, uint32_t(at / C::kStages) & 1, abort_flag);
+                    // the buffer held P of two tiles before
+                    if (i >= 2) ok = ok && wait_bar(pv_bar + (i & 1), uint32_t((i >> 1) - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    gdn::tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t kb = tb + stage * C::kTile, d = tmem + C::kS + uint32_t(i & 1) * TK;
 #pragma unroll
-                    for (int k = 0; k < TK / 16; ++k)  // O += P V
-                        mma_f16_ta(tmem + C::kO, p + 8 * k, desc_mn_sw128(vb + k * 2048, C::kChunkBytes), kIdO,
-                                   k > 0 || t > g.tile0);
-                    gdn::mma_commit(empty_bar + stage);
-                    gdn::mma_commit(&pv_bar);
+                        for (int z = 0; z < D / 16; ++z)
+                            mma_f16_ta(d, tmem + C::kQ + 8 * z,
+                                       gdn::desc_sw128(kb + (z >> 2) * C::kChunkBytes) + 2 * (z & 3), kIdS, z > 0);
+                        gdn::mma_commit(s_bar + (i & 1));
+                        gdn::mma_commit(empty_bar + stage);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                advance();
+            } else {
+                for (int k = 0; k < n && ok; ++k) {
+                    const long long at = loads + C::v_at(k, n), i = tile + k;
+                    const int stage = int(at % C::kStages);
+                    ok = wait_bar(full_bar + stage, uint32_t(at / C::kStages) & 1, abort_flag);
+                    const bool clean = (g.tile0 + k + 1) * TK > g.safe;  // the cleaning runs beside this tile's softmax
+                    if (clean && lane == 0) arrive(&go_bar);
+                    ok = ok && wait_bar(p_bar + (i & 1), uint32_t(i >> 1) & 1, abort_flag);
+                    if (clean) ok = ok && wait_bar(&clean_bar, masked++ & 1, abort_flag);
+                    if (!ok) break;
+                    gdn::tc_fence_after_sync();
+                    if (elect_one()) {
+                        const uint32_t vb = tb + stage * C::kTile, p = tmem + C::kS + uint32_t(i & 1) * TK;
+                        const uint32_t o = tmem + C::kO + (C::kStreams == 2 ? uint32_t(i & 1) * D : 0u);
+#pragma unroll
+                        for (int z = 0; z < TK / 16; ++z)
+                            mma_f16_ta(o, p + 8 * z, desc_mn_sw128(vb + z * 2048, C::kChunkBytes), kIdO,
+                                       z > 0 || k >= C::kStreams);
+                        gdn::mma_commit(pv_bar + (i & 1));
+                        gdn::mma_commit(empty_bar + stage);
+                    }
+                    __syncwarp();
+                }
             }
+            loads += 2 * n;
+            tile += n;
+            ++seg;
         }
-        if (elect_one()) gdn::mma_commit(&drain_bar);
+        if (elect_one()) gdn::mma_commit(drain_bar + (is_s ? 0 : 1));
         __syncwarp();
-        gdn::mbar_wait_bounded(&drain_bar, 0);
+        gdn::mbar_wait_bounded(drain_bar + (is_s ? 0 : 1), 0);
     } else if (warp >= kClean0) {
         // ---- values of tiles that not every row sees whole ----------------------------
         long long loads = 0;  // ring position of the segment's first load
@@ -521,16 +529,14 @@ __global__ void __launch_bounds__(att::kThreads, 1)
             const int n = g.tile1 - g.tile0;
             uint32_t bits[4] = {0, 0, 0, 0};
             for (int t = max(g.tile0, g.safe / TK); t < g.tile1 && ok; ++t) {
-                // V of the segment's tile k is load 2 k + 2, the last one 2 n - 1
-                const int k = t - g.tile0;
-                const long long at = loads + (k + 1 < n ? 2 * k + 2 : 2 * n - 1);
+                const long long at = loads + C::v_at(t - g.tile0, n);
                 const int stage = int(at % C::kStages);
                 ok = wait_bar(&go_bar, masked++ & 1, abort_flag) &&
                      wait_bar(full_bar + stage, uint32_t(at / C::kStages) & 1, abort_flag);
                 if (!ok) break;
                 const int r0 = max(0, g.safe - t * TK);  // rows (positions) that some rows do not see
                 unsigned char *vt = tiles + size_t(stage) * C::kTile;
-                for (int u = ct; u < (TK - r0) * C::kChunks * 8; u += 64) {
+                for (int u = ct; u < (TK - r0) * C::kChunks * 8; u += 32 * C::kCleanWarps) {
                     const int r = r0 + u / (C::kChunks * 8), c16 = u % (C::kChunks * 8);
                     uint4 *w = reinterpret_cast<uint4 *>(vt + (c16 >> 3) * C::kChunkBytes + r * 128 + (c16 & 7) * 16);
                     const int x = t * TK + r;
@@ -575,9 +581,12 @@ __global__ void __launch_bounds__(att::kThreads, 1)
         }
     } else {
         // ---- rows ------------------------------------------------------------------------
-        const uint32_t trow = tmem + (uint32_t(warp) << 21);  // this warp's lanes
-        const int row = tid;
-        long long tile = 0;
+        const int w = warp & 3, stream = warp >> 2;        // lanes 32 w .. of tensor memory; the warpgroup
+        const uint32_t trow = tmem + (uint32_t(w) << 21);  // this warp's lanes
+        const int row = 32 * w + lane;
+        constexpr int kCols = D / C::kStreams;             // columns of Q and of the results that a warpgroup moves
+        const int col0 = stream * kCols;
+        long long tile = 0;  // tiles of the segments before
         uint32_t seg = 0;
         bool ok = true;
         const float c = a.c;
@@ -585,7 +594,8 @@ __global__ void __launch_bounds__(att::kThreads, 1)
         bool head_part = false, tail_part = false;
         int line_s = -1;
         while (ok && walk.next(g)) {
-            const bool live_warp = warp * 32 < g.rows, live = row < g.rows;
+            const int n = g.tile1 - g.tile0;
+            const bool live_warp = w * 32 < g.rows, live = row < g.rows;
             const int i = g.i0 + row / a.G, hd = g.h * a.G + row % a.G;
             // Q rows into tensor memory (the last segment's products are complete)
             if (live_warp) {
@@ -593,16 +603,17 @@ __global__ void __launch_bounds__(att::kThreads, 1)
                                                                    (int64_t(g.q.n0) + i) * a.q_stride + int64_t(hd) * D);
 #pragma unroll
                 for (int cc = 0; cc < C::kChunks; ++cc) {
-                    uint32_t w[32];
+                    if (C::kStreams == 2 && (cc & 1) != stream) continue;
+                    uint32_t q[32];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint4 v = live ? src[8 * cc + k] : make_uint4(0, 0, 0, 0);
-                        w[4 * k] = v.x;
-                        w[4 * k + 1] = v.y;
-                        w[4 * k + 2] = v.z;
-                        w[4 * k + 3] = v.w;
+                        q[4 * k] = v.x;
+                        q[4 * k + 1] = v.y;
+                        q[4 * k + 2] = v.z;
+                        q[4 * k + 3] = v.w;
                     }
-                    tmem_st32(trow + C::kQ + 32 * cc, w);
+                    tmem_st32(trow + C::kQ + 32 * cc, q);
                 }
                 tmem_wait_st();
             }
@@ -632,38 +643,46 @@ __global__ void __launch_bounds__(att::kThreads, 1)
             }
             const int upto = g.q.ctx + i + 1;
             float m = -INFINITY, l = 0.f;
-            for (int t = g.tile0; t < g.tile1; ++t, ++tile) {
-                ok = wait_bar(s_bar + (tile & 1), uint32_t(tile >> 1) & 1, abort_flag);
+            int done = 0;  // tiles of this warpgroup in this segment
+            for (int k = C::kStreams == 2 ? int((tile ^ stream) & 1) : 0; k < n; k += C::kStreams, ++done) {
+                const long long it = tile + k;
+                const int t = g.tile0 + k, buf = int(it & 1);
+                ok = wait_bar(s_bar + buf, uint32_t(it >> 1) & 1, abort_flag);
                 if (!ok) break;
                 if (live_warp) {
                     gdn::tc_fence_after_sync();
-                    const uint32_t ts = trow + C::kS + uint32_t(tile & 1) * TK;
-                    float sv[TK / 32][32];
-#pragma unroll
-                    for (int k = 0; k < TK / 32; k += 2) gdn::tmem_ld32x2(ts + 32 * k, ts + 32 * k + 32, sv[k], sv[k + 1]);
+                    const uint32_t ts = trow + C::kS + uint32_t(buf) * TK;
+                    float sv[2][32];
+                    gdn::tmem_ld32x2(ts, ts + 32, sv[0], sv[1]);
                     if ((t + 1) * TK > g.safe) {
 #pragma unroll
-                        for (int k = 0; k < TK / 32; ++k) {
-                            const uint32_t vis = seen32(a.parents != nullptr, t * TK + 32 * k, g.q.ctx, upto, line);
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t vis = seen32(a.parents != nullptr, t * TK + 32 * z, g.q.ctx, upto, line);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!((vis >> e) & 1)) sv[k][e] = -INFINITY;
+                                if (!((vis >> e) & 1)) sv[z][e] = -INFINITY;
                         }
                     }
-                    float mx = -INFINITY;
+                    float mv[8];  // eight chains: few warps share a scheduler, so latency counts
 #pragma unroll
-                    for (int k = 0; k < TK / 32; ++k)
+                    for (int e = 0; e < 8; ++e) mv[e] = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, sv[k][e]);
-                    mx *= c;
-                    if (t == g.tile0) {
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mv[e & 7] = fmaxf(mv[e & 7], sv[z][e]);
+                    const float mx = c * fmaxf(fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3])),
+                                               fmaxf(fmaxf(mv[4], mv[5]), fmaxf(mv[6], mv[7])));
+                    if (done == 0) {
                         m = mx;
                     } else {
                         const bool move = mx > m + 8.f;
                         if (__any_sync(full, move)) {
-                            // O may be scaled once the product before this one has added to it
-                            ok = wait_bar(&pv_bar, uint32_t(tile - 1) & 1, abort_flag);
-                            if (!ok) break;
+                            // O may be scaled once the product before this one has added to it (with two
+                            // streams it has: S of this tile took the place of that product's P)
+                            if (C::kStreams == 1) {
+                                ok = wait_bar(pv_bar + ((it - 1) & 1), uint32_t((it - 1) >> 1) & 1, abort_flag);
+                                if (!ok) break;
+                            }
                             gdn::tc_fence_after_sync();
                             const float f = move ? exp2_approx(m - mx) : 1.f;
                             if (move) m = mx;
@@ -671,44 +690,58 @@ __global__ void __launch_bounds__(att::kThreads, 1)
 #pragma unroll 1
                             for (int cc = 0; cc < D; cc += 32) {
                                 float v[32];
-                                uint32_t w[32];
-                                gdn::tmem_ld32(trow + C::kO + cc, v);
+                                uint32_t r[32];
+                                gdn::tmem_ld32(trow + C::kO + stream * D + cc, v);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(v[e] * f);
-                                tmem_st32(trow + C::kO + cc, w);
+                                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(v[e] * f);
+                                tmem_st32(trow + C::kO + stream * D + cc, r);
                             }
                         }
                     }
                     const float mu = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet
                     const uint64_t c2 = gdn::f2pack(c, c), mu2 = gdn::f2pack(-mu, -mu);
-                    uint64_t sum = gdn::f2pack(0.f, 0.f);
+                    uint64_t sum[4];
 #pragma unroll
-                    for (int k = 0; k < TK / 64; ++k) {
-                        uint32_t w[32];
+                    for (int e = 0; e < 4; ++e) sum[e] = gdn::f2pack(0.f, 0.f);
+                    uint32_t r[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float *x = &sv[2 * k + (e >> 4)][2 * (e & 15)];
-                            const float2 y = gdn::f2unpack(gdn::fma2(gdn::f2pack(x[0], x[1]), c2, mu2));
-                            const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
-                            sum = gdn::add2(sum, gdn::f2pack(p0, p1));
-                            w[e] = gdn::Half2<T>::pack(p0, p1);
-                        }
-                        tmem_st32(ts + 32 * k, w);
+                    for (int e = 0; e < 32; ++e) {
+                        const float *x = &sv[e >> 4][2 * (e & 15)];
+                        const float2 y = gdn::f2unpack(gdn::fma2(gdn::f2pack(x[0], x[1]), c2, mu2));
+                        const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+                        sum[e & 3] = gdn::add2(sum[e & 3], gdn::f2pack(p0, p1));
+                        r[e] = gdn::Half2<T>::pack(p0, p1);
                     }
-                    const float2 s2 = gdn::f2unpack(sum);
+                    tmem_st32(ts, r);
+                    const float2 s2 = gdn::f2unpack(gdn::add2(gdn::add2(sum[0], sum[1]), gdn::add2(sum[2], sum[3])));
                     l += s2.x + s2.y;
                     tmem_wait_st();
                     gdn::tc_fence_before_sync();
                 }
                 __syncwarp();
-                if (lane == 0) arrive(p_bar + (tile & 1));
+                if (lane == 0) arrive(p_bar + buf);
             }
             if (!ok) break;
             // ---- the segment's rows out ---------------------------------------------------
-            // the last product; the one before it first, so that the phase is not mistaken for that of two before
-            if (tile > 1) ok = wait_bar(&pv_bar, uint32_t(tile - 2) & 1, abort_flag);
-            ok = ok && wait_bar(&pv_bar, uint32_t(tile - 1) & 1, abort_flag);
-            if (!ok) break;
+            if (done > 0) {  // this warpgroup's last product (all before it are complete with it)
+                const long long it = tile + n - 1 - (C::kStreams == 2 ? int((tile + n - 1 - stream) & 1) : 0);
+                ok = wait_bar(pv_bar + (it & 1), uint32_t(it >> 1) & 1, abort_flag);
+                if (!ok) break;
+            }
+            float f0 = 1.f, f1 = 0.f;  // factors of the streams' O
+            if (C::kStreams == 2) {
+                ml[seg & 1][stream][row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) arrive(&ml_bar);
+                ok = wait_bar(&ml_bar, seg & 1, abort_flag);
+                if (!ok) break;
+                const float2 x0 = ml[seg & 1][0][row], x1 = ml[seg & 1][C::kStreams - 1][row];
+                m = fmaxf(x0.x, x1.x);
+                // a stream that has seen nothing has no part (its O may never have been written)
+                f0 = x0.x == -INFINITY ? 0.f : exp2_approx(x0.x - m);
+                f1 = x1.x == -INFINITY ? 0.f : exp2_approx(x1.x - m);
+                l = (f0 == 0.f ? 0.f : f0 * x0.y) + (f1 == 0.f ? 0.f : f1 * x1.y);
+            }
             gdn::tc_fence_after_sync();
             const bool whole = g.starts && g.ends;
             const int slot = g.starts ? 1 : 0;
@@ -717,7 +750,7 @@ __global__ void __launch_bounds__(att::kThreads, 1)
                 if (tid == 0) meta[slot] = make_int4(g.rows, g.ends, g.q.n0 + g.i0, g.h);
                 if (slot) tail_part = true;
                 else head_part = true;
-                if (live) {
+                if (live && stream == 0) {
                     part[row] = m;
                     part[kRows + row] = l;
                 }
@@ -728,7 +761,7 @@ __global__ void __launch_bounds__(att::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     bits[k] = *reinterpret_cast<volatile uint32_t *>(&nf[0][seg % kNfBufs][k]) |
-                              *reinterpret_cast<volatile uint32_t *>(&nf[1][seg % kNfBufs][k]);
+                              *reinterpret_cast<volatile uint32_t *>(&nf[C::kCleanWarps - 1][seg % kNfBufs][k]);
                     odd |= bits[k] != 0;
                 }
             }
@@ -736,13 +769,21 @@ __global__ void __launch_bounds__(att::kThreads, 1)
             if (live_warp) {
                 T *orow = static_cast<T *>(a.o) + ((int64_t(g.q.n0) + i) * a.Hq + hd) * D;
 #pragma unroll 1
-                for (int cc = 0; cc < D; cc += 32) {
+                for (int cc = col0; cc < col0 + kCols; cc += 32) {
                     float v[32];
-                    gdn::tmem_ld32(trow + C::kO + cc, v);
+                    if (C::kStreams == 2) {
+                        float v1[32];
+                        gdn::tmem_ld32x2(trow + C::kO + cc, trow + C::kO + D + cc, v, v1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = (f0 == 0.f ? 0.f : f0 * v[e]) + (f1 == 0.f ? 0.f : f1 * v1[e]);
+                    } else {
+                        gdn::tmem_ld32(trow + C::kO + cc, v);
+                    }
                     if (odd && live) {  // values that are not finite, for the rows that see them
                         for (int k = 0; k < 4; ++k)
-                            for (uint32_t w = bits[k]; w; w &= w - 1) {
-                                const int x = g.safe + 32 * k + __ffs(w) - 1;
+                            for (uint32_t b = bits[k]; b; b &= b - 1) {
+                                const int x = g.safe + 32 * k + __ffs(b) - 1;
                                 if (!(seen32(a.parents != nullptr, x, g.q.ctx, upto, line) & 1)) continue;
                                 const int64_t at = gdn::position_offset(a.pl, g.s, x);
                                 if (at < 0) continue;
@@ -774,6 +815,7 @@ __global__ void __launch_bounds__(att::kThreads, 1)
                     }
                 }
             }
+            tile += n;
             ++seg;
         }
         if (tid == 0) {
@@ -784,7 +826,7 @@ __global__ void __launch_bounds__(att::kThreads, 1)
     gdn::tc_fence_before_sync();
     __syncthreads();
     if (tid == 0 && abort_s) gdn::record_status(a.status, GDN_DEV_TIMEOUT);
-    if (warp == kMma) gdn::tmem_dealloc(tmem, 512);
+    if (warp == C::kMmaS) gdn::tmem_dealloc(tmem, 512);
 }
 
 // Joins the parts of items that more than one CTA worked on: block (b, y) takes
@@ -836,7 +878,7 @@ template <typename T, int D>
 int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *workspace, int ctas, cudaStream_t st) {
     using C = att::Cfg<D>;
     CUtensorMap kmap, vmap;
-    const uint32_t rows = uint32_t(dims->page_size < C::TK ? dims->page_size : C::TK);
+    const uint32_t rows = uint32_t(dims->page_size < att::TK ? dims->page_size : att::TK);
     int rc;
     if ((rc = gdn::encode_kv_pages(&kmap, k_pool, dims, rows)) || (rc = gdn::encode_kv_pages(&vmap, a.v_pool, dims, rows)))
         return rc;
@@ -845,7 +887,7 @@ int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *wor
     auto k = paged_attention_kernel<T, D>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem)) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    if (gdn::launch_pdl(k, dim3(unsigned(ctas)), dim3(att::kThreads), C::kSmem, st, kmap, vmap, a) != cudaSuccess)
+    if (gdn::launch_pdl(k, dim3(unsigned(ctas)), dim3(C::kThreads), C::kSmem, st, kmap, vmap, a) != cudaSuccess)
         return GDN_ERR_LAUNCH;
     return gdn::launch_pdl(attention_join_kernel<T, D>, dim3(unsigned(ctas), 8), dim3(256), 0, st, a, ctas) == cudaSuccess
                ? GDN_OK
