@@ -34,7 +34,10 @@
 //           moves of m, results out.  For D <= 128 the softmax is longer than the
 //           products: two warpgroups take alternate tiles, each with an O, m and l of
 //           its own, joined at the end of a segment.
-//   TMA     K_0 K_1 V_0 K_2 V_1 ...; a lane per (page, 64 columns)
+//   TMA     K_0 K_1 V_0 K_2 V_1 ...  A box costs ~90 cycles whatever it holds, so a
+//           tile is one box where it lies in one page, and else one per page (V,
+//           whose K = 16 steps need not be evenly spaced) or per page and 64 columns
+//           (K, whose rows have to be).
 //   mma     two warps: S_{i+1} = Q K_{i+1}^T runs while P_i is formed
 //   clean   values of tiles in which some rows do not see some positions: what no row
 //           sees (the rest of a page) is set to 0, and elements that are not finite
@@ -78,6 +81,15 @@ struct Cfg {
     // workspace of a CTA: two parts (0: an item that began before, 1: one that goes on) of m, l and O
     static constexpr size_t kPartFloats = size_t(kRows) * (D + 2);
 };
+
+// A tile of values lies as boxes of v_rows positions, each [64 columns][position];
+// pages of 16 and 32 tokens arrive as one box each.
+__device__ __forceinline__ int v_box_rows(int shift) { return shift == 4 ? 16 : shift == 5 ? 32 : TK; }
+template <typename C>
+__device__ __forceinline__ uint32_t v_place(int v_rows, int r) {  // bytes from the tile's start to row r of its first 64 columns
+    const int box = r & ~(v_rows - 1);
+    return uint32_t(box) * (128 * C::kChunks) + uint32_t(r - box) * 128;
+}
 
 struct Args {
     const void *__restrict__ q;
@@ -231,12 +243,12 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead)
     return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(lead >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int row, int head, int page,
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int row, int chunk, int head, int page,
                                             uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(page), "r"(gdn::smem_addr(bar))
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(head), "r"(page), "r"(gdn::smem_addr(bar))
         : "memory");
 }
 // Warp-collective: thread t writes 32 columns (words) of lane (taddr lane) + t.
@@ -399,30 +411,28 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     if (warp == kTma) {
         // ---- keys and values by TMA -------------------------------------------------
         asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
-        const int bx = min(1 << a.pl.shift, TK);            // rows of a box
-        const int b = lane / C::kChunks, ch = lane % C::kChunks;
-        const uint32_t dst = ch * C::kChunkBytes + uint32_t(b) * bx * 128u;
+        const int ps = 1 << a.pl.shift, np = max(1, TK / ps);  // pages of a tile
+        // boxes of K: the whole tile, or (page, 64 columns); of V: whole pages from 16 tokens on
+        const bool k_whole = ps >= TK, v_pages = ps >= 16;
+        const int kb = k_whole ? 0 : lane / C::kChunks, kc = k_whole ? 0 : lane % C::kChunks;
+        const int vb = v_pages ? lane : kb, vc = v_pages ? 0 : kc;
+        const bool k_lane = k_whole ? lane == 0 : kb < np, v_lane = vb < np;
+        const uint32_t k_bytes = k_whole ? C::kTile : ps * 128u;
+        const uint32_t v_bytes = v_pages ? min(ps, TK) * 128u * C::kChunks : ps * 128u;
+        const uint32_t k_dst = kc * C::kChunkBytes + uint32_t(kb) * ps * 128u;
+        const uint32_t v_dst = v_pages ? vb * v_bytes : k_dst;
         int stage = 0;
         uint32_t phase = 0;
         long long issued = 0;
         bool ok = true, bad_page = false;
-        // the page of this lane's box of tile t (-1: nothing to load)
-        auto page_of = [&](const Segment &sg, int t) {
-            const int x = t * TK + b * bx;
-            if (b * bx >= TK || x >= sg.limit) return -1;
-            const int p = a.pl.table[int64_t(sg.s) * a.pl.width + (x >> a.pl.shift)];
-            if (p < 0 || p >= a.pl.n_pages) {
-                bad_page = true;
-                return -1;
-            }
-            return p;
-        };
-        auto load = [&](const CUtensorMap *map, int page, int row, int head) {
+        auto load = [&](const CUtensorMap *map, bool mine, int page, uint32_t dst, uint32_t bytes, int chunk, int row,
+                        int head) {
             if (!wait_bar(empty_bar + stage, phase ^ 1, abort_flag)) return false;
-            const unsigned m = __ballot_sync(full, page >= 0);
-            if (lane == 0) gdn::mbar_arrive_expect_tx(full_bar + stage, __popc(m) * bx * 128u);
+            mine = mine && page >= 0;
+            const unsigned m = __ballot_sync(full, mine);
+            if (lane == 0) gdn::mbar_arrive_expect_tx(full_bar + stage, __popc(m) * bytes);
             __syncwarp();
-            if (page >= 0) tma_load_4d(tb + stage * C::kTile + dst, map, 64 * ch, row, head, page, full_bar + stage);
+            if (mine) tma_load_5d(tb + stage * C::kTile + dst, map, row, chunk, head, page, full_bar + stage);
             ++issued;
             if (++stage == C::kStages) {
                 stage = 0;
@@ -431,16 +441,41 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             return true;
         };
         while (ok && walk.next(g)) {
-            int page = page_of(g, g.tile0), prev = -1;
-            const int mask = (1 << a.pl.shift) - 1;
-            for (int t = g.tile0; t < g.tile1 && ok; ++t) {
-                const int nextp = t + 1 < g.tile1 ? page_of(g, t + 1) : -1;
-                ok = load(&kmap, page, (t * TK + b * bx) & mask, g.h);
-                if (ok && t > g.tile0) ok = load(&vmap, prev, ((t - 1) * TK + b * bx) & mask, g.h);
-                prev = page;
-                page = nextp;
+            // the segment's page-table entries, 32 in each of two registers, loaded ahead and
+            // looked at when their tile is requested
+            const int32_t *table = a.pl.table + int64_t(g.s) * a.pl.width;
+            const int last = (g.limit - 1) >> a.pl.shift;  // the item's last page
+            int base = (g.tile0 * TK) >> a.pl.shift;
+            auto entry = [&](int o) { return o <= last ? table[o] : -1; };
+            int cur = entry(base + lane), nxt = entry(base + 32 + lane);
+            auto page_of = [&](int first, int b) {  // page `first + b` (checked)
+                const int o = first + b - base;
+                const int lo = __shfl_sync(full, cur, o & 31), hi = __shfl_sync(full, nxt, o & 31);
+                const int p = o < 32 ? lo : hi;
+                if (first + b > last) return -1;
+                if (p < 0 || p >= a.pl.n_pages) {
+                    bad_page = true;
+                    return -1;
+                }
+                return p;
+            };
+            int v_page = -1;
+            for (int t = g.tile0; t <= g.tile1 && ok; ++t) {
+                int k_page = -1, next_v = -1;
+                if (t < g.tile1) {
+                    const int first = (t * TK) >> a.pl.shift;
+                    if (first - base >= 32) {
+                        cur = nxt;
+                        base += 32;
+                        nxt = entry(base + 32 + lane);
+                    }
+                    k_page = page_of(first, k_lane ? kb : 0);
+                    next_v = page_of(first, v_lane ? vb : 0);
+                    ok = load(&kmap, k_lane, k_page, k_dst, k_bytes, kc, (t * TK) & (ps - 1), g.h);
+                }
+                if (ok && t > g.tile0) ok = load(&vmap, v_lane, v_page, v_dst, v_bytes, vc, ((t - 1) * TK) & (ps - 1), g.h);
+                v_page = next_v;
             }
-            if (ok) ok = load(&vmap, prev, ((g.tile1 - 1) * TK + b * bx) & mask, g.h);
         }
         if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
         if (!ok) {  // after a timeout copies may be in flight: wait for them (bounded)
@@ -461,6 +496,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         constexpr uint32_t kIdS = (1u << 4) | (fmt << 7) | (fmt << 10) | (uint32_t(TK >> 3) << 17) | (8u << 24);
         constexpr uint32_t kIdO = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);
         const bool is_s = warp == C::kMmaS;
+        const int v_rows = v_box_rows(a.pl.shift);
         uint32_t seg = 0, masked = 0;
         long long loads = 0, tile = 0;  // of the segments before: ring places, tiles (buffers and phases of S, P)
         bool ok = true;
@@ -503,7 +539,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         const uint32_t o = tmem + C::kO + (C::kStreams == 2 ? uint32_t(i & 1) * D : 0u);
 #pragma unroll
                         for (int z = 0; z < TK / 16; ++z)
-                            mma_f16_ta(o, p + 8 * z, desc_mn_sw128(vb + z * 2048, C::kChunkBytes), kIdO,
+                            mma_f16_ta(o, p + 8 * z, desc_mn_sw128(vb + v_place<C>(v_rows, 16 * z), v_rows * 128), kIdO,
                                        z > 0 || k >= C::kStreams);
                         gdn::mma_commit(pv_bar + (i & 1));
                         gdn::mma_commit(empty_bar + stage);
@@ -524,7 +560,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         uint32_t seg = 0, masked = 0;
         bool ok = true;
         constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
-        const int ct = tid - kClean0 * 32;
+        const int ct = tid - kClean0 * 32, v_rows = v_box_rows(a.pl.shift);
         while (ok && walk.next(g)) {
             const int n = g.tile1 - g.tile0;
             uint32_t bits[4] = {0, 0, 0, 0};
@@ -538,7 +574,8 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 unsigned char *vt = tiles + size_t(stage) * C::kTile;
                 for (int u = ct; u < (TK - r0) * C::kChunks * 8; u += 32 * C::kCleanWarps) {
                     const int r = r0 + u / (C::kChunks * 8), c16 = u % (C::kChunks * 8);
-                    uint4 *w = reinterpret_cast<uint4 *>(vt + (c16 >> 3) * C::kChunkBytes + r * 128 + (c16 & 7) * 16);
+                    uint4 *w = reinterpret_cast<uint4 *>(vt + v_place<C>(v_rows, r) + (c16 >> 3) * (v_rows * 128) +
+                                                         (c16 & 7) * 16);
                     const int x = t * TK + r;
                     if (x >= g.limit) {
                         *w = make_uint4(0, 0, 0, 0);
@@ -878,9 +915,11 @@ template <typename T, int D>
 int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *workspace, int ctas, cudaStream_t st) {
     using C = att::Cfg<D>;
     CUtensorMap kmap, vmap;
-    const uint32_t rows = uint32_t(dims->page_size < att::TK ? dims->page_size : att::TK);
+    const int ps = dims->page_size;
+    const uint32_t rows = uint32_t(ps < att::TK ? ps : att::TK);
     int rc;
-    if ((rc = gdn::encode_kv_pages(&kmap, k_pool, dims, rows)) || (rc = gdn::encode_kv_pages(&vmap, a.v_pool, dims, rows)))
+    if ((rc = gdn::encode_kv_pages(&kmap, k_pool, dims, rows, ps >= att::TK ? C::kChunks : 1)) ||
+        (rc = gdn::encode_kv_pages(&vmap, a.v_pool, dims, rows, ps >= 16 ? C::kChunks : 1)))
         return rc;
     a.meta = static_cast<int4 *>(workspace);
     a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);
