@@ -17,7 +17,8 @@
 // Work.  The h_q / h_kv heads that share a key/value head are rows of one tile:
 // row r is (token i0 + r / G, head r % G), 128 / G tokens a tile, so keys and
 // values are read once for all of them.  An item is (sequence, key/value head, row
-// tile); its positions come in tiles of TK.  All items' tiles in a row are cut into
+// tile); its positions come in tiles of TK.  All items in a row,
+// each its tiles and a few tiles' worth for its beginning and end, are cut into
 // equal shares, one per CTA (one CTA per SM): lengths as ragged as they come keep
 // every SM busy to the end, one sequence alone spreads over the GPU, and a CTA has
 // at most one item that began before it and one that ends after it.  Those parts
@@ -26,8 +27,9 @@
 //
 // Mapping (GB300).  Tensor memory holds O (D columns, fp32), Q (D / 2 columns, the
 // A operand of Q K^T: nothing of it is read again from shared memory, which leaves
-// all of that to keys and values) and two score tiles (64 columns each), P taking
-// its scores' place as the A operand of P V.  Shared memory is a ring of 192 KB of
+// all of that to keys and values), one score tile per warpgroup (64 columns) and two
+// of P (32 columns, the A operand of P V), so that the next scores need not wait for
+// the product.  Shared memory is a ring of 192 KB of
 // key and value tiles, filled by TMA page by page in the 128-byte swizzle: keys as
 // they lie are the K-major B operand, values as they lie the MN-major one.
 //   rows    four warps, row r = 32 w + lane = tensor-memory lane: Q in, scores -> P,
@@ -55,6 +57,7 @@ namespace att {
 
 constexpr int kRows = 128;
 constexpr int TK = 64;       // positions of a tile
+constexpr int kItemUnits = 4; // what an item costs beside its tiles (Q in, results out), in tiles
 constexpr int kNfBufs = 16;  // the ring holds the values of 12 segments at most, and one may still be going out
 
 template <int D_>
@@ -72,8 +75,11 @@ struct Cfg {
     static constexpr int kStages = 196608 / kTile;
     static constexpr size_t kSmem = 1024 + 196608;
     // tensor-memory columns
-    static constexpr uint32_t kO = 0, kQ = kStreams * D, kS = kQ + D / 2;
-    static_assert(kStreams * D + D / 2 + 2 * TK <= 512, "tensor memory");
+    static constexpr int kSBufs = kStreams;
+    static constexpr uint32_t kO = 0, kQ = kStreams * D, kS = kQ + D / 2, kP = kS + kSBufs * TK;
+    static_assert(kP + 2 * (TK / 2) <= 512, "tensor memory");
+    static __device__ __forceinline__ int s_buf(long long i) { return kSBufs == 2 ? int(i & 1) : 0; }
+    static __device__ __forceinline__ uint32_t s_use(long long i) { return uint32_t(kSBufs == 2 ? i >> 1 : i); }
     static_assert(kStages / 2 + 2 <= kNfBufs, "flags of the segments in the ring");
     // place in the ring of a segment's K and V tile k of n: K_0 K_1 V_0 K_2 V_1 ... V_{n-1}
     static __device__ __forceinline__ int k_at(int k) { return k == 0 ? 0 : 2 * k - 1; }
@@ -145,22 +151,23 @@ __device__ __forceinline__ Seq checked(const Args &a, int s, const RawSeq &r, in
     if (err) *err = e;
     return q;
 }
-__device__ __forceinline__ int item_tiles(const Seq &q, int j, int R) {
-    return (q.ctx + min((j + 1) * R, q.n) + TK - 1) / TK;
+// Units of work of row tile j: its tiles and kItemUnits at its front.
+__device__ __forceinline__ int item_units(const Seq &q, int j, int R) {
+    return (q.ctx + min((j + 1) * R, q.n) + TK - 1) / TK + kItemUnits;
 }
-// tiles of row tiles 0 .. j - 1 (j <= the number of row tiles - 1)
-__device__ __forceinline__ long long tiles_before(const Seq &q, int j, int R) {
-    return floor_sum(j, TK, R, (long long)q.ctx + R + TK - 1);
+// units of row tiles 0 .. j - 1 (j <= the number of row tiles - 1)
+__device__ __forceinline__ long long units_before(const Seq &q, int j, int R) {
+    return floor_sum(j, TK, R, (long long)q.ctx + R + TK - 1) + (long long)j * kItemUnits;
 }
-__device__ __forceinline__ long long head_tiles(const Seq &q, int R) {
+__device__ __forceinline__ long long head_units(const Seq &q, int R) {
     if (q.n == 0) return 0;
     const int J = (q.n + R - 1) / R;
-    return tiles_before(q, J - 1, R) + item_tiles(q, J - 1, R);
+    return units_before(q, J - 1, R) + item_units(q, J - 1, R);
 }
 
 struct Start {
     int s, h, j, off;
-    long long count;  // tiles of this CTA
+    long long count;  // units of this CTA
 };
 
 // A CTA's run through its share, segment by segment (a segment: consecutive tiles
@@ -185,41 +192,43 @@ struct Walk {
         }
     }
     __device__ __forceinline__ bool next(Segment &g) {
-        if (left <= 0) return false;
-        const int total = item_tiles(q, j, a.R);
-        const int take = int(min((long long)(total - off), left));
-        g.s = s;
-        g.h = h;
-        g.i0 = j * a.R;
-        const int toks = min(a.R, q.n - g.i0);
-        g.rows = toks * a.G;
-        g.tile0 = off;
-        g.tile1 = off + take;
-        g.starts = off == 0;
-        g.ends = off + take == total;
-        g.limit = q.ctx + g.i0 + toks;
-        g.safe = a.parents ? q.ctx : q.ctx + g.i0 + 1;
-        g.q = q;
-        left -= take;
-        off += take;
-        if (g.ends) {
-            off = 0;
-            if ((j + 1) * a.R >= q.n) {
-                j = 0;
-                if (++h == a.Hkv) {
-                    h = 0;
-                    while (left > 0 && s + 1 < a.S) {  // the next sequence with tokens
-                        ++s;
-                        q = checked(a, s, nx);
-                        if (s + 1 < a.S) nx = load_raw(a, s + 1);
-                        if (q.n > 0) break;
+        while (left > 0) {
+            const int total = item_units(q, j, a.R);
+            const int take = int(min((long long)(total - off), left));
+            g.s = s;
+            g.h = h;
+            g.i0 = j * a.R;
+            const int toks = min(a.R, q.n - g.i0);
+            g.rows = toks * a.G;
+            g.tile0 = max(0, off - kItemUnits);
+            g.tile1 = max(0, off + take - kItemUnits);
+            g.starts = g.tile0 == 0;
+            g.ends = off + take == total;
+            g.limit = q.ctx + g.i0 + toks;
+            g.safe = a.parents ? q.ctx : q.ctx + g.i0 + 1;
+            g.q = q;
+            left -= take;
+            off += take;
+            if (g.ends) {
+                off = 0;
+                if ((j + 1) * a.R >= q.n) {
+                    j = 0;
+                    if (++h == a.Hkv) {
+                        h = 0;
+                        while (left > 0 && s + 1 < a.S) {  // the next sequence with tokens
+                            ++s;
+                            q = checked(a, s, nx);
+                            if (s + 1 < a.S) nx = load_raw(a, s + 1);
+                            if (q.n > 0) break;
+                        }
                     }
+                } else {
+                    ++j;
                 }
-            } else {
-                ++j;
             }
+            if (g.tile1 > g.tile0) return true;  // (a share that ends in an item's front has no tile of it)
         }
-        return true;
+        return false;
     }
 };
 
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     constexpr int kThreads = C::kThreads, kTma = C::kTma, kClean0 = C::kClean0;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
-    __shared__ uint64_t s_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, go_bar, clean_bar, drain_bar[2];
+    __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, go_bar, clean_bar, drain_bar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     __shared__ Start start_s;
@@ -327,6 +336,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             gdn::mbar_init(s_bar + i, 1);
+            gdn::mbar_init(sfree_bar + i, 4);
             gdn::mbar_init(p_bar + i, 4);
             gdn::mbar_init(pv_bar + i, 1);
             gdn::mbar_init(drain_bar + i, 1);
@@ -345,7 +355,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     }
     gdn::grid_dep_wait();  // lengths, q, the pools and the workspace
 
-    // ---- the schedule: tiles of all sequences, cut into equal shares ------------
+    // ---- the schedule: units of all sequences, cut into equal shares ------------
     const int per = (a.S + kThreads - 1) / kThreads;
     long long mine = 0;
     for (int k = 0; k < per; ++k) {
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         int err;
         const Seq q = checked(a, s, load_raw(a, s), &err);
         if (err && blockIdx.x == 0) gdn::record_status(a.status, err);
-        mine += head_tiles(q, a.R) * a.Hkv;
+        mine += head_units(q, a.R) * a.Hkv;
     }
     long long inc = mine;
 #pragma unroll
@@ -383,20 +393,20 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 for (int k = 0; k < per; ++k) {
                     const int s = tid * per + k;
                     const Seq q = checked(a, s, load_raw(a, s));
-                    const long long ht = head_tiles(q, a.R);
+                    const long long ht = head_units(q, a.R);
                     if (x >= ht * a.Hkv) {
                         x -= ht * a.Hkv;
                         continue;
                     }
                     const int h = int(x / ht);
                     x -= h * ht;
-                    int lo = 0, hi = (q.n + a.R - 1) / a.R;  // the last row tile with tiles_before <= x
+                    int lo = 0, hi = (q.n + a.R - 1) / a.R;  // the last row tile with units_before <= x
                     while (hi - lo > 1) {
                         const int mid = (lo + hi) / 2;
-                        if (tiles_before(q, mid, a.R) <= x) lo = mid;
+                        if (units_before(q, mid, a.R) <= x) lo = mid;
                         else hi = mid;
                     }
-                    start_s = Start{s, h, lo, int(x - tiles_before(q, lo, a.R)), t1 - t0};
+                    start_s = Start{s, h, lo, int(x - units_before(q, lo, a.R)), t1 - t0};
                     break;
                 }
             }
@@ -508,17 +518,17 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     const long long at = loads + C::k_at(k), i = tile + k;
                     const int stage = int(at % C::kStages);
                     ok = wait_bar(full_bar + stage, uint32_t(at / C::kStages) & 1, abort_flag);
-                    // the buffer held P of two tiles before
-                    if (i >= 2) ok = ok && wait_bar(pv_bar + (i & 1), uint32_t((i >> 1) - 1) & 1, abort_flag);
+                    const int sb = C::s_buf(i);  // its last scores have been read
+                    if (i >= C::kSBufs) ok = ok && wait_bar(sfree_bar + sb, (C::s_use(i) - 1) & 1, abort_flag);
                     if (!ok) break;
                     gdn::tc_fence_after_sync();
                     if (elect_one()) {
-                        const uint32_t kb = tb + stage * C::kTile, d = tmem + C::kS + uint32_t(i & 1) * TK;
+                        const uint32_t kb = tb + stage * C::kTile, d = tmem + C::kS + uint32_t(sb) * TK;
 #pragma unroll
                         for (int z = 0; z < D / 16; ++z)
                             mma_f16_ta(d, tmem + C::kQ + 8 * z,
                                        gdn::desc_sw128(kb + (z >> 2) * C::kChunkBytes) + 2 * (z & 3), kIdS, z > 0);
-                        gdn::mma_commit(s_bar + (i & 1));
+                        gdn::mma_commit(s_bar + sb);
                         gdn::mma_commit(empty_bar + stage);
                     }
                     __syncwarp();
@@ -535,7 +545,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     if (!ok) break;
                     gdn::tc_fence_after_sync();
                     if (elect_one()) {
-                        const uint32_t vb = tb + stage * C::kTile, p = tmem + C::kS + uint32_t(i & 1) * TK;
+                        const uint32_t vb = tb + stage * C::kTile, p = tmem + C::kP + uint32_t(i & 1) * (TK / 2);
                         const uint32_t o = tmem + C::kO + (C::kStreams == 2 ? uint32_t(i & 1) * D : 0u);
 #pragma unroll
                         for (int z = 0; z < TK / 16; ++z)
@@ -572,35 +582,46 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 if (!ok) break;
                 const int r0 = max(0, g.safe - t * TK);  // rows (positions) that some rows do not see
                 unsigned char *vt = tiles + size_t(stage) * C::kTile;
-                for (int u = ct; u < (TK - r0) * C::kChunks * 8; u += 32 * C::kCleanWarps) {
-                    const int r = r0 + u / (C::kChunks * 8), c16 = u % (C::kChunks * 8);
-                    uint4 *w = reinterpret_cast<uint4 *>(vt + v_place<C>(v_rows, r) + (c16 >> 3) * (v_rows * 128) +
+                constexpr int kRowPieces = C::kChunks * 8, kStep = 32 * C::kCleanWarps;
+                for (int u0 = ct; u0 < (TK - r0) * kRowPieces; u0 += 8 * kStep) {
+                    uint4 v[8];
+                    uint4 *w[8];
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) {
+                        const int u = min(u0 + z * kStep, (TK - r0) * kRowPieces - 1);
+                        const int r = r0 + u / kRowPieces, c16 = u % kRowPieces;
+                        w[z] = reinterpret_cast<uint4 *>(vt + v_place<C>(v_rows, r) + (c16 >> 3) * (v_rows * 128) +
                                                          (c16 & 7) * 16);
-                    const int x = t * TK + r;
-                    if (x >= g.limit) {
-                        *w = make_uint4(0, 0, 0, 0);
-                        continue;
+                        v[z] = *w[z];
                     }
-                    const uint4 v = *w;
-                    uint32_t e[4] = {v.x, v.y, v.z, v.w};
-                    bool any = false;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if ((e[i] & kExp) == kExp) {
-                            e[i] &= 0xFFFF0000u;
-                            any = true;
+                    for (int z = 0; z < 8; ++z) {
+                        const int u = u0 + z * kStep, x = t * TK + r0 + u / kRowPieces;
+                        if (u >= (TK - r0) * kRowPieces) break;
+                        if (x >= g.limit) {
+                            *w[z] = make_uint4(0, 0, 0, 0);
+                            continue;
                         }
-                        if (((e[i] >> 16) & kExp) == kExp) {
-                            e[i] &= 0xFFFFu;
-                            any = true;
-                        }
-                    }
-                    if (any) {
-                        *w = make_uint4(e[0], e[1], e[2], e[3]);
-                        const int bit = x - g.safe;
+                        uint32_t e[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+                        bool any = false;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i == bit >> 5) bits[i] |= 1u << (bit & 31);
+                        for (int i = 0; i < 4; ++i) {
+                            if ((e[i] & kExp) == kExp) {
+                                e[i] &= 0xFFFF0000u;
+                                any = true;
+                            }
+                            if (((e[i] >> 16) & kExp) == kExp) {
+                                e[i] &= 0xFFFFu;
+                                any = true;
+                            }
+                        }
+                        if (any) {
+                            *w[z] = make_uint4(e[0], e[1], e[2], e[3]);
+                            const int bit = x - g.safe;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i == bit >> 5) bits[i] |= 1u << (bit & 31);
+                        }
                     }
                 }
                 gdn::fence_proxy_async_smem();
@@ -683,14 +704,19 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             int done = 0;  // tiles of this warpgroup in this segment
             for (int k = C::kStreams == 2 ? int((tile ^ stream) & 1) : 0; k < n; k += C::kStreams, ++done) {
                 const long long it = tile + k;
-                const int t = g.tile0 + k, buf = int(it & 1);
-                ok = wait_bar(s_bar + buf, uint32_t(it >> 1) & 1, abort_flag);
+                const int t = g.tile0 + k, buf = int(it & 1), sb = C::s_buf(it);
+                ok = wait_bar(s_bar + sb, C::s_use(it) & 1, abort_flag);
                 if (!ok) break;
+                float sv[2][32];
                 if (live_warp) {
                     gdn::tc_fence_after_sync();
-                    const uint32_t ts = trow + C::kS + uint32_t(buf) * TK;
-                    float sv[2][32];
+                    const uint32_t ts = trow + C::kS + uint32_t(sb) * TK;
                     gdn::tmem_ld32x2(ts, ts + 32, sv[0], sv[1]);
+                    gdn::tc_fence_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0) arrive(sfree_bar + sb);
+                if (live_warp) {
                     if ((t + 1) * TK > g.safe) {
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
@@ -714,12 +740,10 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     } else {
                         const bool move = mx > m + 8.f;
                         if (__any_sync(full, move)) {
-                            // O may be scaled once the product before this one has added to it (with two
-                            // streams it has: S of this tile took the place of that product's P)
-                            if (C::kStreams == 1) {
-                                ok = wait_bar(pv_bar + ((it - 1) & 1), uint32_t((it - 1) >> 1) & 1, abort_flag);
-                                if (!ok) break;
-                            }
+                            // O may be scaled once this warpgroup's product before this one has added to it
+                            const long long pr = it - C::kStreams;
+                            ok = wait_bar(pv_bar + (pr & 1), uint32_t(pr >> 1) & 1, abort_flag);
+                            if (!ok) break;
                             gdn::tc_fence_after_sync();
                             const float f = move ? exp2_approx(m - mx) : 1.f;
                             if (move) m = mx;
@@ -749,11 +773,20 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         sum[e & 3] = gdn::add2(sum[e & 3], gdn::f2pack(p0, p1));
                         r[e] = gdn::Half2<T>::pack(p0, p1);
                     }
-                    tmem_st32(ts, r);
+                    // the place of P: the product of two tiles before has read it
+                    if (it >= 2) {
+                        ok = wait_bar(pv_bar + buf, uint32_t((it >> 1) - 1) & 1, abort_flag);
+                        if (!ok) break;
+                        gdn::tc_fence_after_sync();
+                    }
+                    tmem_st32(trow + C::kP + uint32_t(buf) * (TK / 2), r);
                     const float2 s2 = gdn::f2unpack(gdn::add2(gdn::add2(sum[0], sum[1]), gdn::add2(sum[2], sum[3])));
                     l += s2.x + s2.y;
                     tmem_wait_st();
                     gdn::tc_fence_before_sync();
+                } else if (it >= 2) {  // in step with the others, so that no phase is passed twice
+                    ok = wait_bar(pv_bar + buf, uint32_t((it >> 1) - 1) & 1, abort_flag);
+                    if (!ok) break;
                 }
                 __syncwarp();
                 if (lane == 0) arrive(p_bar + buf);
