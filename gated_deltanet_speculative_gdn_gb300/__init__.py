@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -129,12 +130,11 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:
-            pass
+        # torch can have initialised CUDA only if something has imported it; an initialised CUDA is an
+        # available one, and asking for availability again costs more than a launch
+        torch = sys.modules.get("torch")
+        if torch is not None and torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(stream, int):
         return stream

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     constexpr int kThreads = C::kThreads, kTma = C::kTma, kClean0 = C::kClean0;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
-    __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, go_bar, clean_bar, drain_bar[2];
+    __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, go_bar[2], clean_bar[2], drain_bar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     __shared__ Start start_s;
@@ -339,12 +339,12 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             gdn::mbar_init(sfree_bar + i, 4);
             gdn::mbar_init(p_bar + i, 4);
             gdn::mbar_init(pv_bar + i, 1);
+            gdn::mbar_init(go_bar + i, 1);
+            gdn::mbar_init(clean_bar + i, C::kCleanWarps);
             gdn::mbar_init(drain_bar + i, 1);
         }
         gdn::mbar_init(&q_bar, C::kRowWarps);
         gdn::mbar_init(&ml_bar, C::kRowWarps);
-        gdn::mbar_init(&go_bar, 1);
-        gdn::mbar_init(&clean_bar, C::kCleanWarps);
         gdn::fence_mbar_init();
         abort_s = 0;
         start_s.count = 0;
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         constexpr uint32_t kIdO = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);
         const bool is_s = warp == C::kMmaS;
         const int v_rows = v_box_rows(a.pl.shift);
-        uint32_t seg = 0, masked = 0;
+        uint32_t seg = 0, masked = 0, asked = 0;
         long long loads = 0, tile = 0;  // of the segments before: ring places, tiles (buffers and phases of S, P)
         bool ok = true;
         while (ok && walk.next(g)) {
@@ -538,10 +538,26 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     const long long at = loads + C::v_at(k, n), i = tile + k;
                     const int stage = int(at % C::kStages);
                     ok = wait_bar(full_bar + stage, uint32_t(at / C::kStages) & 1, abort_flag);
-                    const bool clean = (g.tile0 + k + 1) * TK > g.safe;  // the cleaning runs beside this tile's softmax
-                    if (clean && lane == 0) arrive(&go_bar);
-                    ok = ok && wait_bar(p_bar + (i & 1), uint32_t(i >> 1) & 1, abort_flag);
-                    if (clean) ok = ok && wait_bar(&clean_bar, masked++ & 1, abort_flag);
+                    if (!ok) break;
+                    // cleaning runs beside the softmax: this tile's is asked for now, the next one's too if its
+                    // values are there (two barriers each, as one may be under way while another is asked for)
+                    const bool clean = (g.tile0 + k + 1) * TK > g.safe;
+                    if (clean && asked == masked) {
+                        if (lane == 0) arrive(go_bar + (asked & 1));
+                        ++asked;
+                    }
+                    if (k + 1 < n && (g.tile0 + k + 2) * TK > g.safe) {
+                        const long long nx = loads + C::v_at(k + 1, n);
+                        if (__all_sync(full, gdn::mbar_test_wait(full_bar + nx % C::kStages, uint32_t(nx / C::kStages) & 1))) {
+                            if (lane == 0) arrive(go_bar + (asked & 1));
+                            ++asked;
+                        }
+                    }
+                    ok = wait_bar(p_bar + (i & 1), uint32_t(i >> 1) & 1, abort_flag);
+                    if (clean) {
+                        ok = ok && wait_bar(clean_bar + (masked & 1), (masked >> 1) & 1, abort_flag);
+                        ++masked;
+                    }
                     if (!ok) break;
                     gdn::tc_fence_after_sync();
                     if (elect_one()) {
@@ -569,7 +585,9 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         long long loads = 0;  // ring position of the segment's first load
         uint32_t seg = 0, masked = 0;
         bool ok = true;
-        constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+        // the exponents of two values, and their lowest bits
+        constexpr uint32_t kExp2 = std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
+        constexpr uint32_t kLow2 = std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u;
         const int ct = tid - kClean0 * 32, v_rows = v_box_rows(a.pl.shift);
         while (ok && walk.next(g)) {
             const int n = g.tile1 - g.tile0;
@@ -577,53 +595,51 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             for (int t = max(g.tile0, g.safe / TK); t < g.tile1 && ok; ++t) {
                 const long long at = loads + C::v_at(t - g.tile0, n);
                 const int stage = int(at % C::kStages);
-                ok = wait_bar(&go_bar, masked++ & 1, abort_flag) &&
+                const uint32_t mk = masked++;
+                ok = wait_bar(go_bar + (mk & 1), (mk >> 1) & 1, abort_flag) &&
                      wait_bar(full_bar + stage, uint32_t(at / C::kStages) & 1, abort_flag);
                 if (!ok) break;
                 const int r0 = max(0, g.safe - t * TK);  // rows (positions) that some rows do not see
                 unsigned char *vt = tiles + size_t(stage) * C::kTile;
-                constexpr int kRowPieces = C::kChunks * 8, kStep = 32 * C::kCleanWarps;
-                for (int u0 = ct; u0 < (TK - r0) * kRowPieces; u0 += 8 * kStep) {
+                constexpr int kRowPieces = C::kChunks * 8, kStep = 32 * C::kCleanWarps;  // 16-byte pieces
+                auto piece = [&](int u) {
+                    const int r = r0 + u / kRowPieces, c16 = u % kRowPieces;
+                    return reinterpret_cast<uint4 *>(vt + v_place<C>(v_rows, r) + (c16 >> 3) * (v_rows * 128) +
+                                                     (c16 & 7) * 16);
+                };
+                const int some = min(max(g.limit - t * TK - r0, 0), TK - r0) * kRowPieces;  // seen by some rows
+                for (int u0 = ct; u0 < some; u0 += 8 * kStep) {
                     uint4 v[8];
-                    uint4 *w[8];
+                    uint32_t any = 0;  // the top bit of a half is set where its exponent is all ones
 #pragma unroll
+                    for (int z = 0; z < 8; ++z) v[z] = *piece(min(u0 + z * kStep, some - 1));
+#pragma unroll
+                    for (int z = 0; z < 8; ++z)
+                        any |= (((v[z].x & kExp2) + kLow2) | ((v[z].y & kExp2) + kLow2) | ((v[z].z & kExp2) + kLow2) |
+                                ((v[z].w & kExp2) + kLow2)) & 0x80008000u;
+                    if (any == 0) continue;
+#pragma unroll 1
                     for (int z = 0; z < 8; ++z) {
-                        const int u = min(u0 + z * kStep, (TK - r0) * kRowPieces - 1);
-                        const int r = r0 + u / kRowPieces, c16 = u % kRowPieces;
-                        w[z] = reinterpret_cast<uint4 *>(vt + v_place<C>(v_rows, r) + (c16 >> 3) * (v_rows * 128) +
-                                                         (c16 & 7) * 16);
-                        v[z] = *w[z];
-                    }
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) {
-                        const int u = u0 + z * kStep, x = t * TK + r0 + u / kRowPieces;
-                        if (u >= (TK - r0) * kRowPieces) break;
-                        if (x >= g.limit) {
-                            *w[z] = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint32_t e[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-                        bool any = false;
-#pragma unroll
+                        const int u = u0 + z * kStep;
+                        if (u >= some) break;
+                        uint32_t *e = reinterpret_cast<uint32_t *>(piece(u));
+                        bool odd = false;
                         for (int i = 0; i < 4; ++i) {
-                            if ((e[i] & kExp) == kExp) {
-                                e[i] &= 0xFFFF0000u;
-                                any = true;
-                            }
-                            if (((e[i] >> 16) & kExp) == kExp) {
-                                e[i] &= 0xFFFFu;
-                                any = true;
+                            const uint32_t x = e[i], f = ((x & kExp2) + kLow2) & 0x80008000u;
+                            if (f) {
+                                e[i] = x & ~((f & 0x80000000u ? 0xFFFF0000u : 0u) | (f & 0x8000u ? 0xFFFFu : 0u));
+                                odd = true;
                             }
                         }
-                        if (any) {
-                            *w[z] = make_uint4(e[0], e[1], e[2], e[3]);
-                            const int bit = x - g.safe;
+                        if (odd) {
+                            const int bit = t * TK + r0 + u / kRowPieces - g.safe;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 if (i == bit >> 5) bits[i] |= 1u << (bit & 31);
                         }
                     }
                 }
+                for (int u = some + ct; u < (TK - r0) * kRowPieces; u += kStep) *piece(u) = make_uint4(0, 0, 0, 0);
                 gdn::fence_proxy_async_smem();
                 __syncwarp();
 #pragma unroll
@@ -632,7 +648,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     if (lane == i) nf[warp - kClean0][seg % kNfBufs][i] = bits[i];
                 }
                 __syncwarp();
-                if (lane == 0) arrive(&clean_bar);
+                if (lane == 0) arrive(clean_bar + (mk & 1));
             }
             loads += 2 * n;
             ++seg;
