@@ -134,7 +134,8 @@ def _stream(stream) -> Optional[int]:
         # available one, and asking for availability again costs more than a launch
         torch = sys.modules.get("torch")
         if torch is not None and torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object
+            return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(stream, int):
         return stream

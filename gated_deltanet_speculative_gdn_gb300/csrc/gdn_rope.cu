@@ -5,8 +5,9 @@
 // Mathematics.  A pair (y_a, y_b) is turned by phi = pos * f.  Far positions need
 // phi mod 2 pi to more than fp32: with f / (2 pi) mod 1 as a 64-bit fraction F,
 // the product pos * F wraps modulo 2^64, which is the reduction modulo one turn
-// itself, exact but for F's own rounding (2^-53 relative).  The top 32 bits, as a
-// signed fraction, go to sincospif.
+// itself, exact but for F's own rounding (2^-64).  The top 32 bits, as a signed
+// fraction, go to sincospif.  F comes from f's mantissa by one integer product:
+// in fp64 arithmetic (1/64 of the fp32 rate here) it took most of the kernel's time.
 //
 // Mapping.  A warp takes one token and a share of its rows (q heads, k heads, v
 // heads); a lane holds 8 elements (128-bit loads and stores), so a row of d takes
@@ -19,7 +20,23 @@
 namespace {
 
 constexpr int kWarps = 4;
-constexpr double kInv2Pi = 0.15915494309189533576888376337251;
+
+// f mod 2 pi, f finite and >= 0, as a 64-bit fraction of a turn.  f = m 2^(e - 52) with a
+// 53-bit m; f / (2 pi) 2^64 = m R 2^(e - 52) with R = 2^64 / (2 pi).
+__device__ __forceinline__ unsigned long long turn_fraction(double f) {
+    constexpr unsigned long long R = 0x28be60db9391054aull;
+    const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(f));
+    const int be = int((b >> 52) & 0x7ff);
+    const unsigned long long m = (b & 0xfffffffffffffull) | (be ? 1ull << 52 : 0);
+    const int shift = 52 - ((be ? be : 1) - 1023);  // to the right
+    const unsigned long long hi = __umul64hi(m, R), lo = m * R;
+    unsigned long long r;
+    if (shift >= 128) r = 0;
+    else if (shift >= 64) r = hi >> (shift - 64);
+    else if (shift > 0) r = (lo >> shift) | (hi << (64 - shift));
+    else r = shift > -64 ? lo << -shift : 0;
+    return b >> 63 ? 0ull - r : r;
+}
 
 struct RopeArgs {
     const void *__restrict__ q, *__restrict__ k, *__restrict__ v;
@@ -54,6 +71,17 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs
     }
     const int n = int(wid / a.shares), share = int(wid % a.shares);
     if (n >= a.N) return;
+    const int rows = a.Hq + 2 * a.Hkv, slots = (rows + RW - 1) / RW;
+    const int col = 8 * l;
+    auto load_row = [&](int slot) {  // q heads, then k heads, then v heads
+        const int r = slot * RW + sub;
+        if (r >= rows) return make_uint4(0, 0, 0, 0);
+        const T *src = r < a.Hq ? static_cast<const T *>(a.q) + n * a.q_stride + int64_t(r) * D
+                       : r < a.Hq + a.Hkv ? static_cast<const T *>(a.k) + n * a.k_stride + int64_t(r - a.Hq) * D
+                                          : static_cast<const T *>(a.v) + n * a.v_stride + int64_t(r - a.Hq - a.Hkv) * D;
+        return *reinterpret_cast<const uint4 *>(src + col);
+    };
+    uint4 next = load_row(share);  // its latency passes under the angles'
     const int s = gdn::find_sequence(a.node_off, a.S, n);
     const int n0 = a.node_off[s], ctx = a.ctx_len[s];
     const int i = n - n0;
@@ -73,7 +101,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs
     }
 
     // the lane's cosines and sines: element e of the lane is column 8 l + e
-    const int half = a.rot / 2, col = 8 * l;
+    const int half = a.rot / 2;
     const bool turned = col < a.rot;
     const bool upper = !a.interleaved && col >= half;  // the lane holds second elements of pairs
     float cs[8], sn[8];
@@ -94,11 +122,9 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs
                 bad = true;
                 ax = 0;
             }
-            double f = a.inv_freq[p0 + e] * kInv2Pi;  // turns per position
-            f -= floor(f);
-            const unsigned long long frac = __double2ull_rz(f * 18446744073709551616.0);
             const unsigned long long turns =
-                static_cast<unsigned long long>(static_cast<long long>(a.pos[int64_t(n) * a.n_axes + ax])) * frac;
+                static_cast<unsigned long long>(static_cast<long long>(a.pos[int64_t(n) * a.n_axes + ax])) *
+                turn_fraction(a.inv_freq[p0 + e]);
             // a signed 32-bit fraction of a turn, in units of half turns
             sincospif(float(int(turns >> 32)) * (1.0f / 2147483648.0f), &sn[e], &cs[e]);
         }
@@ -113,7 +139,6 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs
     }
     const int hop = a.rot / 16;  // lanes between the halves of a pair
     const int partner = turned && !a.interleaved ? (upper ? lane - hop : lane + hop) : lane;
-    const int rows = a.Hq + 2 * a.Hkv, slots = (rows + RW - 1) / RW;
     float qw[8], kw[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -125,13 +150,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs
         const int r = slot * RW + sub;  // q heads, then k heads, then v heads
         const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv, live = r < rows;
         const int h = is_q ? r : is_k ? r - a.Hq : r - a.Hq - a.Hkv;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) {
-            const T *src = is_q ? static_cast<const T *>(a.q) + n * a.q_stride
-                                : is_k ? static_cast<const T *>(a.k) + n * a.k_stride
-                                       : static_cast<const T *>(a.v) + n * a.v_stride;
-            raw = *reinterpret_cast<const uint4 *>(src + int64_t(h) * D + col);
-        }
+        const uint4 raw = next;
+        if (slot + a.shares < slots) next = load_row(slot + a.shares);
         float y[8], z[8];
         gdn::unpack8<T>(raw, y);
         const bool norm = live && ((is_q && a.qw) || (is_k && a.kw));
