@@ -17,7 +17,8 @@
 // borders, so p - c q is formed as an unevaluated pair of floats (Dekker's and
 // Knuth's error-free product and sum; c as a pair too) and summed as one: 2^-48
 // relative, at ~16 fp32 operations an element, where fp64 arithmetic would run at
-// 1/64 of that rate.  The few scalars are fp64.
+// 1/64 of that rate.  The scalars (c, W, Z, thresholds, coarse cumulative sums) are
+// pairs too: as fp64 they took 3,000 to 13,000 cycles between passes.
 //
 // Mapping.  A cluster of CTAs takes a sequence, each CTA a contiguous slice of
 // the vocabulary.  Thread 0 of every CTA walks the tree with the same numbers (so
@@ -49,12 +50,17 @@ struct AcceptArgs {
     int S, N, V, max_nodes, replacement;
 };
 
+// An unevaluated sum of two floats, |l| <= ulp(h) / 2 where it is said to be normal.
 struct Pair {
     float h, l;
 };
 __device__ __forceinline__ Pair two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ Pair normal(float h, float l) {  // |h| >= |l|
+    const float s = __fadd_rn(h, l);
+    return {s, __fsub_rn(l, __fsub_rn(s, h))};
 }
 // max(p - (ch + cl) q, 0) as a pair
 __device__ __forceinline__ Pair residual(float p, float q, float ch, float cl) {
@@ -65,11 +71,31 @@ __device__ __forceinline__ Pair residual(float p, float q, float ch, float cl) {
     if (!(h > 0.f)) return {0.f, 0.f};
     return {h, __fsub_rn(l, __fsub_rn(h, s.h))};
 }
+// acc += v for terms >= 0; the result is made normal once, at the end of a sum
 __device__ __forceinline__ void add(Pair &acc, const Pair &v) {
     const Pair s = two_sum(acc.h, v.h);
     acc.h = s.h;
     acc.l = __fadd_rn(acc.l, __fadd_rn(s.l, v.l));
 }
+__device__ __forceinline__ Pair plus(const Pair &a, const Pair &b) {
+    Pair s = two_sum(a.h, b.h);
+    return normal(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Pair minus(const Pair &a, const Pair &b) { return plus(a, {-b.h, -b.l}); }
+__device__ __forceinline__ Pair times(const Pair &a, const Pair &b) {
+    const float p = __fmul_rn(a.h, b.h), e = __fmaf_rn(a.h, b.h, -p);
+    return normal(p, __fadd_rn(e, __fmaf_rn(a.h, b.l, __fmul_rn(a.l, b.h))));
+}
+__device__ __forceinline__ Pair over(const Pair &a, const Pair &b) {
+    const float q1 = __fdiv_rn(a.h, b.h);
+    Pair r = minus(a, times(b, {q1, 0.f}));
+    const float q2 = __fdiv_rn(r.h, b.h);
+    r = minus(r, times(b, {q2, 0.f}));
+    const Pair q = normal(q1, q2);
+    return normal(q.h, __fadd_rn(q.l, __fdiv_rn(r.h, b.h)));
+}
+__device__ __forceinline__ bool less(const Pair &a, const Pair &b) { return a.h < b.h || (a.h == b.h && a.l < b.l); }
+__device__ __forceinline__ Pair positive(const Pair &a) { return a.h > 0.f ? a : Pair{0.f, 0.f}; }
 
 // What a pass computes: rows of a node, c, and the tokens that are taken out.
 struct Pass {
@@ -79,31 +105,32 @@ struct Pass {
     int last;  // the pass is the one that the next token comes from
 };
 
-// The four residuals of vector i of the row (elements 4 i ..; zero past V)
-__device__ __forceinline__ void load4(const Pass &ps, const int *out, int i, int V, Pair (&r)[4]) {
-    const float4 p4 = *reinterpret_cast<const float4 *>(ps.p + 4 * int64_t(i));
-    float pv[4] = {p4.x, p4.y, p4.z, p4.w};
-    if (ps.q) {
-        const float4 q4 = *reinterpret_cast<const float4 *>(ps.q + 4 * int64_t(i));
-        const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
+// The four residuals of vector i of the row (elements 4 i ..; zero past V) from its values.  With q the
+// tokens that are taken out have none left by the formula itself.
+template <bool kQ>
+__device__ __forceinline__ void residual4(const Pass &ps, const int *out, int i, int V, const float4 &p4, const float4 &q4,
+                                          Pair (&r)[4]) {
+    const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, qv[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = residual(pv[e], qv[e], ps.ch, ps.cl);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = {pv[e] > 0.f ? pv[e] : 0.f, 0.f};
+    for (int e = 0; e < 4; ++e) {
+        if (kQ) r[e] = residual(pv[e], qv[e], ps.ch, ps.cl);
+        else r[e] = {pv[e] > 0.f ? pv[e] : 0.f, 0.f};
     }
-    for (int k = 0; k < ps.n_out; ++k)
-        if ((out[k] >> 2) == i) {
+    if (!kQ) {
+        for (int k = 0; k < ps.n_out; ++k)
+            if ((out[k] >> 2) == i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if ((out[k] & 3) == e) r[e] = {0.f, 0.f};
-        }
+                for (int e = 0; e < 4; ++e)
+                    if ((out[k] & 3) == e) r[e] = {0.f, 0.f};
+            }
+    }
     if (4 * i + 3 >= V) {  // the row's last vector: what lies behind the row is not read as values
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (4 * i + e >= V) r[e] = {0.f, 0.f};
     }
 }
+__device__ __forceinline__ float4 vec(const float *row, int i) { return __ldg(reinterpret_cast<const float4 *>(row) + i); }
 
 // Sum over the warp (lane 0's result is the one that is used).
 __device__ __forceinline__ Pair warp_sum(Pair v) {
@@ -112,20 +139,37 @@ __device__ __forceinline__ Pair warp_sum(Pair v) {
         const Pair w = {__shfl_down_sync(0xffffffffu, v.h, o), __shfl_down_sync(0xffffffffu, v.l, o)};
         add(v, w);
     }
-    return v;
+    return normal(v.h, v.l);
 }
 
-// Sum of vectors [lo, hi) of the row, lanes side by side (lane 0's result).
-__device__ __forceinline__ Pair sum_range(const Pass &ps, const int *out, int lo, int hi, int V) {
+// Sum of vectors [lo, hi) of the row, lanes side by side (lane 0's result): four vectors a lane are on
+// their way at a time.
+template <bool kQ>
+__device__ __forceinline__ Pair sum_range_t(const Pass &ps, const int *out, int lo, int hi, int V) {
+    constexpr int U = 4;
     Pair acc = {0.f, 0.f};
-#pragma unroll 4
-    for (int i = lo + (threadIdx.x & 31); i < hi; i += 32) {
-        Pair r[4];
-        load4(ps, out, i, V, r);
+    for (int i0 = lo + int(threadIdx.x & 31); i0 < hi; i0 += 32 * U) {
+        float4 p4[U], q4[U];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) add(acc, r[e]);
+        for (int z = 0; z < U; ++z) {
+            const int i = min(i0 + 32 * z, hi - 1);
+            p4[z] = vec(ps.p, i);
+            q4[z] = kQ ? vec(ps.q, i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int z = 0; z < U; ++z) {
+            const int i = i0 + 32 * z;
+            if (i >= hi) break;
+            Pair r[4];
+            residual4<kQ>(ps, out, i, V, p4[z], q4[z], r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) add(acc, r[e]);
+        }
     }
     return warp_sum(acc);
+}
+__device__ __forceinline__ Pair sum_range(const Pass &ps, const int *out, int lo, int hi, int V) {
+    return ps.q ? sum_range_t<true>(ps, out, lo, hi, V) : sum_range_t<false>(ps, out, lo, hi, V);
 }
 
 // Warp-collective: the first of `count` consecutive parts (lane k holds part k's
@@ -133,25 +177,27 @@ __device__ __forceinline__ Pair sum_range(const Pass &ps, const int *out, int lo
 // When none does (rounding at the very end, or no distribution) the last part
 // that is not empty, and thr becomes infinite, so that finer selections take the
 // last one too.
-__device__ __forceinline__ int select_part(double v, int count, double &b, double &thr) {
+__device__ __forceinline__ int select_part(Pair v, int count, Pair &b, Pair &thr) {
     const int lane = threadIdx.x & 31;
-    if (lane >= count) v = 0.0;
-    double inc = v;
+    if (lane >= count) v = {0.f, 0.f};
+    Pair inc = v, exc = {0.f, 0.f};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const Pair y = {__shfl_up_sync(0xffffffffu, inc.h, o), __shfl_up_sync(0xffffffffu, inc.l, o)};
+        if (lane >= o) inc = plus(inc, y);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, v > 0.0 && b + inc > thr);
-    const unsigned some = __ballot_sync(0xffffffffu, v > 0.0);
+    exc = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
+    if (lane == 0) exc = {0.f, 0.f};
+    const unsigned hit = __ballot_sync(0xffffffffu, v.h > 0.f && less(thr, plus(b, inc)));
+    const unsigned some = __ballot_sync(0xffffffffu, v.h > 0.f);
     int k;
     if (hit) {
         k = __ffs(hit) - 1;
     } else {
         k = some ? 31 - __clz(some) : 0;
-        thr = __longlong_as_double(0x7ff0000000000000ll);
+        thr = {INFINITY, 0.f};
     }
-    b += __shfl_sync(0xffffffffu, inc - v, k);
+    b = plus(b, {__shfl_sync(0xffffffffu, exc.h, k), __shfl_sync(0xffffffffu, exc.l, k)});
     return k;
 }
 
@@ -162,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
     __shared__ float pc[gdn::kMaxSeqNodes], qc[gdn::kMaxSeqNodes], uc[gdn::kMaxSeqNodes];  // p, q at the parent's row
     __shared__ Pass pass_s;
     __shared__ int err_s, step_s;              // what follows the pass: another, the selection, nothing
-    __shared__ double base_s, thr_s;           // of the selection
+    __shared__ Pair base_s, thr_s;             // of the selection
     __shared__ int lo_s, hi_s;
     cg::cluster_group cl = cg::this_cluster();
     const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
@@ -213,36 +259,39 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
 
     // thread 0's walk
     int cur = 0, t = 1, depth = 1, n_out = 0, parity = 0;
-    double c = 0.0, W = 1.0, Z = 1.0;
+    Pair c = {0.f, 0.f}, W = {1.f, 0.f}, Z = {1.f, 0.f};
     bool fallback = false;
     Pass ps;
+    const float un = a.u_next[s];
     for (;;) {
         if (tid == 0) {
             bool need = false;
             while (t < n && !need) {
-                if (par[t] == cur && Z > 0.0) {
+                if (par[t] == cur && Z.h > 0.f) {
                     const int y = tok[t];
                     bool was_out = false;
                     for (int k = 0; k < n_out; ++k) was_out |= out[k] == y;
-                    const double qx = was_out && a.q ? 0.0 : double(qc[t]);
-                    double px = was_out ? 0.0 : double(pc[t]) - (a.q ? c * double(qc[t]) : 0.0);
-                    px = px > 0.0 ? px : 0.0;
-                    if (double(uc[t]) * qx * W < px * Z) {
+                    const float qx = was_out && a.q ? 0.f : qc[t];
+                    Pair px = {0.f, 0.f};
+                    if (!was_out) px = a.q ? positive(minus({pc[t], 0.f}, times(c, {qx, 0.f}))) : positive({pc[t], 0.f});
+                    // both sides times 2^64 (exact): the low parts of small probabilities stay normal
+                    constexpr float kUp = 18446744073709551616.0f;
+                    if (less(times(times({uc[t], 0.f}, {qx * kUp, 0.f}), W), times({px.h * kUp, px.l * kUp}, Z))) {
                         cur = t;
                         ++depth;
                         n_out = 0;
-                        c = 0.0;
-                        W = Z = 1.0;
+                        c = {0.f, 0.f};
+                        W = Z = {1.f, 0.f};
                     } else {
                         if (!(a.q && a.replacement) && !was_out) out[n_out++] = y;
                         if (a.q) {
-                            c += W / Z;
-                            if (!a.replacement) Z = Z > qx ? Z - qx : 0.0;
+                            c = plus(c, over(W, Z));
+                            if (!a.replacement) Z = positive(minus(Z, {qx, 0.f}));
                             // the sum is wanted only if another child is tried
                             for (int x = t + 1; x < n; ++x) need |= par[x] == cur;
-                            need = need && Z > 0.0;
+                            need = need && Z.h > 0.f;
                         } else {
-                            W = W > px ? W - px : 0.0;
+                            W = positive(minus(W, px));
                         }
                     }
                 }
@@ -250,10 +299,10 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
             }
             const int64_t row = n0 + cur;
             pass_s.p = a.p + row * a.p_stride;
-            pass_s.q = a.q && c > 0.0 && !fallback ? a.q + row * a.q_stride : nullptr;
-            pass_s.ch = float(c);
-            pass_s.cl = float(c - double(float(c)));
-            pass_s.n_out = fallback ? 0 : n_out;
+            pass_s.q = a.q && c.h > 0.f && !fallback ? a.q + row * a.q_stride : nullptr;
+            pass_s.ch = c.h;
+            pass_s.cl = c.l;
+            pass_s.n_out = fallback || a.q ? 0 : n_out;
             pass_s.last = !need;
         }
         __syncthreads();
@@ -272,20 +321,19 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
         if (warp == 0) {
             const Pair mine = lane < C ? cta_tot[parity][lane] : Pair{0.f, 0.f};
             const Pair sum = warp_sum(mine);
-            double total = double(sum.h) + double(sum.l);
-            total = __shfl_sync(0xffffffffu, total, 0);
+            const Pair total = {__shfl_sync(0xffffffffu, sum.h, 0), __shfl_sync(0xffffffffu, sum.l, 0)};
             int step = 0;
             if (ps.last) {
-                const bool empty = !(total > 0.0) && !__shfl_sync(0xffffffffu, int(fallback), 0);
+                const bool empty = !(total.h > 0.f) && !__shfl_sync(0xffffffffu, int(fallback), 0);
                 if (empty) {
                     fallback = true;  // nothing is left: the target's own row
                 } else {
-                    double b = 0.0, thr = double(a.u_next[s]) * total;
-                    const bool owner = select_part(double(mine.h) + double(mine.l), C, b, thr) == rank;
+                    Pair b = {0.f, 0.f}, thr = times({un, 0.f}, total);
+                    const bool owner = select_part(mine, C, b, thr) == rank;
                     step = owner ? 2 : 1;
                     if (owner) {
                         const Pair w = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
-                        const int k = select_part(double(w.h) + double(w.l), kWarpsA, b, thr);
+                        const int k = select_part(w, kWarpsA, b, thr);
                         if (lane == 0) {
                             base_s = b;
                             thr_s = thr;
@@ -318,8 +366,8 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
         __syncthreads();
         if (warp == 0) {
             const Pair w = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
-            double b = base_s, thr = thr_s;
-            const int k = select_part(double(w.h) + double(w.l), kWarpsA, b, thr);
+            Pair b = base_s, thr = thr_s;
+            const int k = select_part(w, kWarpsA, b, thr);
             if (lane == 0) {
                 base_s = b;
                 thr_s = thr;
@@ -332,19 +380,26 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
     if (warp == 0) {
         Pair r[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
         const int i = lo_s + lane;
-        if (i < hi_s) load4(ps, out, i, a.V, r);
-        double e[4], run = 0.0;
+        if (i < hi_s) {
+            if (ps.q) residual4<true>(ps, out, i, a.V, vec(ps.p, i), vec(ps.q, i), r);
+            else residual4<false>(ps, out, i, a.V, vec(ps.p, i), make_float4(0.f, 0.f, 0.f, 0.f), r);
+        }
+        Pair e[4], run = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            run += double(r[k].h) + double(r[k].l);
+            run = plus(run, r[k]);
             e[k] = run;
         }
-        double b = base_s, thr = thr_s;
+        Pair b = base_s, thr = thr_s;
         const int src = select_part(run, 32, b, thr);
         if (lane == src) {
             int k = 0;
-            while (k < 3 && !(r[k].h > 0.f && b + e[k] > thr)) ++k;
-            while (k > 0 && !(r[k].h > 0.f)) --k;  // rounding: the lane's last element that is not 0
+#pragma unroll
+            for (int z = 2; z >= 0; --z)  // the first that passes the threshold, else the last that is not 0
+                if (r[z + 1].h > 0.f && k == 0) k = z + 1;
+#pragma unroll
+            for (int z = 3; z >= 0; --z)
+                if (r[z].h > 0.f && less(thr, plus(b, e[z]))) k = z;
             a.next_token[s] = min(max(4 * i + k, 0), a.V - 1);
         }
     }

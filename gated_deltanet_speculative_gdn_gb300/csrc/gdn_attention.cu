@@ -65,10 +65,8 @@ struct Cfg {
     static constexpr int D = D_;
     static constexpr int kStreams = D == 256 ? 1 : 2;     // softmax warpgroups, each with an O of its own
     static constexpr int kRowWarps = 4 * kStreams;
-    static constexpr int kTma = kRowWarps, kMmaS = kTma + 1, kMmaO = kTma + 2, kClean0 = kTma + 3;
-    // one cleaning warp beside two warpgroups: 12 warps, three to a scheduler, leave 168 registers a thread
-    static constexpr int kCleanWarps = kStreams == 2 ? 1 : 2;
-    static constexpr int kThreads = 32 * (kRowWarps + 3 + kCleanWarps);
+    static constexpr int kTma = kRowWarps, kMmaS = kTma + 1, kMmaO = kTma + 2, kClean = kTma + 3;
+    static constexpr int kThreads = 32 * (kRowWarps + 4);  // 8 or 12 warps: two or three to a scheduler
     static constexpr int kChunks = D / 64;                // 128-byte columns of a row
     static constexpr uint32_t kChunkBytes = TK * 128;
     static constexpr uint32_t kTile = TK * D * 2;         // 32, 16, 8 KB
@@ -166,6 +164,7 @@ __device__ __forceinline__ long long head_units(const Seq &q, int R) {
 }
 
 struct Start {
+    Seq q;
     int s, h, j, off;
     long long count;  // units of this CTA
 };
@@ -186,10 +185,8 @@ struct Walk {
     Seq q;
     RawSeq nx;  // of the next sequence, loaded one ahead and looked at when it is its turn
     __device__ Walk(const Args &a_, const Start &st) : a(a_), s(st.s), h(st.h), j(st.j), off(st.off), left(st.count) {
-        if (left > 0) {
-            q = checked(a, s, load_raw(a, s));
-            if (s + 1 < a.S) nx = load_raw(a, s + 1);
-        }
+        q = st.q;
+        if (left > 0 && s + 1 < a.S) nx = load_raw(a, s + 1);
     }
     __device__ __forceinline__ bool next(Segment &g) {
         while (left > 0) {
@@ -310,7 +307,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                            const att::Args a) {
     using namespace att;
     using C = Cfg<D>;
-    constexpr int kThreads = C::kThreads, kTma = C::kTma, kClean0 = C::kClean0;
+    constexpr int kThreads = C::kThreads, kTma = C::kTma;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
     __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, go_bar[2], clean_bar[2], drain_bar[2];
@@ -320,7 +317,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     __shared__ long long wsum[kThreads / 32];
     __shared__ int tree_par[C::kRowWarps][gdn::kMaxSeqNodes];
     __shared__ float2 ml[2][C::kStreams][kRows];  // by segment: m and l of each stream's rows
-    __shared__ uint32_t nf[C::kCleanWarps][kNfBufs][4];  // by cleaning warp and segment: positions from `safe` on with values that are not finite
+    __shared__ uint32_t nf[kNfBufs][4];  // by segment: positions from `safe` on with values that are not finite
     volatile int *abort_flag = &abort_s;
     unsigned char *tiles =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -340,7 +337,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             gdn::mbar_init(p_bar + i, 4);
             gdn::mbar_init(pv_bar + i, 1);
             gdn::mbar_init(go_bar + i, 1);
-            gdn::mbar_init(clean_bar + i, C::kCleanWarps);
+            gdn::mbar_init(clean_bar + i, 1);
             gdn::mbar_init(drain_bar + i, 1);
         }
         gdn::mbar_init(&q_bar, C::kRowWarps);
@@ -358,11 +355,13 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     // ---- the schedule: units of all sequences, cut into equal shares ------------
     const int per = (a.S + kThreads - 1) / kThreads;
     long long mine = 0;
+    Seq q0{0, 0, 0};  // the thread's first sequence (its only one up to kThreads of them)
     for (int k = 0; k < per; ++k) {
         const int s = tid * per + k;
         if (s >= a.S) break;
         int err;
         const Seq q = checked(a, s, load_raw(a, s), &err);
+        if (k == 0) q0 = q;
         if (err && blockIdx.x == 0) gdn::record_status(a.status, err);
         mine += head_units(q, a.R) * a.Hkv;
     }
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 long long x = t0 - before;
                 for (int k = 0; k < per; ++k) {
                     const int s = tid * per + k;
-                    const Seq q = checked(a, s, load_raw(a, s));
+                    const Seq q = k == 0 ? q0 : checked(a, s, load_raw(a, s));
                     const long long ht = head_units(q, a.R);
                     if (x >= ht * a.Hkv) {
                         x -= ht * a.Hkv;
@@ -406,7 +405,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         if (units_before(q, mid, a.R) <= x) lo = mid;
                         else hi = mid;
                     }
-                    start_s = Start{s, h, lo, int(x - units_before(q, lo, a.R)), t1 - t0};
+                    start_s = Start{q, s, h, lo, int(x - units_before(q, lo, a.R)), t1 - t0};
                     break;
                 }
             }
@@ -580,7 +579,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         if (elect_one()) gdn::mma_commit(drain_bar + (is_s ? 0 : 1));
         __syncwarp();
         gdn::mbar_wait_bounded(drain_bar + (is_s ? 0 : 1), 0);
-    } else if (warp >= kClean0) {
+    } else if (warp == C::kClean) {
         // ---- values of tiles that not every row sees whole ----------------------------
         long long loads = 0;  // ring position of the segment's first load
         uint32_t seg = 0, masked = 0;
@@ -588,7 +587,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         // the exponents of two values, and their lowest bits
         constexpr uint32_t kExp2 = std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
         constexpr uint32_t kLow2 = std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u;
-        const int ct = tid - kClean0 * 32, v_rows = v_box_rows(a.pl.shift);
+        const int v_rows = v_box_rows(a.pl.shift);
         while (ok && walk.next(g)) {
             const int n = g.tile1 - g.tile0;
             uint32_t bits[4] = {0, 0, 0, 0};
@@ -601,14 +600,14 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 if (!ok) break;
                 const int r0 = max(0, g.safe - t * TK);  // rows (positions) that some rows do not see
                 unsigned char *vt = tiles + size_t(stage) * C::kTile;
-                constexpr int kRowPieces = C::kChunks * 8, kStep = 32 * C::kCleanWarps;  // 16-byte pieces
+                constexpr int kRowPieces = C::kChunks * 8, kStep = 32;  // 16-byte pieces
                 auto piece = [&](int u) {
                     const int r = r0 + u / kRowPieces, c16 = u % kRowPieces;
                     return reinterpret_cast<uint4 *>(vt + v_place<C>(v_rows, r) + (c16 >> 3) * (v_rows * 128) +
                                                      (c16 & 7) * 16);
                 };
                 const int some = min(max(g.limit - t * TK - r0, 0), TK - r0) * kRowPieces;  // seen by some rows
-                for (int u0 = ct; u0 < some; u0 += 8 * kStep) {
+                for (int u0 = lane; u0 < some; u0 += 8 * kStep) {
                     uint4 v[8];
                     uint32_t any = 0;  // the top bit of a half is set where its exponent is all ones
 #pragma unroll
@@ -639,13 +638,13 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         }
                     }
                 }
-                for (int u = some + ct; u < (TK - r0) * kRowPieces; u += kStep) *piece(u) = make_uint4(0, 0, 0, 0);
+                for (int u = some + lane; u < (TK - r0) * kRowPieces; u += kStep) *piece(u) = make_uint4(0, 0, 0, 0);
                 gdn::fence_proxy_async_smem();
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     bits[i] = __reduce_or_sync(full, bits[i]);
-                    if (lane == i) nf[warp - kClean0][seg % kNfBufs][i] = bits[i];
+                    if (lane == i) nf[seg % kNfBufs][i] = bits[i];
                 }
                 __syncwarp();
                 if (lane == 0) arrive(clean_bar + (mk & 1));
@@ -675,19 +674,27 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             if (live_warp) {
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
                                                                    (int64_t(g.q.n0) + i) * a.q_stride + int64_t(hd) * D);
+                constexpr int kAhead = C::kStreams == 2 ? 1 : 2;  // chunks whose loads go out before the first is waited for
 #pragma unroll
-                for (int cc = 0; cc < C::kChunks; ++cc) {
-                    if (C::kStreams == 2 && (cc & 1) != stream) continue;
-                    uint32_t q[32];
+                for (int z0 = 0; z0 < (C::kChunks + C::kStreams - 1) / C::kStreams; z0 += kAhead) {
+                    uint32_t q[kAhead][32];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint4 v = live ? src[8 * cc + k] : make_uint4(0, 0, 0, 0);
-                        q[4 * k] = v.x;
-                        q[4 * k + 1] = v.y;
-                        q[4 * k + 2] = v.z;
-                        q[4 * k + 3] = v.w;
+                    for (int z = 0; z < kAhead; ++z) {
+                        const int cc = (z0 + z) * C::kStreams + (C::kStreams == 2 ? stream : 0);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint4 v = live && cc < C::kChunks ? src[8 * cc + k] : make_uint4(0, 0, 0, 0);
+                            q[z][4 * k] = v.x;
+                            q[z][4 * k + 1] = v.y;
+                            q[z][4 * k + 2] = v.z;
+                            q[z][4 * k + 3] = v.w;
+                        }
                     }
-                    tmem_st32(trow + C::kQ + 32 * cc, q);
+#pragma unroll
+                    for (int z = 0; z < kAhead; ++z) {
+                        const int cc = (z0 + z) * C::kStreams + (C::kStreams == 2 ? stream : 0);
+                        if (cc < C::kChunks) tmem_st32(trow + C::kQ + 32 * cc, q[z]);
+                    }
                 }
                 tmem_wait_st();
             }
@@ -846,8 +853,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             if (g.tile1 * TK > g.safe) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    bits[k] = *reinterpret_cast<volatile uint32_t *>(&nf[0][seg % kNfBufs][k]) |
-                              *reinterpret_cast<volatile uint32_t *>(&nf[C::kCleanWarps - 1][seg % kNfBufs][k]);
+                    bits[k] = *reinterpret_cast<volatile uint32_t *>(&nf[seg % kNfBufs][k]);
                     odd |= bits[k] != 0;
                 }
             }
@@ -925,13 +931,23 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const att::Args a, 
     const int b = blockIdx.x;
     const int4 me = a.meta[2 * b + 1];
     if (me.x <= 0 || me.x > att::kRows) return;
-    int last = b + 1;  // the CTA with the item's end
-    while (last < ctas - 1 && a.meta[2 * last].x > 0 && !a.meta[2 * last].y) ++last;
+    int last = ctas;  // the CTA with the item's end, looked for 32 at a time
+    for (int k0 = b + 1; k0 < ctas && last == ctas; k0 += 32) {
+        const int k = k0 + (threadIdx.x & 31);
+        bool end = k == ctas - 1;
+        if (k < ctas) {
+            const int4 m = a.meta[2 * k];
+            end |= m.x <= 0 || m.y != 0;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, end);
+        if (hit) last = k0 + __ffs(hit) - 1;
+    }
     if (last >= ctas) return;
     const int rows = me.x;
     for (int u = blockIdx.y * 256 + threadIdx.x; u < rows * (D / 4); u += gridDim.y * 256) {
         const int row = u % rows, c4 = u / rows;
         float M = -INFINITY;
+#pragma unroll 8
         for (int k = b; k <= last; ++k)
             M = fmaxf(M, a.parts[(size_t(k) * 2 + (k == b)) * C::kPartFloats + row]);
         float l = 0.f;
