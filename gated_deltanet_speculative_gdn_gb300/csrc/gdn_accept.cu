@@ -17,8 +17,11 @@
 // borders, so p - c q is formed as an unevaluated pair of floats (Dekker's and
 // Knuth's error-free product and sum; c as a pair too) and summed as one: 2^-48
 // relative, at ~16 fp32 operations an element, where fp64 arithmetic would run at
-// 1/64 of that rate.  The scalars (c, W, Z, thresholds, coarse cumulative sums) are
-// pairs too: as fp64 they took 3,000 to 13,000 cycles between passes.
+// 1/64 of that rate.  A lane's sum is then rounded once to an integer multiple of
+// 2^-61 (the sums of a distribution stay below 2): from there on sums, their scans
+// and the threshold are 64-bit integers, exact in any order, at two instructions a
+// sum.  (As fp64, or as pairs, the reductions and scans of one warp between the
+// passes took longer than the passes.)  c, W and Z are pairs.
 //
 // Mapping.  A cluster of CTAs takes a sequence, each CTA a contiguous slice of
 // the vocabulary.  Thread 0 of every CTA walks the tree with the same numbers (so
@@ -32,6 +35,8 @@
 // It does not release its dependent kernel early: the commits read `accepted`
 // before their own wait.
 #include <cooperative_groups.h>
+
+#include <cstdint>
 
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
@@ -132,20 +137,23 @@ __device__ __forceinline__ void residual4(const Pass &ps, const int *out, int i,
 }
 __device__ __forceinline__ float4 vec(const float *row, int i) { return __ldg(reinterpret_cast<const float4 *>(row) + i); }
 
-// Sum over the warp (lane 0's result is the one that is used).
-__device__ __forceinline__ Pair warp_sum(Pair v) {
+// Sums in units of 2^-61.
+typedef long long Fix;
+constexpr float kFix = 2305843009213693952.0f;
+__device__ __forceinline__ Fix to_fix(const Pair &v) { return __float2ll_rn(v.h * kFix) + __float2ll_rn(v.l * kFix); }
+__device__ __forceinline__ Pair to_pair(Fix v) {
+    const float h = __ll2float_rn(v);
+    return normal(h * (1.0f / kFix), __ll2float_rn(v - __float2ll_rn(h)) * (1.0f / kFix));
+}
+__device__ __forceinline__ Fix warp_sum(Fix v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Pair w = {__shfl_down_sync(0xffffffffu, v.h, o), __shfl_down_sync(0xffffffffu, v.l, o)};
-        add(v, w);
-    }
-    return normal(v.h, v.l);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// Sum of vectors [lo, hi) of the row, lanes side by side (lane 0's result): four vectors a lane are on
-// their way at a time.
+// Sum of vectors [lo, hi) of the row, lanes side by side: four vectors a lane are on their way at a time.
 template <bool kQ>
-__device__ __forceinline__ Pair sum_range_t(const Pass &ps, const int *out, int lo, int hi, int V) {
+__device__ __forceinline__ Fix sum_range_t(const Pass &ps, const int *out, int lo, int hi, int V) {
     constexpr int U = 4;
     Pair acc = {0.f, 0.f};
     for (int i0 = lo + int(threadIdx.x & 31); i0 < hi; i0 += 32 * U) {
@@ -166,49 +174,41 @@ __device__ __forceinline__ Pair sum_range_t(const Pass &ps, const int *out, int 
             for (int e = 0; e < 4; ++e) add(acc, r[e]);
         }
     }
-    return warp_sum(acc);
+    return warp_sum(to_fix(acc));
 }
-__device__ __forceinline__ Pair sum_range(const Pass &ps, const int *out, int lo, int hi, int V) {
+__device__ __forceinline__ Fix sum_range(const Pass &ps, const int *out, int lo, int hi, int V) {
     return ps.q ? sum_range_t<true>(ps, out, lo, hi, V) : sum_range_t<false>(ps, out, lo, hi, V);
 }
 
-// Warp-collective: the first of `count` consecutive parts (lane k holds part k's
-// sum) whose cumulative sum, from b on, passes thr; b becomes the sum before it.
-// When none does (rounding at the very end, or no distribution) the last part
-// that is not empty, and thr becomes infinite, so that finer selections take the
-// last one too.
-__device__ __forceinline__ int select_part(Pair v, int count, Pair &b, Pair &thr) {
+// Warp-collective: the first of the parts (lane k holds part k's sum, 0 past the
+// last) whose cumulative sum, from b on, passes thr; b becomes the sum before it.
+// When none does (u_next at 1, or a row that is no distribution) the last part that
+// is not empty, and thr becomes the largest, so that finer selections take the last
+// one too.
+__device__ __forceinline__ int select_part(Fix v, Fix &b, Fix &thr) {
     const int lane = threadIdx.x & 31;
-    if (lane >= count) v = {0.f, 0.f};
-    Pair inc = v, exc = {0.f, 0.f};
+    Fix inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const Pair y = {__shfl_up_sync(0xffffffffu, inc.h, o), __shfl_up_sync(0xffffffffu, inc.l, o)};
-        if (lane >= o) inc = plus(inc, y);
+        const Fix y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
     }
-    exc = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
-    if (lane == 0) exc = {0.f, 0.f};
-    const unsigned hit = __ballot_sync(0xffffffffu, v.h > 0.f && less(thr, plus(b, inc)));
-    const unsigned some = __ballot_sync(0xffffffffu, v.h > 0.f);
-    int k;
-    if (hit) {
-        k = __ffs(hit) - 1;
-    } else {
-        k = some ? 31 - __clz(some) : 0;
-        thr = {INFINITY, 0.f};
-    }
-    b = plus(b, {__shfl_sync(0xffffffffu, exc.h, k), __shfl_sync(0xffffffffu, exc.l, k)});
+    const unsigned hit = __ballot_sync(0xffffffffu, v > 0 && b + inc > thr);
+    const unsigned some = __ballot_sync(0xffffffffu, v > 0);
+    const int k = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : 0;
+    if (!hit) thr = INT64_MAX;
+    b += __shfl_sync(0xffffffffu, inc - v, k);
     return k;
 }
 
 __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs a) {
-    __shared__ Pair warp_tot[kWarpsA];
-    __shared__ Pair cta_tot[2][kMaxCluster];  // [pass parity][rank], written by every CTA of the cluster
+    __shared__ Fix warp_tot[kWarpsA];
+    __shared__ Fix cta_tot[2][kMaxCluster];  // [pass parity][rank], written by every CTA of the cluster
     __shared__ int par[gdn::kMaxSeqNodes], tok[gdn::kMaxSeqNodes], out[gdn::kMaxSeqNodes];
     __shared__ float pc[gdn::kMaxSeqNodes], qc[gdn::kMaxSeqNodes], uc[gdn::kMaxSeqNodes];  // p, q at the parent's row
     __shared__ Pass pass_s;
     __shared__ int err_s, step_s;              // what follows the pass: another, the selection, nothing
-    __shared__ Pair base_s, thr_s;             // of the selection
+    __shared__ Fix base_s, thr_s;              // of the selection
     __shared__ int lo_s, hi_s;
     cg::cluster_group cl = cg::this_cluster();
     const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
@@ -307,33 +307,29 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
         }
         __syncthreads();
         ps = pass_s;
-        const Pair wt = sum_range(ps, out, w0, w1, a.V);
+        const Fix wt = sum_range(ps, out, w0, w1, a.V);
         if (lane == 0) warp_tot[warp] = wt;
         __syncthreads();
         if (warp == 0) {
-            Pair v = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
-            v = warp_sum(v);
-            v.h = __shfl_sync(0xffffffffu, v.h, 0);
-            v.l = __shfl_sync(0xffffffffu, v.l, 0);
+            const Fix v = warp_sum(lane < kWarpsA ? warp_tot[lane] : 0);
             if (lane < C) cl.map_shared_rank(&cta_tot[0][0], lane)[parity * kMaxCluster + rank] = v;
         }
         cl.sync();
         if (warp == 0) {
-            const Pair mine = lane < C ? cta_tot[parity][lane] : Pair{0.f, 0.f};
-            const Pair sum = warp_sum(mine);
-            const Pair total = {__shfl_sync(0xffffffffu, sum.h, 0), __shfl_sync(0xffffffffu, sum.l, 0)};
+            const Fix mine = lane < C ? cta_tot[parity][lane] : 0;
+            const Fix total = warp_sum(mine);
             int step = 0;
             if (ps.last) {
-                const bool empty = !(total.h > 0.f) && !__shfl_sync(0xffffffffu, int(fallback), 0);
-                if (empty) {
+                if (total <= 0 && !__shfl_sync(0xffffffffu, int(fallback), 0)) {
                     fallback = true;  // nothing is left: the target's own row
                 } else {
-                    Pair b = {0.f, 0.f}, thr = times({un, 0.f}, total);
-                    const bool owner = select_part(mine, C, b, thr) == rank;
+                    // cumulative sums pass u total exactly where they pass its floor; u in units of 2^-63
+                    const unsigned long long u63 = __float2ull_rn(fminf(fmaxf(un, 0.f), 1.f) * 9223372036854775808.0f);
+                    Fix b = 0, thr = Fix(__umul64hi(u63, static_cast<unsigned long long>(max(total, Fix(0))) << 1));
+                    const bool owner = select_part(mine, b, thr) == rank;
                     step = owner ? 2 : 1;
                     if (owner) {
-                        const Pair w = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
-                        const int k = select_part(w, kWarpsA, b, thr);
+                        const int k = select_part(lane < kWarpsA ? warp_tot[lane] : 0, b, thr);
                         if (lane == 0) {
                             base_s = b;
                             thr_s = thr;
@@ -344,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
                 }
             }
             if (lane == 0) {
-                W = total;
+                if (!step) W = to_pair(total);
                 step_s = step;
             }
         }
@@ -361,13 +357,12 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
     if (step_s != 2) return;
     while (hi_s - lo_s > 32) {
         const int lo = lo_s, hi = hi_s, part = (hi - lo + kWarpsA - 1) / kWarpsA;
-        const Pair wt = sum_range(ps, out, min(hi, lo + warp * part), min(hi, lo + (warp + 1) * part), a.V);
+        const Fix wt = sum_range(ps, out, min(hi, lo + warp * part), min(hi, lo + (warp + 1) * part), a.V);
         if (lane == 0) warp_tot[warp] = wt;
         __syncthreads();
         if (warp == 0) {
-            const Pair w = lane < kWarpsA ? warp_tot[lane] : Pair{0.f, 0.f};
-            Pair b = base_s, thr = thr_s;
-            const int k = select_part(w, kWarpsA, b, thr);
+            Fix b = base_s, thr = thr_s;
+            const int k = select_part(lane < kWarpsA ? warp_tot[lane] : 0, b, thr);
             if (lane == 0) {
                 base_s = b;
                 thr_s = thr;
@@ -384,22 +379,20 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
             if (ps.q) residual4<true>(ps, out, i, a.V, vec(ps.p, i), vec(ps.q, i), r);
             else residual4<false>(ps, out, i, a.V, vec(ps.p, i), make_float4(0.f, 0.f, 0.f, 0.f), r);
         }
-        Pair e[4], run = {0.f, 0.f};
+        Fix e[4], run = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            run = plus(run, r[k]);
+            run += to_fix(r[k]);
             e[k] = run;
         }
-        Pair b = base_s, thr = thr_s;
-        const int src = select_part(run, 32, b, thr);
+        Fix b = base_s, thr = thr_s;
+        const int src = select_part(run, b, thr);
         if (lane == src) {
-            int k = 0;
-#pragma unroll
-            for (int z = 2; z >= 0; --z)  // the first that passes the threshold, else the last that is not 0
-                if (r[z + 1].h > 0.f && k == 0) k = z + 1;
+            // the first that passes the threshold, else the last that is not 0
+            int k = e[3] > e[2] ? 3 : e[2] > e[1] ? 2 : e[1] > e[0] ? 1 : 0;
 #pragma unroll
             for (int z = 3; z >= 0; --z)
-                if (r[z].h > 0.f && less(thr, plus(b, e[z]))) k = z;
+                if (e[z] > (z ? e[z - 1] : 0) && b + e[z] > thr) k = z;
             a.next_token[s] = min(max(4 * i + k, 0), a.V - 1);
         }
     }
@@ -436,9 +429,11 @@ extern "C" int gdn_tree_accept(const gdn_dims *dims, int vocab, const float *p, 
 
     AcceptArgs a{p, q, p_stride, q_stride, tokens, parents, node_off, u, u_next, accepted, next_token, n_accepted,
                  status, int(S), int(N), vocab, dims->max_seq_nodes, replacement};
-    // a CTA's slice is at least 2048 elements (one vector a thread)
+    // A cluster as large as leaves every CTA resident at once (two per SM) and a slice of one vector a
+    // thread: 64 sequences of 131072 tokens take 39 us with 4 CTAs each and 48 us with 8, whose second wave
+    // runs alone; one sequence 13.7 us with 8.
     int C = 1;
-    while (C < kMaxCluster && int64_t(vocab) / (2 * C) >= 2048) C *= 2;
+    while (C < kMaxCluster && int64_t(vocab) / (2 * C) >= 2048 && S * 2 * C <= 304) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(S * C));
     cfg.blockDim = dim3(kThreads);

@@ -110,7 +110,7 @@ struct Args {
 };
 
 // sum_{j < n} floor((a j + b) / m), a, b >= 0, m > 0: by Euclid's steps on (a, m)
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+__device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
     long long r = 0;
     while (n > 0) {
         r += (a / m) * (n * (n - 1) / 2) + (b / m) * n;

@@ -20,6 +20,7 @@
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kBatch = 4;  // rows of a warp in flight
 
 // f mod 2 pi, f finite and >= 0, as a 64-bit fraction of a turn.  f = m 2^(e - 52) with a
 // 53-bit m; f / (2 pi) 2^64 = m R 2^(e - 52) with R = 2^64 / (2 pi).
@@ -56,7 +57,7 @@ struct RopeArgs {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 6) rope_append_kernel(const RopeArgs a) {
     constexpr int LH = D / 8, RW = 32 / LH;  // lanes of a row, rows of a warp
     const unsigned full = 0xffffffffu;
     gdn::grid_dep_launch();
@@ -71,17 +72,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs
     }
     const int n = int(wid / a.shares), share = int(wid % a.shares);
     if (n >= a.N) return;
-    const int rows = a.Hq + 2 * a.Hkv, slots = (rows + RW - 1) / RW;
     const int col = 8 * l;
-    auto load_row = [&](int slot) {  // q heads, then k heads, then v heads
-        const int r = slot * RW + sub;
-        if (r >= rows) return make_uint4(0, 0, 0, 0);
-        const T *src = r < a.Hq ? static_cast<const T *>(a.q) + n * a.q_stride + int64_t(r) * D
-                       : r < a.Hq + a.Hkv ? static_cast<const T *>(a.k) + n * a.k_stride + int64_t(r - a.Hq) * D
-                                          : static_cast<const T *>(a.v) + n * a.v_stride + int64_t(r - a.Hq - a.Hkv) * D;
-        return *reinterpret_cast<const uint4 *>(src + col);
-    };
-    uint4 next = load_row(share);  // its latency passes under the angles'
     const int s = gdn::find_sequence(a.node_off, a.S, n);
     const int n0 = a.node_off[s], ctx = a.ctx_len[s];
     const int i = n - n0;
@@ -100,91 +91,107 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeArgs
         if (err && lane == 0) gdn::record_status(a.status, err);
     }
 
-    // the lane's cosines and sines: element e of the lane is column 8 l + e
+    // Each frequency once a warp: lane p % 32 forms pair p's cosine and sine, then every lane fetches those
+    // of its eight elements (element e is column 8 l + e).
     const int half = a.rot / 2;
-    const bool turned = col < a.rot;
-    const bool upper = !a.interleaved && col >= half;  // the lane holds second elements of pairs
     float cs[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         cs[e] = 1.f;
         sn[e] = 0.f;
     }
-    if (turned) {
-        const int pairs = a.interleaved ? 4 : 8;
-        const int p0 = a.interleaved ? col / 2 : (upper ? col - half : col);
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (e >= pairs) break;
-            int ax = a.axis ? a.axis[p0 + e] : 0;
+    const bool turned = col < a.rot;
+    const bool upper = !a.interleaved && col >= half;  // the lane holds second elements of pairs
+    const int p0 = a.interleaved ? col / 2 : (upper ? col - half : col);
+    bool bad = false;
+    for (int k = 0; 32 * k < half; ++k) {
+        const int p = 32 * k + lane;
+        float c = 1.f, sv = 0.f;
+        if (p < half) {
+            int ax = a.axis ? a.axis[p] : 0;
             if (ax < 0 || ax >= a.n_axes) {
                 bad = true;
                 ax = 0;
             }
             const unsigned long long turns =
                 static_cast<unsigned long long>(static_cast<long long>(a.pos[int64_t(n) * a.n_axes + ax])) *
-                turn_fraction(a.inv_freq[p0 + e]);
+                turn_fraction(a.inv_freq[p]);
             // a signed 32-bit fraction of a turn, in units of half turns
-            sincospif(float(int(turns >> 32)) * (1.0f / 2147483648.0f), &sn[e], &cs[e]);
+            sincospif(float(int(turns >> 32)) * (1.0f / 2147483648.0f), &sv, &c);
         }
-        if (bad) gdn::record_status(a.status, GDN_DEV_BAD_AXIS);
-        if (a.interleaved) {  // pair p of the lane: elements 2 p, 2 p + 1
 #pragma unroll
-            for (int e = 7; e >= 0; --e) {
-                cs[e] = cs[e / 2];
-                sn[e] = sn[e / 2];
+        for (int e = 0; e < 8; ++e) {
+            const int q = p0 + (a.interleaved ? e / 2 : e);
+            const float fc = __shfl_sync(full, c, q & 31), fs = __shfl_sync(full, sv, q & 31);
+            if (turned && q >> 5 == k) {
+                cs[e] = fc;
+                sn[e] = fs;
             }
         }
     }
+    if (bad) gdn::record_status(a.status, GDN_DEV_BAD_AXIS);
+    // the first of a pair takes the other's share away
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (a.interleaved ? (e & 1) == 0 : !upper) sn[e] = -sn[e];
     const int hop = a.rot / 16;  // lanes between the halves of a pair
     const int partner = turned && !a.interleaved ? (upper ? lane - hop : lane + hop) : lane;
-    float qw[8], kw[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        qw[e] = a.qw ? a.qw[col + e] : 1.f;
-        kw[e] = a.kw ? a.kw[col + e] : 1.f;
-    }
 
-    for (int slot = share; slot < slots; slot += a.shares) {
-        const int r = slot * RW + sub;  // q heads, then k heads, then v heads
-        const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv, live = r < rows;
-        const int h = is_q ? r : is_k ? r - a.Hq : r - a.Hq - a.Hkv;
-        const uint4 raw = next;
-        if (slot + a.shares < slots) next = load_row(slot + a.shares);
-        float y[8], z[8];
-        gdn::unpack8<T>(raw, y);
-        const bool norm = live && ((is_q && a.qw) || (is_k && a.kw));
-        float ss = 0.f;
+    // The rows of one kind, RW heads at a time, this warp's slots of them: kBatch rows are in flight.
+    // first: the kind's first slot in the token's numbering (q, k, v).
+    auto rows_of = [&](const T *src, int heads, int first, const float *w, bool turn, T *dst, int64_t dst_head) {
+        const int slots = (heads + RW - 1) / RW;
+        int j = share - first % a.shares;
+        if (j < 0) j += a.shares;
+        if (j >= slots) return;
+        float wv[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+        for (int e = 0; e < 8; ++e) wv[e] = w ? w[col + e] : 1.f;
+        for (; j < slots; j += kBatch * a.shares) {
+            uint4 raw[kBatch];
 #pragma unroll
-        for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(full, ss, o);
-        if (norm) {
-            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+            for (int z = 0; z < kBatch; ++z) {
+                const int r = (j + z * a.shares) * RW + sub;
+                raw[z] = r < heads ? *reinterpret_cast<const uint4 *>(src + r * D + col) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * (is_q ? qw[e] : kw[e]);
-        }
-        if (a.interleaved) {
+            for (int z = 0; z < kBatch; ++z) {
+                const int r = (j + z * a.shares) * RW + sub;
+                uint4 out = raw[z];
+                if (turn) {
+                    float y[8], x[8];
+                    gdn::unpack8<T>(raw[z], y);
+                    if (w) {
+                        float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = (e & 1) ? y[e] * cs[e] + y[e - 1] * sn[e] : y[e] * cs[e] - y[e + 1] * sn[e];
-        } else {
+                        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float other = __shfl_sync(full, y[e], partner);
-                z[e] = upper ? y[e] * cs[e] + other * sn[e] : y[e] * cs[e] - other * sn[e];
+                        for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(full, ss, o);
+                        const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * wv[e];
+                    }
+                    if (a.interleaved) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = fmaf(y[e ^ 1], sn[e], y[e] * cs[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = fmaf(__shfl_sync(full, y[e], partner), sn[e], y[e] * cs[e]);
+                    }
+                    // untouched values are copied, not converted: a NaN keeps its bits
+                    if (turned || w) out = gdn::pack8<T>(x);
+                }
+                if (r < heads && dst) *reinterpret_cast<uint4 *>(dst + r * dst_head + col) = out;
             }
         }
-        if (!live) continue;
-        // untouched values are copied, not converted: a NaN keeps its bits
-        const uint4 out = (is_q || is_k) && (turned || norm) ? gdn::pack8<T>(z) : raw;
-        if (is_q) {
-            *reinterpret_cast<uint4 *>(static_cast<T *>(a.qo) + n * a.qo_stride + int64_t(h) * D + col) = out;
-        } else if (place >= 0) {
-            T *pool = static_cast<T *>(is_k ? a.k_pool : a.v_pool);
-            *reinterpret_cast<uint4 *>(pool + place + int64_t(h) * a.pl.head_stride + col) = out;
-        }
-    }
+    };
+    const int sq = (a.Hq + RW - 1) / RW, sk = (a.Hkv + RW - 1) / RW;
+    rows_of(static_cast<const T *>(a.q) + n * a.q_stride, a.Hq, 0, a.qw, a.rot > 0 || a.qw,
+            static_cast<T *>(a.qo) + n * a.qo_stride, D);
+    rows_of(static_cast<const T *>(a.k) + n * a.k_stride, a.Hkv, sq, a.kw, a.rot > 0 || a.kw,
+            place >= 0 ? static_cast<T *>(a.k_pool) + place : nullptr, a.pl.head_stride);
+    rows_of(static_cast<const T *>(a.v) + n * a.v_stride, a.Hkv, sq + sk, nullptr, false,
+            place >= 0 ? static_cast<T *>(a.v_pool) + place : nullptr, a.pl.head_stride);
 }
 
 template <typename T>
@@ -244,7 +251,7 @@ extern "C" int gdn_rope_append(const gdn_attn_dims *dims, const void *q, int64_t
     // a token's rows are shared by as many warps as it takes to fill the GPU
     // when there are few tokens; a warp with all rows of a token forms the
     // angles once for all of them
-    const int64_t slots = (Hq + 2 * Hkv + 256 / D - 1) / (256 / D);
+    const int64_t rw = 256 / D, slots = (Hq + rw - 1) / rw + 2 * ((Hkv + rw - 1) / rw);
     const int64_t want = 152 * 24;
     const int64_t shares = N >= want ? 1 : (want / N < slots ? want / N : slots);
     RopeArgs a{q, k, v, q_stride, k_stride, v_stride, q_out_stride, q_norm_w, k_norm_w, eps, pos, inv_freq, axis,
