@@ -386,7 +386,11 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         const long long active = min((long long)gridDim.x, total);
         const int b = blockIdx.x;
         if (b < active) {
-            const long long t0 = total * b / active, t1 = total * (b + 1) / active;
+            // (32-bit division where it does: the 64-bit one is a call)
+            const bool small = total < (1 << 23);  // times at most 2^8 CTAs and below 2^31
+            const long long t0 = small && active <= 256 ? unsigned(total) * unsigned(b) / unsigned(active) : total * b / active;
+            const long long t1 =
+                small && active <= 256 ? unsigned(total) * unsigned(b + 1) / unsigned(active) : total * (b + 1) / active;
             if (mine > 0 && t0 >= before && t0 < before + mine) {  // one thread of the CTA
                 long long x = t0 - before;
                 for (int k = 0; k < per; ++k) {
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         x -= ht * a.Hkv;
                         continue;
                     }
-                    const int h = int(x / ht);
+                    const int h = small ? int(unsigned(x) / unsigned(ht)) : int(x / ht);
                     x -= h * ht;
                     int lo = 0, hi = (q.n + a.R - 1) / a.R;  // the last row tile with units_before <= x
                     while (hi - lo > 1) {
@@ -921,19 +925,41 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     if (warp == C::kMmaS) gdn::tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of items that more than one CTA worked on: block (b, y) takes
-// the item that begins in CTA b and goes on in b + 1, ..., in that order.
+// Joins the parts of items that more than one CTA worked on: block (b, y) takes its
+// share of the item that begins in CTA b and goes on in b + 1, ...  A unit is four
+// columns of a row.  Few parts: a thread takes a unit and all its parts.  Many (one
+// long sequence spread over the GPU): the block's warps take the parts in turn for 32
+// units at a time and their eight sums are joined in order.  Bound by latency; every
+// thread has the loads of four parts under way (one at a time took 24 us for 126 parts).
+struct Joined {
+    float m, l;
+    float4 o;
+};
+__device__ __forceinline__ void join(Joined &a, const Joined &b) {
+    if (b.m == -INFINITY) return;  // nothing seen in that part
+    const float M = fmaxf(a.m, b.m);
+    const float f = a.m == -INFINITY ? 0.f : att::exp2_approx(a.m - M), w = att::exp2_approx(b.m - M);
+    const bool first = a.m == -INFINITY;
+    a.m = M;
+    a.l = fmaf(w, b.l, first ? 0.f : f * a.l);
+    a.o.x = fmaf(w, b.o.x, first ? 0.f : f * a.o.x);
+    a.o.y = fmaf(w, b.o.y, first ? 0.f : f * a.o.y);
+    a.o.z = fmaf(w, b.o.z, first ? 0.f : f * a.o.z);
+    a.o.w = fmaf(w, b.o.w, first ? 0.f : f * a.o.w);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(const att::Args a, int ctas) {
     using C = att::Cfg<D>;
+    __shared__ Joined sums[8][32];
     gdn::grid_dep_launch();
     gdn::grid_dep_wait();
-    const int b = blockIdx.x;
+    const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int4 me = a.meta[2 * b + 1];
     if (me.x <= 0 || me.x > att::kRows) return;
     int last = ctas;  // the CTA with the item's end, looked for 32 at a time
     for (int k0 = b + 1; k0 < ctas && last == ctas; k0 += 32) {
-        const int k = k0 + (threadIdx.x & 31);
+        const int k = k0 + lane;
         bool end = k == ctas - 1;
         if (k < ctas) {
             const int4 m = a.meta[2 * k];
@@ -943,32 +969,49 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const att::Args a, 
         if (hit) last = k0 + __ffs(hit) - 1;
     }
     if (last >= ctas) return;
-    const int rows = me.x;
-    for (int u = blockIdx.y * 256 + threadIdx.x; u < rows * (D / 4); u += gridDim.y * 256) {
+    const int rows = me.x, units = rows * (D / 4), parts = last - b + 1;
+    // unit u over parts b + k0, b + k0 + step, ...
+    auto gather = [&](int u, int k0, int step) {
         const int row = u % rows, c4 = u / rows;
-        float M = -INFINITY;
-#pragma unroll 8
-        for (int k = b; k <= last; ++k)
-            M = fmaxf(M, a.parts[(size_t(k) * 2 + (k == b)) * C::kPartFloats + row]);
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = b; k <= last; ++k) {
-            const float *part = a.parts + (size_t(k) * 2 + (k == b)) * C::kPartFloats;
-            const float m = part[row], pl = part[att::kRows + row];
-            const float4 v = *reinterpret_cast<const float4 *>(part + 2 * att::kRows + (size_t(c4) * att::kRows + row) * 4);
-            if (m == -INFINITY) continue;  // nothing seen in this part
-            const float w = att::exp2_approx(m - M);
-            l = fmaf(w, pl, l);
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
+        Joined acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int k = k0; k < parts; k += 4 * step) {
+            Joined p[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int kk = min(k + z * step, parts - 1) + b;
+                const float *part = a.parts + (size_t(kk) * 2 + (kk == b)) * C::kPartFloats;
+                p[z].m = part[row];
+                p[z].l = part[att::kRows + row];
+                p[z].o = *reinterpret_cast<const float4 *>(part + 2 * att::kRows + (size_t(c4) * att::kRows + row) * 4);
+            }
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                if (k + z * step < parts) join(acc, p[z]);
         }
-        const float inv = 1.f / l;
+        return acc;
+    };
+    auto store = [&](int u, const Joined &r) {
+        const int row = u % rows, c4 = u / rows;
+        const float inv = 1.f / r.l;
         T *out = static_cast<T *>(a.o) + ((int64_t(me.z) + row / a.G) * a.Hq + me.w * a.G + row % a.G) * D + 4 * c4;
-        *reinterpret_cast<uint2 *>(out) =
-            make_uint2(gdn::Half2<T>::pack(o.x * inv, o.y * inv), gdn::Half2<T>::pack(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2 *>(out) = make_uint2(gdn::Half2<T>::pack(r.o.x * inv, r.o.y * inv),
+                                                     gdn::Half2<T>::pack(r.o.z * inv, r.o.w * inv));
+    };
+    if (parts <= 4) {
+        for (int u = blockIdx.y * 256 + threadIdx.x; u < units; u += gridDim.y * 256) store(u, gather(u, 0, 1));
+        return;
+    }
+    for (int u0 = blockIdx.y * 32; u0 < units; u0 += gridDim.y * 32) {
+        const int u = u0 + lane;
+        sums[warp][lane] = gather(min(u, units - 1), warp, 8);
+        __syncthreads();
+        if (warp == 0 && u < units) {
+            Joined r = sums[0][lane];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) join(r, sums[w][lane]);
+            store(u, r);
+        }
+        __syncthreads();
     }
 }
 
@@ -993,7 +1036,9 @@ int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *wor
         return GDN_ERR_LAUNCH;
     if (gdn::launch_pdl(k, dim3(unsigned(ctas)), dim3(C::kThreads), C::kSmem, st, kmap, vmap, a) != cudaSuccess)
         return GDN_ERR_LAUNCH;
-    return gdn::launch_pdl(attention_join_kernel<T, D>, dim3(unsigned(ctas), 8), dim3(256), 0, st, a, ctas) == cudaSuccess
+    const int units = a.G * (dims->max_seq_tokens < a.R ? dims->max_seq_tokens : a.R) * (D / 4);  // of a part, at most
+    const unsigned y = units >= 16 * 32 ? 16 : unsigned(units + 31) / 32;
+    return gdn::launch_pdl(attention_join_kernel<T, D>, dim3(unsigned(ctas), y), dim3(256), 0, st, a, ctas) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_LAUNCH;
 }
