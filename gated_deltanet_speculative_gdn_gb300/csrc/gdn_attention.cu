@@ -4,9 +4,14 @@
 //
 // Mathematics.  One pass over the positions with a running reference m and sum l:
 //     p_x = 2^(c s_x - m),  l += p_x,  O += p_x v_x,   c = scale log2(e)
-// where m is the running maximum when it was last moved.  It is moved (l and O
-// scaled by 2^(m - m')) only when the maximum has grown by more than 2^8: until
-// then p stays below 2^8, which costs no precision in a floating type.  Parts of a
+// where m is the largest c s of the first tile that the row sees, or of the tile for
+// which it was last moved.  It is moved (l and O scaled by 2^(m - m')) only when p
+// would pass 2^8: until then p is in the range of either 16-bit type, and a scale costs
+// no precision in a floating type.  With one warpgroup (D = 256) the exponentials are
+// formed without a look at the maximum, which would stand before all of them in the
+// longest chain of the kernel; a tile whose p sum to more than 64 2^8 has its m moved
+// and its p formed again.  (With two, keeping the scores for that costs registers that
+// spill: 270 -> 330 us on the mixed chunks.)  Parts of a
 // row's positions are joined by the same rule: o = sum 2^(m_i - M) O_i / sum
 // 2^(m_i - M) l_i.
 //
@@ -56,6 +61,7 @@ namespace {
 namespace att {
 
 constexpr int kRows = 128;
+constexpr float kMoveAt = 8.f, kMoveAtSum = 256.f;  // m moves when a p passes 2^8, or a tile's sum 64 times that
 constexpr int TK = 64;       // positions of a tile
 constexpr int kItemUnits = 4; // what an item costs beside its tiles (Q in, results out), in tiles
 constexpr int kNfBufs = 16;  // the ring holds the values of 12 segments at most, and one may still be going out
@@ -285,6 +291,12 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *abort_flag = 1;
     return ok;
+}
+// Two waits in one, where both are mostly over.
+__device__ __forceinline__ bool wait_both(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, volatile int *abort_flag) {
+    const bool ok = gdn::mbar_try_wait(b0, p0) & gdn::mbar_try_wait(b1, p1);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    return wait_bar(b0, p0, abort_flag) && wait_bar(b1, p1, abort_flag);
 }
 // Which of the 32 positions from `base` on a row sees: all below `upto` (chain), or
 // all below ctx and the bits of `line` from there (tree).
@@ -732,7 +744,12 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             for (int k = C::kStreams == 2 ? int((tile ^ stream) & 1) : 0; k < n; k += C::kStreams, ++done) {
                 const long long it = tile + k;
                 const int t = g.tile0 + k, buf = int(it & 1), sb = C::s_buf(it);
-                ok = wait_bar(s_bar + sb, C::s_use(it) & 1, abort_flag);
+                // With one stream the place of P is awaited here too (the product of two tiles before has read
+                // it, and the wait is over as a rule); with two it is this warpgroup's last product's.
+                if (C::kStreams == 1 && it >= 2)
+                    ok = wait_both(s_bar + sb, C::s_use(it) & 1, pv_bar + buf, uint32_t((it >> 1) - 1) & 1, abort_flag);
+                else
+                    ok = wait_bar(s_bar + sb, C::s_use(it) & 1, abort_flag);
                 if (!ok) break;
                 float sv[2][32];
                 if (live_warp) {
@@ -753,65 +770,87 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                                 if (!((vis >> e) & 1)) sv[z][e] = -INFINITY;
                         }
                     }
-                    float mv[8];  // eight chains: few warps share a scheduler, so latency counts
+                    auto tile_max = [&] {
+                        float mv[8];  // eight chains: few warps share a scheduler, so latency counts
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mv[e] = -INFINITY;
+                        for (int e = 0; e < 8; ++e) mv[e] = -INFINITY;
 #pragma unroll
-                    for (int z = 0; z < 2; ++z)
+                        for (int z = 0; z < 2; ++z)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mv[e & 7] = fmaxf(mv[e & 7], sv[z][e]);
-                    const float mx = c * fmaxf(fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3])),
-                                               fmaxf(fmaxf(mv[4], mv[5]), fmaxf(mv[6], mv[7])));
-                    if (done == 0) {
-                        m = mx;
-                    } else {
-                        const bool move = mx > m + 8.f;
-                        if (__any_sync(full, move)) {
-                            // O may be scaled once this warpgroup's product before this one has added to it
-                            const long long pr = it - C::kStreams;
-                            ok = wait_bar(pv_bar + (pr & 1), uint32_t(pr >> 1) & 1, abort_flag);
-                            if (!ok) break;
-                            gdn::tc_fence_after_sync();
-                            const float f = move ? exp2_approx(m - mx) : 1.f;
-                            if (move) m = mx;
-                            l *= f;
-#pragma unroll 1
-                            for (int cc = 0; cc < D; cc += 32) {
-                                float v[32];
-                                uint32_t r[32];
-                                gdn::tmem_ld32(trow + C::kO + stream * D + cc, v);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(v[e] * f);
-                                tmem_st32(trow + C::kO + stream * D + cc, r);
-                            }
-                        }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet
-                    const uint64_t c2 = gdn::f2pack(c, c), mu2 = gdn::f2pack(-mu, -mu);
-                    uint64_t sum[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[e] = gdn::f2pack(0.f, 0.f);
+                            for (int e = 0; e < 32; ++e) mv[e & 7] = fmaxf(mv[e & 7], sv[z][e]);
+                        return c * fmaxf(fmaxf(fmaxf(mv[0], mv[1]), fmaxf(mv[2], mv[3])),
+                                         fmaxf(fmaxf(mv[4], mv[5]), fmaxf(mv[6], mv[7])));
+                    };
                     uint32_t r[32];
+                    auto weights = [&] {  // P of the tile; its sum
+                        const float mu = m == -INFINITY ? 0.f : m;  // a row that has seen nothing yet
+                        const uint64_t c2 = gdn::f2pack(c, c), mu2 = gdn::f2pack(-mu, -mu);
+                        uint64_t sum[4];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float *x = &sv[e >> 4][2 * (e & 15)];
-                        const float2 y = gdn::f2unpack(gdn::fma2(gdn::f2pack(x[0], x[1]), c2, mu2));
-                        const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
-                        sum[e & 3] = gdn::add2(sum[e & 3], gdn::f2pack(p0, p1));
-                        r[e] = gdn::Half2<T>::pack(p0, p1);
+                        for (int e = 0; e < 4; ++e) sum[e] = gdn::f2pack(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float *x = &sv[e >> 4][2 * (e & 15)];
+                            const float2 y = gdn::f2unpack(gdn::fma2(gdn::f2pack(x[0], x[1]), c2, mu2));
+                            const float p0 = exp2_approx(y.x), p1 = exp2_approx(y.y);
+                            sum[e & 3] = gdn::add2(sum[e & 3], gdn::f2pack(p0, p1));
+                            r[e] = gdn::Half2<T>::pack(p0, p1);
+                        }
+                        const float2 s2 = gdn::f2unpack(gdn::add2(gdn::add2(sum[0], sum[1]), gdn::add2(sum[2], sum[3])));
+                        return s2.x + s2.y;
+                    };
+                    // m moves to the tile's maximum where `move` says so; O may be scaled once this warpgroup's
+                    // product before this one has added to it
+                    auto move_to = [&](float mx, bool move) {
+                        const float f = move ? exp2_approx(m - mx) : 1.f;
+                        if (move) m = mx;
+                        l *= f;
+                        if (done == 0) return true;
+                        const long long pr = it - C::kStreams;
+                        if (!wait_bar(pv_bar + (pr & 1), uint32_t(pr >> 1) & 1, abort_flag)) return false;
+                        gdn::tc_fence_after_sync();
+#pragma unroll 1
+                        for (int cc = 0; cc < D; cc += 32) {
+                            float v[32];
+                            uint32_t o[32];
+                            gdn::tmem_ld32(trow + C::kO + stream * D + cc, v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(v[e] * f);
+                            tmem_st32(trow + C::kO + stream * D + cc, o);
+                        }
+                        return true;
+                    };
+                    if (C::kStreams == 2) {
+                        const float mx = tile_max();
+                        if (m == -INFINITY) m = mx;
+                        const bool move = mx > m + kMoveAt;
+                        if (__any_sync(full, move)) ok = move_to(mx, move);
+                        if (!ok) break;
+                        l += weights();
+                    } else {
+                        if (__any_sync(full, m == -INFINITY)) {  // the first positions that the row sees
+                            const float mx = tile_max();
+                            if (m == -INFINITY) m = mx;
+                        }
+                        float sum = weights();
+                        const bool move = sum > 64.f * kMoveAtSum;
+                        if (__any_sync(full, move)) {
+                            ok = move_to(tile_max(), move);
+                            if (!ok) break;
+                            sum = weights();
+                        }
+                        l += sum;
                     }
                     // the place of P: the product of two tiles before has read it
-                    if (it >= 2) {
+                    if (C::kStreams == 2 && it >= 2) {
                         ok = wait_bar(pv_bar + buf, uint32_t((it >> 1) - 1) & 1, abort_flag);
                         if (!ok) break;
                         gdn::tc_fence_after_sync();
                     }
                     tmem_st32(trow + C::kP + uint32_t(buf) * (TK / 2), r);
-                    const float2 s2 = gdn::f2unpack(gdn::add2(gdn::add2(sum[0], sum[1]), gdn::add2(sum[2], sum[3])));
-                    l += s2.x + s2.y;
                     tmem_wait_st();
                     gdn::tc_fence_before_sync();
-                } else if (it >= 2) {  // in step with the others, so that no phase is passed twice
+                } else if (C::kStreams == 2 && it >= 2) {  // in step with the others, so that no phase is passed twice
                     ok = wait_bar(pv_bar + buf, uint32_t((it >> 1) - 1) & 1, abort_flag);
                     if (!ok) break;
                 }

@@ -123,15 +123,16 @@ def test_attention_flat_and_peaked(std):
     check(Attn(cache, q, [700], [16], parents, dtype, d ** -0.5).out(), ref, A, big, dtype, d)
 
 
-def test_attention_rising_scores():
-    """Keys grow along the context, so every tile raises the maximum by much."""
-    dtype, d = torch.float16, 128
-    cache, q, _ = case(8, dtype, d, 8, 2, 16, "token", [600], [2], False)
+@pytest.mark.parametrize("name,d,hq,hkv", [("fp16", 128, 8, 2), ("bf16", 256, 16, 2), ("fp16", 256, 6, 3), ("bf16", 64, 4, 4)])
+@pytest.mark.parametrize("step", [0.02, 0.1])
+def test_attention_rising_scores(name, d, hq, hkv, step):
+    """Keys grow along the context, so the maximum rises from tile to tile, by a little or by much."""
+    dtype = R.DTYPES[name]
+    cache, q, _ = case(8, dtype, d, hq, hkv, 16, "token", [600], [2], False)
     for x in range(602):
-        cache.k[cache.index(0, x)] *= 0.02 * x
+        at = cache.index(0, x)
+        cache.k[at] = (cache.k[at].float() * step * x).abs().to(dtype)
     q = q.abs()
-    for x in range(602):
-        cache.k[cache.index(0, x)] = cache.k[cache.index(0, x)].abs()
     ref, A, big = R.attention(q.double(), cache, [600], [2], None, d ** -0.5)
     check(Attn(cache, q, [600], [2], None, dtype, d ** -0.5).out(), ref, A, big, dtype, d)
 
