@@ -42,9 +42,9 @@
 //           products: two warpgroups take alternate tiles, each with an O, m and l of
 //           its own, joined at the end of a segment.
 //   TMA     K_0 K_1 V_0 K_2 V_1 ...  A box costs ~90 cycles whatever it holds, so a
-//           tile is one box where it lies in one page, and else one per page (V,
-//           whose K = 16 steps need not be evenly spaced) or per page and 64 columns
-//           (K, whose rows have to be).
+//           page (from 16 tokens on) is one box, and the products take a tile page by
+//           page.  As a box per page and 64 columns, pages of 16 took 1165 us and
+//           pages of 64 688 us for the chunk of 4096 over 12288 positions.
 //   mma     two warps: S_{i+1} = Q K_{i+1}^T runs while P_i is formed
 //   clean   values of tiles in which some rows do not see some positions: what no row
 //           sees (the rest of a page) is set to 0, and elements that are not finite
@@ -92,12 +92,12 @@ struct Cfg {
     static constexpr size_t kPartFloats = size_t(kRows) * (D + 2);
 };
 
-// A tile of values lies as boxes of v_rows positions, each [64 columns][position];
+// A tile of keys or values lies as boxes of `rows` positions, each [64 columns][position]:
 // pages of 16 and 32 tokens arrive as one box each.
-__device__ __forceinline__ int v_box_rows(int shift) { return shift == 4 ? 16 : shift == 5 ? 32 : TK; }
+__device__ __forceinline__ int box_rows(int shift) { return shift == 4 ? 16 : shift == 5 ? 32 : TK; }
 template <typename C>
-__device__ __forceinline__ uint32_t v_place(int v_rows, int r) {  // bytes from the tile's start to row r of its first 64 columns
-    const int box = r & ~(v_rows - 1);
+__device__ __forceinline__ uint32_t place(int rows, int r) {  // bytes from the tile's start to position r's first 64 columns
+    const int box = r & ~(rows - 1);
     return uint32_t(box) * (128 * C::kChunks) + uint32_t(r - box) * 128;
 }
 
@@ -248,6 +248,18 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// S = Q K^T of a tile that lies in boxes of kBox positions, box by box: products of N = 16 and 32 cost 9 and
+// 16 cycles, in proportion to 64's 32, as long as their issue is straight-line code.
+template <typename C, uint32_t kIdS, int kBox>
+__device__ __forceinline__ void scores_of(uint32_t d, uint32_t q, uint32_t kb) {
+    constexpr uint32_t id = kIdS ^ (uint32_t(TK >> 3) << 17) ^ (uint32_t(kBox >> 3) << 17);
+#pragma unroll
+    for (int r = 0; r < TK; r += kBox)
+#pragma unroll
+        for (int z = 0; z < C::D / 16; ++z)
+            mma_f16_ta(d + r, q + 8 * z,
+                       gdn::desc_sw128(kb) + uint64_t(r * 8 * C::kChunks + (z >> 2) * (kBox * 8) + 2 * (z & 3)), id, z > 0);
 }
 // MN-major operand in the 128-byte swizzle: 64 elements (128 bytes) of MN by 8 of K
 // an atom; `lead` bytes from one atom of MN to the next, 1024 from one of K to the next.
@@ -437,27 +449,23 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         // ---- keys and values by TMA -------------------------------------------------
         asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
         const int ps = 1 << a.pl.shift, np = max(1, TK / ps);  // pages of a tile
-        // boxes of K: the whole tile, or (page, 64 columns); of V: whole pages from 16 tokens on
-        const bool k_whole = ps >= TK, v_pages = ps >= 16;
-        const int kb = k_whole ? 0 : lane / C::kChunks, kc = k_whole ? 0 : lane % C::kChunks;
-        const int vb = v_pages ? lane : kb, vc = v_pages ? 0 : kc;
-        const bool k_lane = k_whole ? lane == 0 : kb < np, v_lane = vb < np;
-        const uint32_t k_bytes = k_whole ? C::kTile : ps * 128u;
-        const uint32_t v_bytes = v_pages ? min(ps, TK) * 128u * C::kChunks : ps * 128u;
-        const uint32_t k_dst = kc * C::kChunkBytes + uint32_t(kb) * ps * 128u;
-        const uint32_t v_dst = v_pages ? vb * v_bytes : k_dst;
+        // a box: the whole tile, a whole page (from 16 tokens on), or a page's 64 columns
+        const bool pages = ps >= 16;
+        const int bb = pages ? lane : lane / C::kChunks, bc = pages ? 0 : lane % C::kChunks;  // this lane's page, chunk
+        const bool box_lane = bb < np;
+        const uint32_t bytes = pages ? min(ps, TK) * 128u * C::kChunks : ps * 128u;
+        const uint32_t dst = pages ? bb * bytes : bc * C::kChunkBytes + uint32_t(bb) * ps * 128u;
         int stage = 0;
         uint32_t phase = 0;
         long long issued = 0;
         bool ok = true, bad_page = false;
-        auto load = [&](const CUtensorMap *map, bool mine, int page, uint32_t dst, uint32_t bytes, int chunk, int row,
-                        int head) {
+        auto load = [&](const CUtensorMap *map, int page, int row, int head) {
             if (!wait_bar(empty_bar + stage, phase ^ 1, abort_flag)) return false;
-            mine = mine && page >= 0;
+            const bool mine = box_lane && page >= 0;
             const unsigned m = __ballot_sync(full, mine);
             if (lane == 0) gdn::mbar_arrive_expect_tx(full_bar + stage, __popc(m) * bytes);
             __syncwarp();
-            if (mine) tma_load_5d(tb + stage * C::kTile + dst, map, row, chunk, head, page, full_bar + stage);
+            if (mine) tma_load_5d(tb + stage * C::kTile + dst, map, row, bc, head, page, full_bar + stage);
             ++issued;
             if (++stage == C::kStages) {
                 stage = 0;
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             };
             int v_page = -1;
             for (int t = g.tile0; t <= g.tile1 && ok; ++t) {
-                int k_page = -1, next_v = -1;
+                int page = -1;
                 if (t < g.tile1) {
                     const int first = (t * TK) >> a.pl.shift;
                     if (first - base >= 32) {
@@ -494,12 +502,11 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         base += 32;
                         nxt = entry(base + 32 + lane);
                     }
-                    k_page = page_of(first, k_lane ? kb : 0);
-                    next_v = page_of(first, v_lane ? vb : 0);
-                    ok = load(&kmap, k_lane, k_page, k_dst, k_bytes, kc, (t * TK) & (ps - 1), g.h);
+                    page = page_of(first, box_lane ? bb : 0);
+                    ok = load(&kmap, page, (t * TK) & (ps - 1), g.h);
                 }
-                if (ok && t > g.tile0) ok = load(&vmap, v_lane, v_page, v_dst, v_bytes, vc, ((t - 1) * TK) & (ps - 1), g.h);
-                v_page = next_v;
+                if (ok && t > g.tile0) ok = load(&vmap, v_page, ((t - 1) * TK) & (ps - 1), g.h);
+                v_page = page;
             }
         }
         if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
@@ -521,7 +528,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         constexpr uint32_t kIdS = (1u << 4) | (fmt << 7) | (fmt << 10) | (uint32_t(TK >> 3) << 17) | (8u << 24);
         constexpr uint32_t kIdO = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);
         const bool is_s = warp == C::kMmaS;
-        const int v_rows = v_box_rows(a.pl.shift);
+        const int rows = box_rows(a.pl.shift);
         uint32_t seg = 0, masked = 0, asked = 0;
         long long loads = 0, tile = 0;  // of the segments before: ring places, tiles (buffers and phases of S, P)
         bool ok = true;
@@ -539,10 +546,9 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     gdn::tc_fence_after_sync();
                     if (elect_one()) {
                         const uint32_t kb = tb + stage * C::kTile, d = tmem + C::kS + uint32_t(sb) * TK;
-#pragma unroll
-                        for (int z = 0; z < D / 16; ++z)
-                            mma_f16_ta(d, tmem + C::kQ + 8 * z,
-                                       gdn::desc_sw128(kb + (z >> 2) * C::kChunkBytes) + 2 * (z & 3), kIdS, z > 0);
+                        if (rows == 64) scores_of<C, kIdS, 64>(d, tmem + C::kQ, kb);
+                        else if (rows == 32) scores_of<C, kIdS, 32>(d, tmem + C::kQ, kb);
+                        else scores_of<C, kIdS, 16>(d, tmem + C::kQ, kb);
                         gdn::mma_commit(s_bar + sb);
                         gdn::mma_commit(empty_bar + stage);
                     }
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         const uint32_t o = tmem + C::kO + (C::kStreams == 2 ? uint32_t(i & 1) * D : 0u);
 #pragma unroll
                         for (int z = 0; z < TK / 16; ++z)
-                            mma_f16_ta(o, p + 8 * z, desc_mn_sw128(vb + v_place<C>(v_rows, 16 * z), v_rows * 128), kIdO,
+                            mma_f16_ta(o, p + 8 * z, desc_mn_sw128(vb + place<C>(rows, 16 * z), rows * 128), kIdO,
                                        z > 0 || k >= C::kStreams);
                         gdn::mma_commit(pv_bar + (i & 1));
                         gdn::mma_commit(empty_bar + stage);
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         // the exponents of two values, and their lowest bits
         constexpr uint32_t kExp2 = std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
         constexpr uint32_t kLow2 = std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u;
-        const int v_rows = v_box_rows(a.pl.shift);
+        const int rows = box_rows(a.pl.shift);
         while (ok && walk.next(g)) {
             const int n = g.tile1 - g.tile0;
             uint32_t bits[4] = {0, 0, 0, 0};
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 constexpr int kRowPieces = C::kChunks * 8, kStep = 32;  // 16-byte pieces
                 auto piece = [&](int u) {
                     const int r = r0 + u / kRowPieces, c16 = u % kRowPieces;
-                    return reinterpret_cast<uint4 *>(vt + v_place<C>(v_rows, r) + (c16 >> 3) * (v_rows * 128) +
+                    return reinterpret_cast<uint4 *>(vt + place<C>(rows, r) + (c16 >> 3) * (rows * 128) +
                                                      (c16 & 7) * 16);
                 };
                 const int some = min(max(g.limit - t * TK - r0, 0), TK - r0) * kRowPieces;  // seen by some rows
@@ -1065,8 +1071,9 @@ int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *wor
     const int ps = dims->page_size;
     const uint32_t rows = uint32_t(ps < att::TK ? ps : att::TK);
     int rc;
-    if ((rc = gdn::encode_kv_pages(&kmap, k_pool, dims, rows, ps >= att::TK ? C::kChunks : 1)) ||
-        (rc = gdn::encode_kv_pages(&vmap, a.v_pool, dims, rows, ps >= 16 ? C::kChunks : 1)))
+    const uint32_t chunks = ps >= 16 ? C::kChunks : 1;
+    if ((rc = gdn::encode_kv_pages(&kmap, k_pool, dims, rows, chunks)) ||
+        (rc = gdn::encode_kv_pages(&vmap, a.v_pool, dims, rows, chunks)))
         return rc;
     a.meta = static_cast<int4 *>(workspace);
     a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);
