@@ -52,6 +52,8 @@
 //           do not see them; rows that do get them back at the end
 // Every mbarrier completes once per use, so a counter gives every wait's phase; a
 // wait is only ever for the next completion that the waiter has not seen.
+#include <cudaTypedefs.h>
+
 #include <type_traits>
 
 #include "gdn_attn.h"
@@ -1060,6 +1062,29 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const att::Args a, 
     }
 }
 
+// A paged pool viewed as [page][head][d / 64][token][64], boxes of [chunks][rows tokens][64] of one head and
+// page in the 128-byte swizzle; GDN_OK or GDN_ERR_TMA.
+int encode_kv_pages(CUtensorMap *map, const void *pool, const gdn_attn_dims *d, uint32_t rows, uint32_t chunks) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (!enc) return GDN_ERR_TMA;
+    const cuuint64_t gdim[5] = {64, cuuint64_t(d->page_size), cuuint64_t(d->d_head / 64), cuuint64_t(d->h_kv),
+                                cuuint64_t(d->n_pages)};
+    const cuuint64_t gstride[4] = {cuuint64_t(d->token_stride) * 2, 128, cuuint64_t(d->head_stride) * 2,
+                                   cuuint64_t(d->page_stride) * 2};
+    const cuuint32_t box[5] = {64, rows, chunks, 1, 1}, estride[5] = {1, 1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void *>(pool), gdim, gstride, box, estride,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GDN_OK : GDN_ERR_TMA;
+}
+
 size_t workspace_bytes(const gdn_attn_dims *dims, int ctas) {
     return size_t(ctas) * (2 * att::kRows * size_t(dims->d_head + 2) * 4 + 2 * sizeof(int4));
 }
@@ -1072,8 +1097,8 @@ int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *wor
     const uint32_t rows = uint32_t(ps < att::TK ? ps : att::TK);
     int rc;
     const uint32_t chunks = ps >= 16 ? C::kChunks : 1;
-    if ((rc = gdn::encode_kv_pages(&kmap, k_pool, dims, rows, chunks)) ||
-        (rc = gdn::encode_kv_pages(&vmap, a.v_pool, dims, rows, chunks)))
+    if ((rc = encode_kv_pages(&kmap, k_pool, dims, rows, chunks)) ||
+        (rc = encode_kv_pages(&vmap, a.v_pool, dims, rows, chunks)))
         return rc;
     a.meta = static_cast<int4 *>(workspace);
     a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);

@@ -1180,19 +1180,6 @@ int encode_xc_tiles(CUtensorMap *map, const float *xc, int64_t N, int64_t C, uin
                     bool swizzle) {
     return encode_xc_map(map, xc, N, C, rows, cols, swizzle);
 }
-int encode_kv_pages(CUtensorMap *map, const void *pool, const gdn_attn_dims *d, uint32_t rows, uint32_t chunks) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return GDN_ERR_TMA;
-    const cuuint64_t gdim[5] = {64, cuuint64_t(d->page_size), cuuint64_t(d->d_head / 64), cuuint64_t(d->h_kv),
-                                cuuint64_t(d->n_pages)};
-    const cuuint64_t gstride[4] = {cuuint64_t(d->token_stride) * 2, 128, cuuint64_t(d->head_stride) * 2,
-                                   cuuint64_t(d->page_stride) * 2};
-    const cuuint32_t box[5] = {64, rows, chunks, 1, 1}, estride[5] = {1, 1, 1, 1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void *>(pool), gdim, gstride, box, estride,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? GDN_OK : GDN_ERR_TMA;
-}
 int sm_count_current() { return sm_count(); }
 uint64_t take_test_stall_ns() { return g_stall_ns.exchange(0); }
 }  // namespace gdn
