@@ -873,6 +873,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 if (!ok) break;
             }
             float f0 = 1.f, f1 = 0.f;  // factors of the streams' O
+            bool s0 = true, s1 = false;  // whether the streams have seen anything (l is not 0: NaN counts, and stays)
             if (C::kStreams == 2) {
                 ml[seg & 1][stream][row] = make_float2(m, l);
                 __syncwarp();
@@ -881,10 +882,12 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 if (!ok) break;
                 const float2 x0 = ml[seg & 1][0][row], x1 = ml[seg & 1][C::kStreams - 1][row];
                 m = fmaxf(x0.x, x1.x);
-                // a stream that has seen nothing has no part (its O may never have been written)
-                f0 = x0.x == -INFINITY ? 0.f : exp2_approx(x0.x - m);
-                f1 = x1.x == -INFINITY ? 0.f : exp2_approx(x1.x - m);
-                l = (f0 == 0.f ? 0.f : f0 * x0.y) + (f1 == 0.f ? 0.f : f1 * x1.y);
+                // (the O of a stream that has seen nothing may never have been written)
+                s0 = x0.y != 0.f;
+                s1 = x1.y != 0.f;
+                f0 = exp2_approx(x0.x - m);
+                f1 = exp2_approx(x1.x - m);
+                l = (s0 ? f0 * x0.y : 0.f) + (s1 ? f1 * x1.y : 0.f);
             }
             gdn::tc_fence_after_sync();
             const bool whole = g.starts && g.ends;
@@ -919,7 +922,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         gdn::tmem_ld32x2(trow + C::kO + cc, trow + C::kO + D + cc, v, v1);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            v[e] = (f0 == 0.f ? 0.f : f0 * v[e]) + (f1 == 0.f ? 0.f : f1 * v1[e]);
+                            v[e] = (s0 ? f0 * v[e] : 0.f) + (s1 ? f1 * v1[e] : 0.f);
                     } else {
                         gdn::tmem_ld32(trow + C::kO + cc, v);
                     }
@@ -983,16 +986,18 @@ struct Joined {
     float4 o;
 };
 __device__ __forceinline__ void join(Joined &a, const Joined &b) {
-    if (b.m == -INFINITY) return;  // nothing seen in that part
-    const float M = fmaxf(a.m, b.m);
-    const float f = a.m == -INFINITY ? 0.f : att::exp2_approx(a.m - M), w = att::exp2_approx(b.m - M);
-    const bool first = a.m == -INFINITY;
+    if (b.l == 0.f) return;  // nothing seen in that part (l is NaN where a score is)
+    if (a.l == 0.f) {
+        a = b;
+        return;
+    }
+    const float M = fmaxf(a.m, b.m), f = att::exp2_approx(a.m - M), w = att::exp2_approx(b.m - M);
     a.m = M;
-    a.l = fmaf(w, b.l, first ? 0.f : f * a.l);
-    a.o.x = fmaf(w, b.o.x, first ? 0.f : f * a.o.x);
-    a.o.y = fmaf(w, b.o.y, first ? 0.f : f * a.o.y);
-    a.o.z = fmaf(w, b.o.z, first ? 0.f : f * a.o.z);
-    a.o.w = fmaf(w, b.o.w, first ? 0.f : f * a.o.w);
+    a.l = fmaf(w, b.l, f * a.l);
+    a.o.x = fmaf(w, b.o.x, f * a.o.x);
+    a.o.y = fmaf(w, b.o.y, f * a.o.y);
+    a.o.z = fmaf(w, b.o.z, f * a.o.z);
+    a.o.w = fmaf(w, b.o.w, f * a.o.w);
 }
 
 template <typename T, int D>

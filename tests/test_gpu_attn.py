@@ -177,6 +177,20 @@ def test_nan_in_the_context_reaches_the_rows_that_see_it():
     assert torch.isfinite(o[:3]).all() and torch.isnan(o[3:, :4, 0]).all() and torch.isfinite(o[3:, 4:]).all()
 
 
+@pytest.mark.parametrize("d,hq,hkv,name", [(256, 16, 2, "bf16"), (128, 8, 2, "fp16"), (64, 4, 2, "bf16")])
+@pytest.mark.parametrize("where", [range(100, 101), range(64, 128), range(128, 320)])
+def test_nan_keys_in_the_context_reach_the_rows_that_see_them(d, hq, hkv, name, where):
+    """One key, a whole tile of keys and several: the sequence's rows are NaN at that key/value head, in
+    whichever parts of the work the keys fall; the other sequence's and the other heads' are not."""
+    dtype = R.DTYPES[name]
+    cache, q, _ = case(14, dtype, d, hq, hkv, 16, "token", [700, 100], [2, 2], False)
+    for x in where:
+        cache.k[cache.index(0, x)[0]] = float("nan")
+    o = Attn(cache, q, [700, 100], [2, 2], None, dtype, d ** -0.5).out()
+    assert torch.isnan(o[:2, :hq // hkv]).all()
+    assert torch.isfinite(o[:2, hq // hkv:]).all() and torch.isfinite(o[2:]).all()
+
+
 def test_far_offsets():
     """Pages whose element offsets pass 2^31."""
     d, hkv, page, dtype = 128, 2, 16, torch.bfloat16
