@@ -16,6 +16,10 @@
  *                       and recurrent state of every sequence by its accepted
  *                       root-to-node path, on the device, as one transaction.
  *
+ * and what stands around it in a hybrid model's round: the full-attention
+ * layers (gdn_rope_append, gdn_paged_attention, gdn_kv_commit) and the decision
+ * on the drafted tokens (gdn_tree_accept).
+ *
  * Sources (page title, section):
  *   lucebox PR #707 "perf(qwen35): fuse the DFlash2 concurrent verify Gated
  *     DeltaNet route" - Optimizations: ssm_conv_tree_step, the read-only
@@ -55,8 +59,10 @@
  *   history); a parent precedes its child.  Value head h reads q/k head
  *   floor(h / G).
  * Streams.  All work is enqueued on `stream` (a cudaStream_t; NULL = the
- *   legacy default stream) and is asynchronous.  verify -> (host decides
- *   acceptance) -> commit must be ordered by the caller's stream.  The
+ *   legacy default stream) and is asynchronous.  verify -> acceptance (by
+ *   gdn_tree_accept or by the host) -> commit must be ordered by the caller's
+ *   stream; gdn_tree_accept does not release its dependents early, so the
+ *   commits may follow it directly.  The
  *   library's kernels use programmatic dependent launch: each may start
  *   while the previous kernel on the stream finishes, and waits for it to
  *   complete before touching any buffer the library writes.  They may read
@@ -65,7 +71,7 @@
  *   must not let that kernel trigger its dependents early
  *   (cudaTriggerProgrammaticLaunchCompletion / griddepcontrol.launch_dependents
  *   before its writes); a plain launch, or a copy, is always safe.
- * Access.  gdn_conv_tree_step and gdn_tree_verify never write the pools
+ * Access.  gdn_conv_tree_step and gdn_tree_verify never write the state pools
  *   (`conv_hist`, `ssm`).  Only gdn_commit writes them.  No float atomics:
  *   results are bit-for-bit reproducible run to run.
  * Errors.  The return value is a host-side status: GDN_OK or a negative
