@@ -619,6 +619,14 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         const int rows = box_rows(a.pl.shift);
         while (ok && walk.next(g)) {
             const int n = g.tile1 - g.tile0;
+            // this warp is the first to come to a segment: its Q rows are on their way into L2 while the last
+            // segment's results go out
+            for (int u = lane; u < g.rows * C::kChunks; u += 32) {
+                const int r = u / C::kChunks;
+                const T *src = static_cast<const T *>(a.q) + (int64_t(g.q.n0) + g.i0 + r / a.G) * a.q_stride +
+                               (int64_t(g.h) * a.G + r % a.G) * D + 64 * (u % C::kChunks);
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+            }
             uint32_t bits[4] = {0, 0, 0, 0};
             for (int t = max(g.tile0, g.safe / TK); t < g.tile1 && ok; ++t) {
                 const long long at = loads + C::v_at(t - g.tile0, n);
