@@ -70,7 +70,10 @@ namespace att {
 constexpr int kRows = 128;
 constexpr float kMoveAt = 8.f, kMoveAtSum = 256.f;  // m moves when a p passes 2^8, or a tile's sum 64 times that
 constexpr int TK = 64;       // positions of a tile
-constexpr int kItemUnits = 4; // what an item costs beside its tiles (Q in, results out), in tiles
+// What an item costs beside its tiles (Q in, results out), in tiles.  Too little makes the CTAs with many
+// short items the last (chunks of up to 701 tokens: 4 289 us, 8 263, 10 266; 64 trees 122.6, 119.5, 120.6),
+// too much those with few long ones (64 single tokens: 186.9, 187.0, 187.2; 24 191.1).
+constexpr int kItemUnits = 10;
 constexpr int kNfBufs = 16;  // the ring holds the values of 12 segments at most, and one may still be going out
 
 template <int D_>
