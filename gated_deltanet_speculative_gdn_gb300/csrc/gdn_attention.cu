@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     constexpr int kThreads = C::kThreads, kTma = C::kTma;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
-    __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, go_bar[2], clean_bar[2], drain_bar[2];
+    __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, ofree_bar, go_bar[2], clean_bar[2], drain_bar[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     __shared__ Start start_s;
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         }
         gdn::mbar_init(&q_bar, C::kRowWarps);
         gdn::mbar_init(&ml_bar, C::kRowWarps);
+        gdn::mbar_init(&ofree_bar, C::kRowWarps);
         gdn::fence_mbar_init();
         abort_s = 0;
         start_s.count = 0;
@@ -585,6 +586,8 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         }
                     }
                     ok = wait_bar(p_bar + (i & 1), uint32_t(i >> 1) & 1, abort_flag);
+                    // both warpgroups read both O at a segment's end (one alone is done before it makes this P)
+                    if (C::kStreams == 2 && k == 0 && seg > 0) ok = ok && wait_bar(&ofree_bar, (seg - 1) & 1, abort_flag);
                     if (clean) {
                         ok = ok && wait_bar(clean_bar + (masked & 1), (masked >> 1) & 1, abort_flag);
                         ++masked;
@@ -706,14 +709,13 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         int4 *meta = a.meta + 2 * blockIdx.x;
         bool head_part = false, tail_part = false;
         int line_s = -1;
-        while (ok && walk.next(g)) {
-            const int n = g.tile1 - g.tile0;
-            const bool live_warp = w * 32 < g.rows, live = row < g.rows;
-            const int i = g.i0 + row / a.G, hd = g.h * a.G + row % a.G;
-            // Q rows into tensor memory (the last segment's products are complete)
-            if (live_warp) {
+        // A segment's Q rows into tensor memory, once every S of the segment before has been formed.
+        auto load_q = [&](const Segment &sg) {
+            if (w * 32 < sg.rows) {
+                const int hd = sg.h * a.G + row % a.G;
+                const bool live = row < sg.rows;
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
-                                                                   (int64_t(g.q.n0) + i) * a.q_stride + int64_t(hd) * D);
+                                                                   (int64_t(sg.q.n0) + sg.i0 + row / a.G) * a.q_stride + int64_t(hd) * D);
                 constexpr int kAhead = C::kStreams == 2 ? 1 : 2;  // chunks whose loads go out before the first is waited for
 #pragma unroll
                 for (int z0 = 0; z0 < (C::kChunks + C::kStreams - 1) / C::kStreams; z0 += kAhead) {
@@ -741,6 +743,13 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             gdn::tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) arrive(&q_bar);
+        };
+        bool more = walk.next(g);
+        if (more) load_q(g);
+        while (ok && more) {
+            const int n = g.tile1 - g.tile0;
+            const bool live_warp = w * 32 < g.rows, live = row < g.rows;
+            const int i = g.i0 + row / a.G, hd = g.h * a.G + row % a.G;
             // the row's ancestors
             unsigned long long line = 0;
             if (a.parents && live_warp) {
@@ -882,6 +891,15 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                 if (lane == 0) arrive(p_bar + buf);
             }
             if (!ok) break;
+            // ---- the next segment's Q in, so that its first scores are formed meanwhile -------
+            if (C::kStreams == 2) {  // the last S may be the other warpgroup's
+                const long long it = tile + n - 1;
+                ok = wait_bar(s_bar + C::s_buf(it), C::s_use(it) & 1, abort_flag);
+                if (!ok) break;
+            }
+            Segment next;
+            more = walk.next(next);
+            if (more) load_q(next);
             // ---- the segment's rows out ---------------------------------------------------
             if (done > 0) {  // this warpgroup's last product (all before it are complete with it)
                 const long long it = tile + n - 1 - (C::kStreams == 2 ? int((tile + n - 1 - stream) & 1) : 0);
@@ -977,8 +995,14 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     }
                 }
             }
+            if (C::kStreams == 2) {
+                gdn::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive(&ofree_bar);
+            }
             tile += n;
             ++seg;
+            g = next;
         }
         if (tid == 0) {
             if (!head_part) meta[0] = make_int4(0, 0, 0, 0);
