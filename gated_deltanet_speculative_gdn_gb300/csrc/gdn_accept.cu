@@ -24,14 +24,14 @@
 // passes took longer than the passes.)  c, W and Z are pairs.
 //
 // Mapping.  A cluster of CTAs takes a sequence, each CTA a contiguous slice of
-// the vocabulary.  Thread 0 of every CTA walks the tree with the same numbers (so
+// the vocabulary.  Warp 0 of every CTA walks the tree with the same numbers (so
 // the CTAs agree without exchange) and calls for a pass when it needs a sum; a
 // pass sums each warp's contiguous range, and the CTAs' sums are exchanged
 // through distributed shared memory in rank order.  The last pass's sums are the
 // coarse cumulative sum: the CTA and the warp whose range holds the threshold
 // narrow it down.  Bound by the latency of the dependent passes (~3 us each at
 // 131072 tokens: 1 MB of rows over a cluster, two cluster-wide exchanges): one tree of
-// 16 nodes takes 14 us, 64 of them 39 us for 71 MB of rows.
+// 16 nodes takes 13 us, 64 of them 40 us for 71 MB of rows.
 //
 // It does not release its dependent kernel early: the commits read `accepted`
 // before their own wait.
@@ -45,7 +45,7 @@
 namespace {
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarpsA = kThreads / 32, kMaxCluster = 8;
+constexpr int kThreads = 256, kWarpsA = kThreads / 32, kMaxCluster = 16;
 
 struct AcceptArgs {
     const float *__restrict__ p, *__restrict__ q;
@@ -202,7 +202,7 @@ __device__ __forceinline__ int select_part(Fix v, Fix &b, Fix &thr) {
     return k;
 }
 
-__global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) tree_accept_kernel(const AcceptArgs a) {
     __shared__ Fix warp_tot[kWarpsA];
     __shared__ Fix cta_tot[2][kMaxCluster];  // [pass parity][rank], written by every CTA of the cluster
     __shared__ int par[gdn::kMaxSeqNodes], tok[gdn::kMaxSeqNodes], out[gdn::kMaxSeqNodes];
@@ -258,53 +258,65 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
     const int per = (nvec + C - 1) / C, v0 = min(nvec, rank * per), v1 = min(nvec, v0 + per);
     const int perw = (v1 - v0 + kWarpsA - 1) / kWarpsA, w0 = min(v1, v0 + warp * perw), w1 = min(v1, w0 + perw);
 
-    // thread 0's walk
-    int cur = 0, t = 1, depth = 1, n_out = 0, parity = 0;
+    // warp 0's walk, the same in every lane; lane l looks after the parents of nodes l and l + 32
+    int cur = 0, t = 1, depth = 1, n_out = 0, parity = 0;  // t: the first node that has not been looked at
     Pair c = {0.f, 0.f}, W = {1.f, 0.f}, Z = {1.f, 0.f};
     bool fallback = false;
     Pass ps;
     const float un = a.u_next[s];
+    const int par_lo = lane < n ? par[lane] : -2, par_hi = lane + 32 < n ? par[lane + 32] : -2;
+    auto kids_from = [&](int node, int first) {  // node's children from `first` on, as a mask
+        const unsigned long long m = (static_cast<unsigned long long>(__ballot_sync(0xffffffffu, par_hi == node)) << 32) |
+                                     __ballot_sync(0xffffffffu, par_lo == node);
+        return first < 64 ? m >> first << first : 0ull;
+    };
     for (;;) {
-        if (tid == 0) {
+        if (warp == 0) {
             bool need = false;
-            while (t < n && !need) {
-                if (par[t] == cur && Z.h > 0.f) {
-                    const int y = tok[t];
-                    bool was_out = false;
-                    for (int k = 0; k < n_out; ++k) was_out |= out[k] == y;
-                    const float qx = was_out && a.q ? 0.f : qc[t];
-                    Pair px = {0.f, 0.f};
-                    if (!was_out) px = a.q ? positive(minus({pc[t], 0.f}, times(c, {qx, 0.f}))) : positive({pc[t], 0.f});
-                    // both sides times 2^64 (exact): the low parts of small probabilities stay normal
-                    constexpr float kUp = 18446744073709551616.0f;
-                    if (less(times(times({uc[t], 0.f}, {qx * kUp, 0.f}), W), times({px.h * kUp, px.l * kUp}, Z))) {
-                        cur = t;
-                        ++depth;
-                        n_out = 0;
-                        c = {0.f, 0.f};
-                        W = Z = {1.f, 0.f};
+            unsigned long long kids = kids_from(cur, t);
+            while (kids && Z.h > 0.f && !need) {
+                const int x = __ffsll(static_cast<long long>(kids)) - 1, y = tok[x];
+                kids &= kids - 1;
+                t = x + 1;
+                bool was_out = false;
+                for (int k = 0; k < n_out; ++k) was_out |= out[k] == y;
+                const float qx = was_out && a.q ? 0.f : qc[x];
+                Pair px = {0.f, 0.f};
+                if (!was_out) px = a.q ? positive(minus({pc[x], 0.f}, times(c, {qx, 0.f}))) : positive({pc[x], 0.f});
+                // both sides times 2^64 (exact): the low parts of small probabilities stay normal
+                constexpr float kUp = 18446744073709551616.0f;
+                if (less(times(times({uc[x], 0.f}, {qx * kUp, 0.f}), W), times({px.h * kUp, px.l * kUp}, Z))) {
+                    cur = x;
+                    ++depth;
+                    n_out = 0;
+                    c = {0.f, 0.f};
+                    W = Z = {1.f, 0.f};
+                    kids = kids_from(cur, t);
+                } else {
+                    if (!(a.q && a.replacement) && !was_out) {
+                        __syncwarp();
+                        if (lane == 0) out[n_out] = y;
+                        __syncwarp();
+                        ++n_out;
+                    }
+                    if (a.q) {
+                        c = plus(c, over(W, Z));
+                        if (!a.replacement) Z = positive(minus(Z, {qx, 0.f}));
+                        need = kids && Z.h > 0.f;  // the sum is wanted only if another child is tried
                     } else {
-                        if (!(a.q && a.replacement) && !was_out) out[n_out++] = y;
-                        if (a.q) {
-                            c = plus(c, over(W, Z));
-                            if (!a.replacement) Z = positive(minus(Z, {qx, 0.f}));
-                            // the sum is wanted only if another child is tried
-                            for (int x = t + 1; x < n; ++x) need |= par[x] == cur;
-                            need = need && Z.h > 0.f;
-                        } else {
-                            W = positive(minus(W, px));
-                        }
+                        W = positive(minus(W, px));
                     }
                 }
-                ++t;
             }
-            const int64_t row = n0 + cur;
-            pass_s.p = a.p + row * a.p_stride;
-            pass_s.q = a.q && c.h > 0.f && !fallback ? a.q + row * a.q_stride : nullptr;
-            pass_s.ch = c.h;
-            pass_s.cl = c.l;
-            pass_s.n_out = fallback || a.q ? 0 : n_out;
-            pass_s.last = !need;
+            if (lane == 0) {
+                const int64_t row = n0 + cur;
+                pass_s.p = a.p + row * a.p_stride;
+                pass_s.q = a.q && c.h > 0.f && !fallback ? a.q + row * a.q_stride : nullptr;
+                pass_s.ch = c.h;
+                pass_s.cl = c.l;
+                pass_s.n_out = fallback || a.q ? 0 : n_out;
+                pass_s.last = !need;
+            }
         }
         __syncthreads();
         ps = pass_s;
@@ -321,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
             const Fix total = warp_sum(mine);
             int step = 0;
             if (ps.last) {
-                if (total <= 0 && !__shfl_sync(0xffffffffu, int(fallback), 0)) {
+                if (total <= 0 && !fallback) {
                     fallback = true;  // nothing is left: the target's own row
                 } else {
                     // cumulative sums pass u total exactly where they pass its floor; u in units of 2^-63
@@ -340,10 +352,8 @@ __global__ void __launch_bounds__(kThreads) tree_accept_kernel(const AcceptArgs 
                     }
                 }
             }
-            if (lane == 0) {
-                if (!step) W = to_pair(total);
-                step_s = step;
-            }
+            if (!step) W = to_pair(total);
+            if (lane == 0) step_s = step;
         }
         parity ^= 1;
         __syncthreads();
@@ -430,11 +440,14 @@ extern "C" int gdn_tree_accept(const gdn_dims *dims, int vocab, const float *p, 
 
     AcceptArgs a{p, q, p_stride, q_stride, tokens, parents, node_off, u, u_next, accepted, next_token, n_accepted,
                  status, int(S), int(N), vocab, dims->max_seq_nodes, replacement};
-    // A cluster as large as leaves every CTA resident at once (two per SM) and a slice of one vector a
-    // thread: 64 sequences of 131072 tokens take 39 us with 4 CTAs each and 48 us with 8, whose second wave
-    // runs alone; one sequence 13.7 us with 8.
+    // A cluster as large as leaves every CTA resident at once (four of 256 threads per SM) and a slice of one
+    // vector a thread.  64 sequences of 131072 tokens, three sets of rows in turn: 40 us with 8 CTAs each, 45 us
+    // with 4 of 512 threads; one sequence 12.9 us with 16, 16.2 with 8 of 512.  (More CTAs than are resident at
+    // once: 48 us, the second wave runs alone.)
     int C = 1;
-    while (C < kMaxCluster && int64_t(vocab) / (2 * C) >= 2048 && S * 2 * C <= 304) C *= 2;
+    while (C < kMaxCluster && int64_t(vocab) / (2 * C) >= 1024 && S * 2 * C <= 608) C *= 2;
+    if (C > 8 && cudaFuncSetAttribute(tree_accept_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(S * C));
     cfg.blockDim = dim3(kThreads);
