@@ -11,9 +11,8 @@
 // formed without a look at the maximum, which would stand before all of them in the
 // longest chain of the kernel; a tile whose p sum to more than 64 2^8 has its m moved
 // and its p formed again.  (With two, keeping the scores for that costs registers that
-// spill: 270 -> 330 us on the mixed chunks.)  Parts of a
-// row's positions are joined by the same rule: o = sum 2^(m_i - M) O_i / sum
-// 2^(m_i - M) l_i.
+// spill: 270 -> 330 us for chunks of up to 701 tokens at D = 128.)  Parts of a row's
+// positions are joined by the same rule: o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // Rounding.  The products run on the tensor cores with 16-bit operands and fp32
 // accumulators, so p is rounded to the cache's type before P V (a relative half
@@ -22,21 +21,20 @@
 // Work.  The h_q / h_kv heads that share a key/value head are rows of one tile:
 // row r is (token i0 + r / G, head r % G), 128 / G tokens a tile, so keys and
 // values are read once for all of them.  An item is (sequence, key/value head, row
-// tile); its positions come in tiles of TK.  All items in a row,
-// each its tiles and a few tiles' worth for its beginning and end, are cut into
-// equal shares, one per CTA (one CTA per SM): lengths as ragged as they come keep
-// every SM busy to the end, one sequence alone spreads over the GPU, and a CTA has
-// at most one item that began before it and one that ends after it.  Those parts
-// go to the workspace and a second kernel joins them in CTA order, so results do
-// not depend on timing.
+// tile); its positions come in tiles of TK.  All items in a row, each its tiles and
+// a few tiles' worth for its beginning and end, are cut into equal shares, one per
+// CTA (one CTA per SM): lengths as ragged as they come keep every SM busy to the end,
+// one sequence alone spreads over the GPU, and a CTA has at most one item that began
+// before it and one that ends after it.  Those parts go to the workspace and a second
+// kernel joins them in CTA order, so results do not depend on timing.
 //
 // Mapping (GB300).  Tensor memory holds O (D columns, fp32), Q (D / 2 columns, the
 // A operand of Q K^T: nothing of it is read again from shared memory, which leaves
 // all of that to keys and values), one score tile per warpgroup (64 columns) and two
 // of P (32 columns, the A operand of P V), so that the next scores need not wait for
-// the product.  Shared memory is a ring of 192 KB of
-// key and value tiles, filled by TMA page by page in the 128-byte swizzle: keys as
-// they lie are the K-major B operand, values as they lie the MN-major one.
+// the product.  Shared memory is a ring of 192 KB of key and value tiles, filled by
+// TMA page by page in the 128-byte swizzle: keys as they lie are the K-major B
+// operand, values as they lie the MN-major one.
 //   rows    four warps, row r = 32 w + lane = tensor-memory lane: Q in, scores -> P,
 //           moves of m, results out.  For D <= 128 the softmax is longer than the
 //           products: two warpgroups take alternate tiles, each with an O, m and l of
@@ -45,11 +43,13 @@
 //           page (from 16 tokens on) is one box, and the products take a tile page by
 //           page.  As a box per page and 64 columns, pages of 16 took 1165 us and
 //           pages of 64 688 us for the chunk of 4096 over 12288 positions.
-//   mma     two warps: S_{i+1} = Q K_{i+1}^T runs while P_i is formed
+//   mma     two warps: S_{i+1} = Q K_{i+1}^T runs while P_i is formed (one warp's waits
+//           for one product kept it from the other: 745 -> 724 us, and 592 with P's own place)
 //   clean   values of tiles in which some rows do not see some positions: what no row
 //           sees (the rest of a page) is set to 0, and elements that are not finite
 //           are set to 0 and remembered, since 0 * NaN in P V would reach rows that
 //           do not see them; rows that do get them back at the end
+//
 // Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 182-188 us, 6.3-6.5 TB/s,
 // bound by HBM; 64 trees of 16 nodes over up to 8,192 121 us, 5.0 TB/s, HBM and the parts' way through memory;
 // 4,096 tokens over 12,288 positions 545-615 us, 1.55-1.75 PFLOP/s, tensor cores under the power cap; one token
