@@ -411,7 +411,8 @@ int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
  * child is tried).  When no child is left the next token is drawn
  * from that residual (from p[t] itself when its sum is 0): the first y whose
  * cumulative sum passes u_next[s] times the total.  The tokens that come out are
- * distributed as the target's.  Sums, c, W and Z carry at least 44 bits.
+ * distributed as the target's.  c and Z carry at least 44 bits, W and the sums
+ * 2^-48 of a distribution's mass.
  *   replacement  0: as above.  1: the draft draws children independently (Z
  *            stays 1 and nothing is taken out)
  *   q        NULL: the children are proposed outright (q[t][y] = 1 for them;
