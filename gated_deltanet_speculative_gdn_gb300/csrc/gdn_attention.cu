@@ -51,9 +51,9 @@
 //           do not see them; rows that do get them back at the end
 //
 // Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 182-188 us, 6.3-6.5 TB/s,
-// bound by HBM; 64 trees of 16 nodes over up to 8,192 121 us, 5.0 TB/s, HBM and the parts' way through memory;
-// 4,096 tokens over 12,288 positions 545-615 us, 1.55-1.75 PFLOP/s, tensor cores under the power cap; one token
-// over 777 positions 13 us, latency.
+// bound by HBM; 64 trees of 16 nodes over up to 8,192 114-120 us, 5.1-5.3 TB/s, HBM and the parts' way through
+// memory; 4,096 tokens over 12,288 positions 533-605 us, 1.6-1.8 PFLOP/s, tensor cores under the power cap; one
+// token over 777 positions 13 us, latency.
 //
 // Every mbarrier completes once per use, so a counter gives every wait's phase; a
 // wait is only ever for the next completion that the waiter has not seen.
