@@ -750,6 +750,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                             q[z][4 * k + 3] = v.w;
                         }
                     }
+                    __syncwarp();  // lanes without a row have loaded nothing; the stores are the whole warp's
 #pragma unroll
                     for (int z = 0; z < kAhead; ++z) {
                         const int cc = (z0 + z) * C::kStreams + (C::kStreams == 2 ? stream : 0);
@@ -788,6 +789,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         x = p;
                     }
                 }
+                __syncwarp();
             }
             const int upto = g.q.ctx + i + 1;
             float m = -INFINITY, l = 0.f;
@@ -969,6 +971,9 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
 #pragma unroll 1
                 for (int cc = col0; cc < col0 + kCols; cc += 32) {
                     float v[32];
+                    // rows past the last and rows with other non-finite values have gone other ways; the loads
+                    // from tensor memory are the whole warp's, together
+                    __syncwarp();
                     if (C::kStreams == 2) {
                         float v1[32];
                         gdn::tmem_ld32x2(trow + C::kO + cc, trow + C::kO + D + cc, v, v1);
@@ -996,8 +1001,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                                 }
                             }
                     }
-                    if (!live) continue;
-                    if (whole) {
+                    if (live && whole) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             float y[8];
@@ -1005,7 +1009,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                             for (int z = 0; z < 8; ++z) y[z] = v[e + z] * inv;
                             *reinterpret_cast<uint4 *>(orow + cc + e) = gdn::pack8<T>(y);
                         }
-                    } else {
+                    } else if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)  // column group, then row: neighbours side by side
                             *reinterpret_cast<float4 *>(part + 2 * kRows + (size_t((cc + e) / 4) * kRows + row) * 4) =
@@ -1027,6 +1031,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             if (!tail_part) meta[1] = make_int4(0, 0, 0, 0);
         }
     }
+    __syncwarp();  // lanes may come from bounded waits of their own
     gdn::tc_fence_before_sync();
     __syncthreads();
     if (tid == 0 && abort_s) gdn::record_status(a.status, GDN_DEV_TIMEOUT);
