@@ -37,7 +37,7 @@ EXPORTED_SYMBOLS = ("gdn_conv_tree_step", "gdn_tree_verify", "gdn_chain_verify",
                     "gdn_conv_tree_step_compact", "gdn_commit_compact", "gdn_gated_rmsnorm",
                     "gdn_decode_step", "gdn_rope_append", "gdn_paged_attention",
                     "gdn_attention_workspace_bytes", "gdn_kv_commit", "gdn_tree_accept",
-                    "gdn_test_stall_next_verify",
+                    "gdn_test_stall_next_verify", "gdn_test_stall_next_attention",
                     "gdn_status_str", "gdn_replay_row_floats")
 
 if not os.path.exists(LIB_PATH):
@@ -98,6 +98,8 @@ lib.gdn_commit_compact.argtypes = [_DP, _P, _P, _P, _P, _P, _I64, _P, _I64, _P, 
 lib.gdn_gated_rmsnorm.argtypes = [_DP, _P, _P, _I64, _P, ctypes.c_float, ctypes.c_int, _P, _P]
 lib.gdn_test_stall_next_verify.argtypes = [ctypes.c_uint64]
 lib.gdn_test_stall_next_verify.restype = None
+lib.gdn_test_stall_next_attention.argtypes = [ctypes.c_uint64, ctypes.c_int]
+lib.gdn_test_stall_next_attention.restype = None
 lib.gdn_decode_step.argtypes = [_DP, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P,
                                 _P]
 _AP = ctypes.POINTER(AttnDims)
@@ -268,3 +270,7 @@ def gdn_tree_accept(dims: GdnDims, vocab: int, p, p_stride: int, q, q_stride: in
 
 def gdn_test_stall_next_verify(wait_ns: int) -> None:
     lib.gdn_test_stall_next_verify(int(wait_ns))
+
+
+def gdn_test_stall_next_attention(wait_ns: int, role: int) -> None:
+    lib.gdn_test_stall_next_attention(int(wait_ns), int(role))

@@ -59,6 +59,8 @@
 // wait is only ever for the next completion that the waiter has not seen.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "gdn_attn.h"
@@ -124,6 +126,8 @@ struct Args {
     int4 *meta;    // [CTA][2]: rows of the part (0: none), ends, token n0 + i0, key/value head
     int S, N, max_tokens, Hq, Hkv, G, R;  // R: tokens of a row tile
     int once;                             // no sequence has more than one row tile
+    uint64_t stall_ns;                    // test hook: a warp of CTA 0 waits for what never comes, so long (0: none)
+    int stall_role;                       // 0 rows, 1 copies, 2 scores, 3 P V, 4 cleaning
 };
 
 // sum_{j < n} floor((a j + b) / m), a, b >= 0, m > 0: by Euclid's steps on (a, m)
@@ -357,7 +361,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     constexpr int kThreads = C::kThreads, kTma = C::kTma;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
-    __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, ofree_bar, go_bar[2], clean_bar[2], drain_bar[2];
+    __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, ofree_bar, go_bar[2], clean_bar[2], drain_bar[2], never_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
     __shared__ Start start_s;
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         gdn::mbar_init(&q_bar, C::kRowWarps);
         gdn::mbar_init(&ml_bar, C::kRowWarps);
         gdn::mbar_init(&ofree_bar, C::kRowWarps);
+        gdn::mbar_init(&never_bar, 1);
         gdn::fence_mbar_init();
         abort_s = 0;
         start_s.count = 0;
@@ -468,6 +473,11 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
     const uint32_t tmem = tmem_slot;
     Walk walk(a, start);
     Segment g;
+    bool ok = true;  // this warp's; false once a wait has run out
+    if (a.stall_ns && blockIdx.x == 0 && warp == (a.stall_role == 0 ? 0 : C::kRowWarps + a.stall_role - 1)) {
+        ok = __all_sync(full, gdn::mbar_wait_bounded(&never_bar, 0, a.stall_ns));
+        if (!ok) *abort_flag = 1;
+    }
 
     if (warp == kTma) {
         // ---- keys and values by TMA -------------------------------------------------
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         int stage = 0;
         uint32_t phase = 0;
         long long issued = 0;
-        bool ok = true, bad_page = false;
+        bool bad_page = false;
         auto load = [&](const CUtensorMap *map, int page, int row, int head) {
             if (!wait_bar(empty_bar + stage, phase ^ 1, abort_flag)) return false;
             const bool mine = box_lane && page >= 0;
@@ -539,16 +549,17 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             }
         }
         if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
-        if (!ok) {  // after a timeout copies may be in flight: wait for them (bounded)
-            const int n = int(min(issued, (long long)C::kStages));
-            for (int k = 0; k < n; ++k) {
-                if (stage == 0) {
-                    stage = C::kStages;
-                    phase ^= 1;
-                }
-                --stage;
-                gdn::mbar_wait_bounded(full_bar + stage, phase);
+        // The last copies into each stage are waited for (bounded) whatever has happened: when a role that was to
+        // take them has given up, this warp may have requested its last one all the same, and the CTA must not
+        // leave with copies under way into its shared memory.
+        const int n = int(min(issued, (long long)C::kStages));
+        for (int k = 0; k < n; ++k) {
+            if (stage == 0) {
+                stage = C::kStages;
+                phase ^= 1;
             }
+            --stage;
+            gdn::mbar_wait_bounded(full_bar + stage, phase);
         }
     } else if (warp == C::kMmaS || warp == C::kMmaO) {
         // ---- the products: one warp issues S = Q K^T, one O += P V, so that neither's
@@ -560,7 +571,6 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         const int rows = box_rows(a.pl.shift);
         uint32_t seg = 0, masked = 0, asked = 0;
         long long loads = 0, tile = 0;  // of the segments before: ring places, tiles (buffers and phases of S, P)
-        bool ok = true;
         while (ok && walk.next(g)) {
             const int n = g.tile1 - g.tile0;
             if (is_s) {
@@ -636,7 +646,6 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         // ---- values of tiles that not every row sees whole ----------------------------
         long long loads = 0;  // ring position of the segment's first load
         uint32_t seg = 0, masked = 0;
-        bool ok = true;
         // the exponents of two values, and their lowest bits
         constexpr uint32_t kExp2 = std::is_same<T, __nv_bfloat16>::value ? 0x7F807F80u : 0x7C007C00u;
         constexpr uint32_t kLow2 = std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u;
@@ -722,7 +731,6 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         const int col0 = stream * kCols;
         long long tile = 0;  // tiles of the segments before
         uint32_t seg = 0;
-        bool ok = true;
         const float c = a.c;
         int4 *meta = a.meta + 2 * blockIdx.x;
         bool head_part = false, tail_part = false;
@@ -763,7 +771,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive(&q_bar);
         };
-        bool more = walk.next(g);
+        bool more = ok && walk.next(g);
         if (more) load_q(g);
         while (ok && more) {
             const int n = g.tile1 - g.tile0;
@@ -1157,6 +1165,8 @@ size_t workspace_bytes(const gdn_attn_dims *dims, int ctas) {
     return size_t(ctas) * (2 * att::kRows * size_t(dims->d_head + 2) * 4 + 2 * sizeof(int4));
 }
 
+std::atomic<uint64_t> g_stall{0};  // the pending test stall: role in the top byte, ns below
+
 template <typename T, int D>
 int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *workspace, int ctas, cudaStream_t st) {
     using C = att::Cfg<D>;
@@ -1170,6 +1180,9 @@ int launch(const gdn_attn_dims *dims, const void *k_pool, att::Args a, void *wor
         return rc;
     a.meta = static_cast<int4 *>(workspace);
     a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);
+    const uint64_t stall = g_stall.exchange(0);
+    a.stall_ns = stall & ((uint64_t(1) << 56) - 1);
+    a.stall_role = int(stall >> 56);
     auto k = paged_attention_kernel<T, D>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem)) != cudaSuccess)
         return GDN_ERR_LAUNCH;
@@ -1234,8 +1247,13 @@ extern "C" int gdn_paged_attention(const gdn_attn_dims *dims, const void *q, int
     const int G = int(Hq / dims->h_kv);
     att::Args a{q, q_stride, v_pool, gdn::paged_layout(dims, page_table), ctx_len, node_off, parents,
                 scale * 1.4426950408889634f, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens, int(Hq),
-                dims->h_kv, G, att::kRows / G, dims->max_seq_tokens <= att::kRows / G};
+                dims->h_kv, G, att::kRows / G, dims->max_seq_tokens <= att::kRows / G, 0, 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dims->dtype == GDN_BF16 ? launch_d<__nv_bfloat16>(dims, k_pool, a, workspace, ctas, st)
                                    : launch_d<__half>(dims, k_pool, a, workspace, ctas, st);
+}
+
+extern "C" void gdn_test_stall_next_attention(uint64_t wait_ns, int role) {
+    if (role < 0 || role > 4) return;
+    g_stall.store(std::min<uint64_t>(wait_ns, gdn::kWaitLimitNs) | (uint64_t(role) << 56));
 }

@@ -448,6 +448,14 @@ int gdn_tree_accept(const gdn_dims *dims, int vocab, const float *p, int64_t p_s
  * path can be tested without a GPU fault. */
 void gdn_test_stall_next_verify(uint64_t wait_ns);
 
+/* The same for gdn_paged_attention: the next call that launches makes one role
+ * of its first CTA wait for wait_ns (capped at 2 s) on a barrier that nothing
+ * ever completes, then give up; the CTA's other roles wait out their own limits
+ * (about 2 s), drain and leave, and the call reports GDN_DEV_TIMEOUT.
+ *   role  0 softmax and results, 1 copies, 2 scores, 3 values' products,
+ *         4 cleaning of values; any other is ignored */
+void gdn_test_stall_next_attention(uint64_t wait_ns, int role);
+
 /* Name of a host or device status code ("GDN_OK", "GDN_DEV_DUP_SLOT", ...);
  * "unknown" for any other value.  Never NULL. */
 const char *gdn_status_str(int code);
