@@ -5,18 +5,25 @@
 // Mathematics.  One pass over the positions with a running reference m and sum l:
 //     p_x = 2^(c s_x - m),  l += p_x,  O += p_x v_x,   c = scale log2(e)
 // where m is the largest c s of the first tile that the row sees, or of the tile for
-// which it was last moved.  It is moved (l and O scaled by 2^(m - m')) only when p
-// would pass 2^8: until then p is in the range of either 16-bit type, and a scale costs
+// which it was last moved, less kLift.  It is moved (l and O scaled by 2^(m - m')) only
+// when p would pass 2^kMoveAt: until then p is in the type's range, and a scale costs
 // no precision in a floating type.  With one warpgroup (D = 256) the exponentials are
 // formed without a look at the maximum, which would stand before all of them in the
-// longest chain of the kernel; a tile whose p sum to more than 64 2^8 has its m moved
-// and its p formed again.  (With two, keeping the scores for that costs registers that
-// spill: 270 -> 330 us for chunks of up to 701 tokens at D = 128.)  Parts of a row's
-// positions are joined by the same rule: o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// longest chain of the kernel; a tile whose p sum to more than kMoveAtSum (so one p
+// alone may reach that) has its m moved and its p formed again.  (With two, keeping the
+// scores for that costs registers that spill: 270 -> 330 us for chunks of up to 701
+// tokens at D = 128.)  Parts of a row's positions are joined by the same rule:
+// o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // Rounding.  The products run on the tensor cores with 16-bit operands and fp32
-// accumulators, so p is rounded to the cache's type before P V (a relative half
-// step of that type, as the result's own rounding); l sums the unrounded p.
+// accumulators, so p is rounded to the cache's type before P V: a relative half
+// step of that type, as the result's own rounding; l sums the unrounded p.  bf16 has
+// fp32's range.  fp16 has steps of 2^-24 below 2^-14, so its range is used from the
+// top: the largest p of a row is 2^8 at least (kLift) and 2^15.9 at most, weights down
+// to 2^-22 of the largest keep their relative half step, and smaller ones are off by
+// 2^-33 of it at most.  (16,384 positions that stand 18 nats below one other with a
+// hundredth of their value: 9 to 17 times the roundings' bound with m at the maximum
+// itself, 0.3 to 0.4 of it so; chunks of up to 701 tokens in fp16 262 and 265 us.)
 //
 // Work.  The h_q / h_kv heads that share a key/value head are rows of one tile:
 // row r is (token i0 + r / G, head r % G), 128 / G tokens a tile, so keys and
@@ -70,7 +77,14 @@ namespace {
 namespace att {
 
 constexpr int kRows = 128;
-constexpr float kMoveAt = 8.f, kMoveAtSum = 256.f;  // m moves when a p passes 2^8, or a tile's sum 64 times that
+// m: log2 of the largest p when it is chosen, and of the p (or, for D = 256, the sum of a tile's p) that moves it.
+// A tile of equal scores right after a move sums to 64 2^kLift, below kMoveAtSum.
+template <typename T> struct Reference {
+    static constexpr float kLift = 0.f, kMoveAt = 8.f, kMoveAtSum = 16384.f;
+};
+template <> struct Reference<__half> {  // up to 65504
+    static constexpr float kLift = 8.f, kMoveAt = 15.9f, kMoveAtSum = 61000.f;
+};
 constexpr int TK = 64;       // positions of a tile
 // What an item costs beside its tiles (Q in, results out), in tiles.  Too little makes the CTAs with many
 // short items the last (chunks of up to 701 tokens: 4 289 us, 8 263, 10 266; 64 trees 122.6, 119.5, 120.6),
@@ -358,6 +372,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                            const att::Args a) {
     using namespace att;
     using C = Cfg<D>;
+    using Ref = Reference<T>;
     constexpr int kThreads = C::kThreads, kTma = C::kTma;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
@@ -860,11 +875,11 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                         const float2 s2 = gdn::f2unpack(gdn::add2(gdn::add2(sum[0], sum[1]), gdn::add2(sum[2], sum[3])));
                         return s2.x + s2.y;
                     };
-                    // m moves to the tile's maximum where `move` says so; O may be scaled once this warpgroup's
-                    // product before this one has added to it
+                    // m moves to what the tile's maximum asks for where `move` says so; O may be scaled once this
+                    // warpgroup's product before this one has added to it
                     auto move_to = [&](float mx, bool move) {
-                        const float f = move ? exp2_approx(m - mx) : 1.f;
-                        if (move) m = mx;
+                        const float f = move ? exp2_approx(m - (mx - Ref::kLift)) : 1.f;
+                        if (move) m = mx - Ref::kLift;
                         l *= f;
                         if (done == 0) return true;
                         const long long pr = it - C::kStreams;
@@ -883,18 +898,18 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
                     };
                     if (C::kStreams == 2) {
                         const float mx = tile_max();
-                        if (m == -INFINITY) m = mx;
-                        const bool move = mx > m + kMoveAt;
+                        if (m == -INFINITY) m = mx - Ref::kLift;
+                        const bool move = mx > m + Ref::kMoveAt;
                         if (__any_sync(full, move)) ok = move_to(mx, move);
                         if (!ok) break;
                         l += weights();
                     } else {
                         if (__any_sync(full, m == -INFINITY)) {  // the first positions that the row sees
                             const float mx = tile_max();
-                            if (m == -INFINITY) m = mx;
+                            if (m == -INFINITY) m = mx - Ref::kLift;
                         }
                         float sum = weights();
-                        const bool move = sum > 64.f * kMoveAtSum;
+                        const bool move = sum > Ref::kMoveAtSum;
                         if (__any_sync(full, move)) {
                             ok = move_to(tile_max(), move);
                             if (!ok) break;

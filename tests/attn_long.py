@@ -125,7 +125,7 @@ class Call:
         return m
 
     def exact(self, s):
-        """Sequence s in 64 bits: o and sum p |v|, [new][hq][d] each, and the largest scale * sum |q k|."""
+        """Sequence s in 64 bits: o, sum p |v| and sum |v|, [new][hq][d] each, and the largest scale * sum |q k|."""
         gr, rows, seen = self.hq // self.hkv, self.rows(s), self.seen(s)
         a, b = int(self.off[s]), int(self.off[s + 1])
         q = self.q[a:b].double().view(b - a, self.hkv, gr, self.d).permute(1, 2, 0, 3)  # [hkv][gr][new][d]
@@ -135,24 +135,25 @@ class Call:
         big = float((q.abs() @ k.abs().transpose(2, 3) * self.scale).masked_fill(hide, 0.0).max())
         p = torch.softmax(x, -1)
         back = lambda t: t.permute(2, 0, 1, 3).reshape(b - a, self.hq, self.d)
-        return back(p @ v), back(p @ v.abs()), big
+        return back(p @ v), back(p @ v.abs()), back(seen.double() @ v.abs().expand(-1, gr, -1, -1)), big
 
     def check(self, o, seqs=None, terms=None):
         """Every output within its roundings of the 64-bit result; the largest share of the tolerance used.
         One rounding to the type is half a step h.  Weights and results are rounded once each; a score is off by
         2^-24 of its `terms` products at most (ds), a weight by twice that; sums of 16 positions are added in fp32
         with an error of a whole step (2^-23) at most, n / 16 of them one after the other, in O and in l; 2^-16 for
-        the exponential and the joining of parts; an fp16 result below the normal range has a step of 2^-24."""
+        the exponential and the joining of parts.  An fp16 weight is 2^8 at least for the largest score, so the step
+        below the normal range, 2^-24, is 2^-32 of that, and half of it counts; a result there has that step too."""
         h, worst = R.half_step(self.dtype), 0.0
         for s in seqs if seqs is not None else range(len(self.new)):
             if self.new[s] == 0:
                 continue
-            ref, A, big = self.exact(s)
+            ref, A, V, big = self.exact(s)
             ds = (terms or self.d) * 2.0 ** -24 * big
             steps = 2 * (self.ctx[s] + self.new[s]) / 16 * 2.0 ** -23
             tol = h * ref.abs() + (h + 2 * ds + steps + 2.0 ** -16) * A + 1e-30
             if self.dtype == torch.float16:
-                tol += 2.0 ** -25
+                tol += 2.0 ** -33 * V + 2.0 ** -25
             got = o[int(self.off[s]):int(self.off[s + 1])].double()
             assert torch.isfinite(got).all(), s
             worst = max(worst, float(((got - ref).abs() / tol).max()))

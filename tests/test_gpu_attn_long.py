@@ -41,3 +41,28 @@ def test_rows_of_a_warp_go_other_ways(name, d, hq, hkv, page, tree):
     assert not torch.isfinite(dirty[~free][..., 3]).any()
     other = [c for c in range(d) if c != 3]
     assert torch.equal(dirty[..., other], clean[..., other])
+
+
+@pytest.mark.parametrize("d", [256, 128, 64])
+@pytest.mark.parametrize("name", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [10.0, 16.0, 18.0])
+def test_weights_far_below_the_largest(name, d, gap):
+    """The first key of a long context stands `gap` (nats) above 16,384 others, as a sequence's first token may, and
+    its value is a hundredth of theirs: the small weights carry a share of the result that no type may lose.  One
+    sequence a CTA, all over the same pages, so that one running maximum holds for all of them."""
+    S = torch.cuda.get_device_properties(0).multi_processor_count
+    pages = np.random.default_rng(0).permutation(259)[:257]
+    a = Call(5, name, d, 8, 1, 64, [16384] * S, [1] * S, pages_of=[pages] * S, n_pages=259)
+    assert a.reached()["longest"] >= 257
+    g = torch.Generator(device="cuda").manual_seed(6)
+    a.q.zero_()
+    a.q[..., 0] = gap * d ** 0.5
+    a.q[..., 1:8] = (torch.randn((a.N, 8, 7), generator=g, device="cuda") * 0.2 * d ** 0.5).to(a.dtype)
+    rows = a.rows(0)
+    a.k[rows] = 0.0
+    a.k[rows, :, 1:8] = torch.randn((len(rows), 1, 7), generator=g, device="cuda").to(a.dtype)
+    a.k[rows[0]] = 0.0
+    a.k[rows[0], :, 0] = 1.0
+    a.v[rows] = (0.5 + torch.rand((len(rows), 1, d), generator=g, device="cuda")).to(a.dtype)
+    a.v[rows[0]] = 0.01
+    a.check(a.out(), terms=8)
