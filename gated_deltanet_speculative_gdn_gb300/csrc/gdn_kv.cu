@@ -119,6 +119,21 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const KvArgs a) {
     }
 }
 
+// Whether no two layers share a row: a thread moves its layer's rows in place, so a row of another layer must not
+// be among them.  What has a smaller stride than the layers' lies within it, what has a larger one beyond all layers.
+bool layers_apart(const gdn_attn_dims *d, int n_layers, int64_t layer_stride) {
+    const int64_t stride[3] = {d->page_stride, d->token_stride, d->head_stride};
+    const int64_t count[3] = {d->n_pages, d->page_size, d->h_kv};
+    double span = d->d_head;  // (an int64 may not hold what dims of no real cache give)
+    for (int k = 0; k < 3; ++k)
+        if (count[k] > 1 && stride[k] < layer_stride) span += double(count[k] - 1) * double(stride[k]);
+    if (double(layer_stride) < span) return false;
+    span += double(n_layers - 1) * double(layer_stride);
+    for (int k = 0; k < 3; ++k)
+        if (count[k] > 1 && stride[k] >= layer_stride && double(stride[k]) < span) return false;
+    return true;
+}
+
 }  // namespace
 
 extern "C" int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const int32_t *accepted,
@@ -134,7 +149,8 @@ extern "C" int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t la
     if (S == 0 || n_layers == 0) return GDN_OK;
     if (!accepted || !node_off || !ctx_len || !page_table || !k_pool || !v_pool || !new_len || (N > 0 && !parents))
         return GDN_ERR_NULL;
-    if (layer_stride < 0 || layer_stride % 8 != 0) return GDN_ERR_STRIDE;
+    if (layer_stride < 0 || layer_stride % 8 != 0 || layer_stride > (int64_t(1) << 38)) return GDN_ERR_STRIDE;
+    if (n_layers > 1 && !layers_apart(dims, n_layers, layer_stride)) return GDN_ERR_STRIDE;
     if (!gdn::aligned16(k_pool) || !gdn::aligned16(v_pool)) return GDN_ERR_ALIGN;
     const size_t pool = size_t(layer_stride) * 2 * size_t(n_layers - 1) + gdn::pool_bytes(dims);
     const gdn::Span ins[] = {{accepted, size_t(S * 4)},

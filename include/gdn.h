@@ -389,6 +389,9 @@ size_t gdn_attention_workspace_bytes(const gdn_attn_dims *dims);
  *   max_seq_tokens <= 64; h_q is not used (give h_kv)
  *   accepted [S], parents [N], node_off, ctx_len, page_table in; new_len [S] out
  *            (must not overlap ctx_len); layer_stride a multiple of 8
+ *            and, for several layers, one that keeps their rows apart: whole pools
+ *            one after the other, or layers between the pages, tokens or heads
+ * Host errors: GDN_ERR_STRIDE also for layers that share rows.
  * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_ACCEPTED,
  * GDN_DEV_BAD_PARENT, GDN_DEV_BAD_LEN, GDN_DEV_BAD_PAGE. */
 int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
