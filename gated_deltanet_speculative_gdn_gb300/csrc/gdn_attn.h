@@ -33,6 +33,24 @@ inline size_t rows_bytes16(int64_t rows, int64_t stride, int64_t width) {
     return rows <= 0 ? 0 : static_cast<size_t>(((rows - 1) * stride + width) * 2);
 }
 
+// Rows of `width` 16-bit elements, `stride` apart.
+struct Rows16 {
+    const void *p;
+    int64_t stride, width;
+};
+inline Span span(const Rows16 &r, int64_t rows) { return {r.p, rows_bytes16(rows, r.stride, r.width)}; }
+
+// Whether two sets of as many rows share a byte.  With one stride, so columns of one buffer as a rule, their places
+// within a stride say so; with two the spans from the first row to the last must be apart.
+inline bool rows_overlap(const Rows16 &a, const Rows16 &b, int64_t rows) {
+    if (!overlaps(span(a, rows), span(b, rows))) return false;
+    if (a.stride != b.stride) return true;
+    const int64_t s = 2 * a.stride;
+    int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % s;
+    if (at < 0) at += s;  // b's place within a's stride
+    return at < 2 * a.width || at + 2 * b.width > s;
+}
+
 inline size_t pool_bytes(const gdn_attn_dims *d) {
     return static_cast<size_t>((int64_t(d->n_pages - 1) * d->page_stride + int64_t(d->page_size - 1) * d->token_stride +
                                 int64_t(d->h_kv - 1) * d->head_stride + d->d_head) * 2);

@@ -233,10 +233,10 @@ extern "C" int gdn_rope_append(const gdn_attn_dims *dims, const void *q, int64_t
         (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
         return GDN_ERR_ALIGN;
     const size_t pool = gdn::pool_bytes(dims);
-    const gdn::Span qs{q, gdn::rows_bytes16(N, q_stride, Hq * D)}, qos{q_out, gdn::rows_bytes16(N, q_out_stride, Hq * D)};
-    const gdn::Span ins[] = {{k, gdn::rows_bytes16(N, k_stride, Hkv * D)},
-                             {v, gdn::rows_bytes16(N, v_stride, Hkv * D)},
-                             {q_norm_w, size_t(D * 4)},
+    const gdn::Rows16 qr{q, q_stride, Hq * D}, kr{k, k_stride, Hkv * D}, vr{v, v_stride, Hkv * D},
+        qor{q_out, q_out_stride, Hq * D};
+    const gdn::Span qos = gdn::span(qor, N);
+    const gdn::Span ins[] = {{q_norm_w, size_t(D * 4)},
                              {k_norm_w, size_t(D * 4)},
                              {pos, size_t(N * n_axes * 4)},
                              {inv_freq, size_t(rot_dim * 4)},
@@ -247,9 +247,12 @@ extern "C" int gdn_rope_append(const gdn_attn_dims *dims, const void *q, int64_t
                              {status, 4}};
     // the pools may interleave, so they are not checked against each other
     const gdn::Span ko[] = {{k_pool, pool}, qos}, vo[] = {{v_pool, pool}, qos};
-    if ((rc = gdn::check_alias(ko, 2, ins, 11)) || (rc = gdn::check_alias(vo, 2, ins, 11))) return rc;
-    if (gdn::overlaps(qs, ko[0]) || gdn::overlaps(qs, vo[0])) return GDN_ERR_ALIAS;
-    if (gdn::overlaps(qs, qos) && !(q == q_out && q_stride == q_out_stride)) return GDN_ERR_ALIAS;
+    if ((rc = gdn::check_alias(ko, 2, ins, 9)) || (rc = gdn::check_alias(vo, 2, ins, 9))) return rc;
+    for (const gdn::Rows16 &r : {qr, kr, vr})
+        if (gdn::overlaps(gdn::span(r, N), ko[0]) || gdn::overlaps(gdn::span(r, N), vo[0])) return GDN_ERR_ALIAS;
+    // q, k, v and q_out may be columns of one buffer, so their rows are looked at, not the spans from first to last
+    if (gdn::rows_overlap(qor, kr, N) || gdn::rows_overlap(qor, vr, N)) return GDN_ERR_ALIAS;
+    if (gdn::rows_overlap(qor, qr, N) && !(q == q_out && q_stride == q_out_stride)) return GDN_ERR_ALIAS;
 
     // a token's rows are shared by as many warps as it takes to fill the GPU
     // when there are few tokens; a warp with all rows of a token forms the

@@ -339,7 +339,8 @@ typedef struct {
  *   pos      [N][n_axes] int32;  inv_freq [rot_dim / 2] fp64
  *   axis     [rot_dim / 2] int32, or NULL (axis 0);  n_axes 1..4
  *   rot_dim  a multiple of 16, 0 .. d_head (0: no rotation)
- *   q_out    [N][q_out_stride] out; may be q itself with the same stride
+ *   q_out    [N][q_out_stride] out; may be q itself with the same stride.  q, k, v
+ *            and q_out may be columns of one buffer, with its row as their stride
  * Host errors: GDN_ERR_ARG for eps, n_axes, rot_dim or interleaved.
  * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_LEN, GDN_DEV_BAD_PAGE (the
  * token's k and v are not written), GDN_DEV_BAD_AXIS. */

@@ -54,3 +54,54 @@ def test_move_with_layers_anywhere(order):
     torch.cuda.synchronize()
     assert int(status) == 0 and nl.tolist() == lens
     assert torch.equal(kg.cpu(), want[0]) and torch.equal(vg.cpu(), want[1])
+
+
+@pytest.mark.parametrize("case", ["one buffer in place", "one buffer to its end", "into the gaps of another", "k | v | q"])
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_from_one_buffer(case, norm):
+    """q, k and v as columns of one projection's output, in place or beside it: the bits of separate tensors."""
+    d, hq, hkv, page, dtype = 64, 6, 2, 8, torch.bfloat16
+    rng = np.random.default_rng(1)
+    ctx, new = [3, 0, 30], [5, 1, 17]
+    N, wq, wk = sum(new), hq * d, hkv * d
+    cache = R.make_cache(rng, [a + b for a, b in zip(ctx, new)], hkv, d, page, dtype, garbage=1.0)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn((N, w), generator=g, device="cuda").to(dtype) for w in (wq, wk, wk))
+    w = 1 + 0.1 * torch.randn(d, generator=g, device="cuda") if norm else None
+    dm = G.AttnDims.make(3, N, max(new), hq, hkv, d, G.GDN_BF16, cache.n_pages, page, cache.table.shape[1], *cache.strides)
+    half = 16
+    inv_freq = torch.tensor([1e4 ** (-i / half) for i in range(half)], dtype=torch.float64, device="cuda")
+    pos, off, lens, table = i32(rng.integers(0, 5000, (N, 1))), i32(np.concatenate([[0], np.cumsum(new)])), i32(ctx), i32(cache.table)
+
+    def append(qt, qs, kt, ks, vt, vs, qo, qos):
+        kp, vp, status = cache.k.cuda(), cache.v.cuda(), i32([0])
+        G.gdn_rope_append(dm, qt, qs, kt, ks, vt, vs, w, w, 1e-6, pos, 1, inv_freq, None, 2 * half, 0, off, lens, table, qo, qos,
+                          kp, vp, status)
+        torch.cuda.synchronize()
+        assert int(status) == 0
+        return kp, vp
+
+    want_q = torch.empty_like(q)
+    want = append(q, wq, k, wk, v, wk, want_q, wq)
+    order = (k, v, q) if case == "k | v | q" else (q, k, v)
+    row = torch.cat([*order, torch.full((N, wq + 8), 7.0, dtype=dtype, device="cuda")], 1)
+    stride, before = row.stride(0), row.clone()
+    at, starts = 0, {}
+    for t in order:
+        starts[id(t)] = at
+        at += t.shape[1]
+    part = lambda t: row[:, starts[id(t)]:]
+    if case == "one buffer to its end":
+        out, first = row, at
+    elif case == "into the gaps of another":
+        out, first = row, at + 8
+    else:
+        out, first = row, starts[id(q)]
+    qt, qs = (q, wq) if case == "into the gaps of another" else (part(q), stride)
+    got = append(qt, qs, part(k), stride, part(v), stride, out[:, first:], stride)
+    assert torch.equal(out[:, first:first + wq], want_q)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    rest = torch.ones(row.shape[1], dtype=torch.bool)
+    rest[first:first + wq] = False
+    assert torch.equal(row[:, rest], before[:, rest])
