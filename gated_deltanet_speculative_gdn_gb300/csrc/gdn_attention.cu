@@ -57,10 +57,10 @@
 //           are set to 0 and remembered, since 0 * NaN in P V would reach rows that
 //           do not see them; rows that do get them back at the end
 //
-// Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 182-188 us, 6.3-6.5 TB/s,
-// bound by HBM; 64 trees of 16 nodes over up to 8,192 114-120 us, 5.1-5.3 TB/s, HBM and the parts' way through
-// memory; 4,096 tokens over 12,288 positions 533-605 us, 1.6-1.8 PFLOP/s, tensor cores under the power cap; one
-// token over 777 positions 13 us, latency.
+// Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 189 us, 6.3 TB/s, bound by HBM;
+// 64 trees of 16 nodes over up to 8,192 122 us, 5.0 TB/s, HBM and the parts' way through memory; 4,096 tokens over
+// 12,288 positions 533-610 us, 1.6-1.8 PFLOP/s, tensor cores under the power cap; one token over 777 positions
+// 14 us, latency.
 //
 // Every mbarrier completes once per use, so a counter gives every wait's phase; a
 // wait is only ever for the next completion that the waiter has not seen.
@@ -139,7 +139,6 @@ struct Args {
     float *parts;  // [CTA][2][part]
     int4 *meta;    // [CTA][2]: rows of the part (0: none), ends, token n0 + i0, key/value head
     int S, N, max_tokens, Hq, Hkv, G, R;  // R: tokens of a row tile
-    int once;                             // no sequence has more than one row tile
     uint64_t stall_ns;                    // test hook: a warp of CTA 0 waits for what never comes, so long (0: none)
     int stall_role;                       // 0 rows, 1 copies, 2 scores, 3 P V, 4 cleaning
 };
@@ -296,25 +295,14 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lead)
     return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(lead >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-// `leave`: the data are the first to leave L2
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int row, int chunk, int head, int page,
-                                            uint64_t *bar, bool leave) {
-    if (leave)
-        asm volatile(
-            "{\n\t.reg .b64 pol;\n\t"
-            "createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
-            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-            " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], pol;\n\t}" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(head), "r"(page),
-            "r"(gdn::smem_addr(bar))
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(head), "r"(page),
-            "r"(gdn::smem_addr(bar))
-            : "memory");
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(head), "r"(page),
+        "r"(gdn::smem_addr(bar))
+        : "memory");
 }
 // Warp-collective: thread t writes 32 columns (words) of lane (taddr lane) + t.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -504,11 +492,9 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
         const bool box_lane = bb < np;
         const uint32_t bytes = pages ? min(ps, TK) * 128u * C::kChunks : ps * 128u;
         const uint32_t dst = pages ? bb * bytes : bc * C::kChunkBytes + uint32_t(bb) * ps * 128u;
-        // Keys and values that are read once, and are more than L2 holds, are the first to leave it: the parts
-        // that the second kernel joins stay (64 trees over up to 8192 positions 121.4 -> 114.5 us).  Read by
-        // several row tiles they stay as long as others (a prompt's chunk 554 us, 660 if they were to leave).
-        // For D <= 128 the choice costs the loads of short items more than it gives (mixed chunks 262 -> 282 us).
-        const bool leave = D == 256 && a.once && total * (2 * C::kTile) > (96ll << 20);
+        // (Loads whose data are the first to leave L2, so that the parts stay there, gave 64 single tokens 185 for
+        // 189 us and 64 trees 120 for 122, but where sequences share a prefix's pages, which no argument tells, cost
+        // 306 for 291 us over 32,768 shared positions and 109 for 106 over 8,192.)
         int stage = 0;
         uint32_t phase = 0;
         long long issued = 0;
@@ -519,7 +505,7 @@ __global__ void __launch_bounds__(att::Cfg<D>::kThreads, 1)
             const unsigned m = __ballot_sync(full, mine);
             if (lane == 0) gdn::mbar_arrive_expect_tx(full_bar + stage, __popc(m) * bytes);
             __syncwarp();
-            if (mine) tma_load_5d(tb + stage * C::kTile + dst, map, row, bc, head, page, full_bar + stage, D == 256 && leave);
+            if (mine) tma_load_5d(tb + stage * C::kTile + dst, map, row, bc, head, page, full_bar + stage);
             ++issued;
             if (++stage == C::kStages) {
                 stage = 0;
@@ -1262,7 +1248,7 @@ extern "C" int gdn_paged_attention(const gdn_attn_dims *dims, const void *q, int
     const int G = int(Hq / dims->h_kv);
     att::Args a{q, q_stride, v_pool, gdn::paged_layout(dims, page_table), ctx_len, node_off, parents,
                 scale * 1.4426950408889634f, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens, int(Hq),
-                dims->h_kv, G, att::kRows / G, dims->max_seq_tokens <= att::kRows / G, 0, 0};
+                dims->h_kv, G, att::kRows / G, 0, 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dims->dtype == GDN_BF16 ? launch_d<__nv_bfloat16>(dims, k_pool, a, workspace, ctas, st)
                                    : launch_d<__half>(dims, k_pool, a, workspace, ctas, st);

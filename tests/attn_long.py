@@ -128,14 +128,15 @@ class Call:
         """Sequence s in 64 bits: o, sum p |v| and sum |v|, [new][hq][d] each, and the largest scale * sum |q k|."""
         gr, rows, seen = self.hq // self.hkv, self.rows(s), self.seen(s)
         a, b = int(self.off[s]), int(self.off[s + 1])
-        q = self.q[a:b].double().view(b - a, self.hkv, gr, self.d).permute(1, 2, 0, 3)  # [hkv][gr][new][d]
-        k, v = (p[rows].double().permute(1, 0, 2)[:, None] for p in (self.k, self.v))   # [hkv][1][L][d]
-        hide = ~seen
-        x = (q @ k.transpose(2, 3) * self.scale).masked_fill(hide, float("-inf"))
-        big = float((q.abs() @ k.abs().transpose(2, 3) * self.scale).masked_fill(hide, 0.0).max())
+        n = b - a
+        q = self.q[a:b].double().view(n, self.hkv, gr, self.d).permute(1, 2, 0, 3).reshape(self.hkv, gr * n, self.d)
+        k, v = (p[rows].double().transpose(0, 1) for p in (self.k, self.v))   # [hkv][L][d]
+        hide = ~seen.repeat(gr, 1)
+        x = (q @ k.transpose(1, 2) * self.scale).masked_fill(hide, float("-inf"))
+        big = float((q.abs() @ k.abs().transpose(1, 2) * self.scale).masked_fill(hide, 0.0).max())
         p = torch.softmax(x, -1)
-        back = lambda t: t.permute(2, 0, 1, 3).reshape(b - a, self.hq, self.d)
-        return back(p @ v), back(p @ v.abs()), back(seen.double() @ v.abs().expand(-1, gr, -1, -1)), big
+        back = lambda t: t.view(self.hkv, gr, n, self.d).permute(2, 0, 1, 3).reshape(n, self.hq, self.d)
+        return back(p @ v), back(p @ v.abs()), back((seen.double() @ v.abs()).repeat(1, gr, 1)), big
 
     def check(self, o, seqs=None, terms=None):
         """Every output within its roundings of the 64-bit result; the largest share of the tolerance used.

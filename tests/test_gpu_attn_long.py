@@ -66,3 +66,23 @@ def test_weights_far_below_the_largest(name, d, gap):
     a.v[rows] = (0.5 + torch.rand((len(rows), 1, d), generator=g, device="cuda")).to(a.dtype)
     a.v[rows[0]] = 0.01
     a.check(a.out(), terms=8)
+
+
+@pytest.mark.parametrize("name,d,hq,hkv,page,tree", [
+    ("bf16", 256, 16, 2, 32, True), ("fp16", 256, 16, 2, 64, False), ("fp16", 128, 8, 2, 16, False),
+    ("bf16", 64, 8, 4, 8, True)])
+def test_sequences_that_share_the_pages_of_a_prefix(name, d, hq, hkv, page, tree):
+    """48 sequences over one prefix of 4,096 positions, each with up to 150 of its own."""
+    S, pre, rng = 48, 4096, np.random.default_rng(d)
+    own, new = rng.integers(0, 150, S), rng.integers(1, 20, S)
+    need = [-(-(int(a) + int(b)) // page) for a, b in zip(own, new)]
+    perm, at, pages = rng.permutation(pre // page + sum(need)), pre // page, []
+    for k in need:
+        pages.append(np.concatenate([perm[:pre // page], perm[at:at + k]]))
+        at += k
+    a = Call(9, name, d, hq, hkv, page, pre + own, new, tree, pages_of=pages, n_pages=len(perm))
+    r = a.reached()
+    assert r["tiles"] >= 24 and r["both"] >= 1, r
+    o = a.out()
+    a.check(o)
+    assert torch.equal(a.out(), o)
