@@ -52,27 +52,34 @@ class Call:
     entries past a sequence's pages are out of range.  `pages_of` gives each sequence its pages (None: pages
     of its own in random order)."""
 
-    def __init__(self, seed, name, d, hq, hkv, page, ctx, new, tree=False, pages_of=None, n_pages=None, q_std=1.0):
+    def __init__(self, seed, name, d, hq, hkv, page, ctx, new, tree=False, pages_of=None, n_pages=None, q_std=1.0,
+                 table=None):
         self.dtype, self.d, self.hq, self.hkv, self.page = R.DTYPES[name], d, hq, hkv, page
         self.ctx, self.new = [int(x) for x in ctx], [int(x) for x in new]
         rng = np.random.default_rng(seed)
         g = torch.Generator(device="cuda").manual_seed(seed)
         need = [-(-(a + b) // page) for a, b in zip(self.ctx, self.new)]
-        if pages_of is None:
+        if table is not None:
+            pages_of = table
+        elif pages_of is None:
             n_pages = sum(need) + 2
             perm, at, pages_of = rng.permutation(n_pages), 0, []
             for k in need:
                 pages_of.append(perm[at:at + k])
                 at += k
-        width = max(need) + 1
-        table = np.full((len(need), width), n_pages + 1000, dtype=np.int32)
-        for s, k in enumerate(need):
-            table[s, :k] = pages_of[s][:k]
-        self.table_np, self.n_pages = table, n_pages
-        self.table = torch.from_numpy(table).cuda()
+        dense = table is not None
+        if dense:
+            width = table.shape[1]
+        else:
+            width = max(need) + 1
+            table = np.full((len(need), width), n_pages + 1000, dtype=np.int32)
+            for s, k in enumerate(need):
+                table[s, :k] = pages_of[s][:k]
+        self.table = torch.from_numpy(np.ascontiguousarray(table, dtype=np.int32)).cuda()
         shape = (n_pages * page, hkv, d)
         self.k, self.v = (torch.full(shape, float("nan"), dtype=self.dtype, device="cuda") for _ in range(2))
-        rows = torch.unique(torch.cat([self.rows(s) for s in range(len(need)) if need[s]]))
+        rows = (torch.arange(n_pages * page, device="cuda") if dense else
+                torch.unique(torch.cat([self.rows(s) for s in range(len(need)) if need[s]])))
         for pool in (self.k, self.v):
             for part in rows.split(1 << 16):
                 pool[part] = torch.randn((len(part), hkv, d), generator=g, device="cuda").to(self.dtype)
