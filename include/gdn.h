@@ -300,6 +300,8 @@ int gdn_decode_step(const gdn_dims *dims, const float *x, int64_t x_stride, cons
  *   gdn_paged_attention  reads them together with the context
  *   gdn_kv_commit        once acceptance is known, moves the accepted path's
  *                        keys and values to positions ctx_len[s] + 0, 1, ...
+ * Positions from ctx_len[s] on are written: their pages belong to s alone.  Pages
+ * that hold only earlier positions may be in any number of sequences' tables.
  * 16-bit tensors hold bf16 or fp16 (dims->dtype).  Both pools have the same
  * strides, in elements, so a cache of [page][token][head][d], of
  * [page][head][token][d] or one that interleaves keys and values all work. */
@@ -331,8 +333,10 @@ typedef struct {
  * d_head - rot_dim other elements keep y.  q rows go to q_out, k rows and the
  * plain v rows to the pools.  A token has n_axes positions (time, height, width
  * of an image's patches, say); `axis` gives each frequency its axis, so sections
- * and interleaved layouts are both a table.  Angles are exact to 2^-53 of
- * inv_freq for any int32 position.
+ * and interleaved layouts are both a table.  For any int32 position an angle is
+ * off by |pos| (inv_freq + 1) 2^-64 + 2^-26 + 2^-32 turns at most: inv_freq / 2 pi is
+ * held to 2^-64, the product modulo a turn is exact and is cut to 32 bits and rounded
+ * to fp32.
  *   q [N][q_stride], k [N][k_stride], v [N][v_stride]   in, 16-bit, strides in
  *            elements, multiples of 8
  *   q_norm_w, k_norm_w  [d_head] fp32, or NULL
@@ -386,7 +390,8 @@ size_t gdn_attention_workspace_bytes(const gdn_attn_dims *dims);
  *     position ctx_len[s] + j  <-  position ctx_len[s] + p_j        j = 0 .. m - 1
  * in k_pool and v_pool, and new_len[s] = ctx_len[s] + m.  accepted[s] = -1 moves
  * nothing (m = 0).  As for gdn_commit, a preflight checks every sequence first;
- * if a check fails, or *status is already non-zero, nothing is written.
+ * if a check fails, or *status is already non-zero, nothing is written.  With
+ * n_layers = 0, as with n_seqs = 0, nothing is enqueued and new_len is not written.
  *   max_seq_tokens <= 64; h_q is not used (give h_kv)
  *   accepted [S], parents [N], node_off, ctx_len, page_table in; new_len [S] out
  *            (must not overlap ctx_len); layer_stride a multiple of 8
@@ -415,14 +420,16 @@ int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
  * child is tried).  When no child is left the next token is drawn
  * from that residual (from p[t] itself when its sum is 0): the first y whose
  * cumulative sum passes u_next[s] times the total.  The tokens that come out are
- * distributed as the target's.  c and Z carry at least 44 bits, W and the sums
- * 2^-48 of a distribution's mass.
+ * distributed as the target's.  W, Z and the sums are good to 2^-48 of a
+ * distribution's mass, and with them c to about 2^-48 (1 + W / Z) / Z a rejection.
  *   replacement  0: as above.  1: the draft draws children independently (Z
  *            stays 1 and nothing is taken out)
  *   q        NULL: the children are proposed outright (q[t][y] = 1 for them;
  *            the residual is p without the rejected tokens, W <- W - p[t][y])
  *   dims     n_seqs, n_nodes, max_seq_nodes (the GDN layers' dims as they are)
- *   p [N][p_stride], q [N][q_stride]   fp32 rows of `vocab` probabilities
+ *   p [N][p_stride], q [N][q_stride]   fp32 rows of `vocab` probabilities; strides
+ *            multiples of 4 and at least vocab rounded up to one (a dense row of
+ *            50003 takes 50004); what a row holds past vocab is not used
  *   tokens [N] (node 0's is not read), parents, node_off, u [N], u_next [S]  in
  *   accepted [S]   deepest accepted node (-1 for a sequence without nodes): the
  *                  argument of gdn_commit and gdn_kv_commit

@@ -105,3 +105,12 @@ def test_append_from_one_buffer(case, norm):
     rest = torch.ones(row.shape[1], dtype=torch.bool)
     rest[first:first + wq] = False
     assert torch.equal(row[:, rest], before[:, rest])
+
+
+def test_no_layers_write_nothing():
+    dm = G.AttnDims.make(2, 8, 4, 2, 2, 64, G.GDN_BF16, 4, 8, 2)
+    pool, nl, status = torch.ones(4 * 8 * 2 * 64, dtype=torch.bfloat16, device="cuda"), i32([-7, -7]), i32([0])
+    assert G.gdn_kv_commit(dm, 0, 0, i32([3, 3]), i32([-1, 0, 1, 2] * 2), i32([0, 4, 8]), i32([1, 2]), i32([[0, 1], [2, 3]]), pool,
+                           pool.clone(), nl, status) == G.GDN_OK
+    torch.cuda.synchronize()
+    assert nl.tolist() == [-7, -7] and int(status) == 0 and bool((pool == 1).all())
