@@ -57,8 +57,8 @@
 //           are set to 0 and remembered, since 0 * NaN in P V would reach rows that
 //           do not see them; rows that do get them back at the end
 //
-// Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 189 us, 6.3 TB/s, bound by HBM;
-// 64 trees of 16 nodes over up to 8,192 122 us, 5.0 TB/s, HBM and the parts' way through memory; 4,096 tokens over
+// Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 185-189 us, 6.3-6.4 TB/s, HBM;
+// 64 trees of 16 nodes over up to 8,192 119-122 us, 5.0-5.1 TB/s, HBM and the parts' way through memory; 4,096 tokens over
 // 12,288 positions 533-610 us, 1.6-1.8 PFLOP/s, tensor cores under the power cap; one token over 777 positions
 // 14 us, latency.
 //
@@ -77,8 +77,8 @@ namespace {
 namespace att {
 
 constexpr int kRows = 128;
-// m: log2 of the largest p when it is chosen, and of the p (or, for D = 256, the sum of a tile's p) that moves it.
-// A tile of equal scores right after a move sums to 64 2^kLift, below kMoveAtSum.
+// m: log2 of the largest p when it is chosen, log2 of the p that moves it and, for D = 256, the sum of a tile's p
+// that does.  A tile of equal scores right after a move sums to 64 2^kLift, below kMoveAtSum.
 template <typename T> struct Reference {
     static constexpr float kLift = 0.f, kMoveAt = 8.f, kMoveAtSum = 16384.f;
 };
@@ -88,7 +88,7 @@ template <> struct Reference<__half> {  // up to 65504
 constexpr int TK = 64;       // positions of a tile
 // What an item costs beside its tiles (Q in, results out), in tiles.  Too little makes the CTAs with many
 // short items the last (chunks of up to 701 tokens: 4 289 us, 8 263, 10 266; 64 trees 122.6, 119.5, 120.6),
-// too much those with few long ones (64 single tokens: 186.9, 187.0, 187.2; 24 191.1).
+// too much those with few long ones (64 single tokens: 186.9, 187.0, 187.2; 24 191.1).  Not measured for D = 64.
 constexpr int kItemUnits = 10;
 constexpr int kNfBufs = 16;  // the ring holds the values of 12 segments at most, and one may still be going out
 

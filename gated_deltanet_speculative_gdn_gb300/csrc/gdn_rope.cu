@@ -15,9 +15,10 @@
 // elements is a whole lane away (rot_dim is a multiple of 16), fetched by
 // shuffles.  The sines and cosines are formed once per token and warp and stay in
 // registers over its rows.  Each row is read and written once: 10,004 tokens of 16 + 2 + 2
-// rows of 256 take 44 us (4.6 TB/s of the copy's 6.8), held back by instruction issue (norm,
-// conversions, shuffles: ~100 a row) and the loads in flight of 24 warps an SM; more warps spill
-// (46 us), eight rows in flight a warp leave fewer warps (52 us).
+// rows of 256 take 45 us (4.5 TB/s of the copy's 6.8), held back by latency: a warp's look-ups,
+// angles and batches of rows follow one another, and no batch is requested before the last one
+// is stored.  (Issue slots are 56 % busy, and loads are what is waited for most.)  More warps
+// spill (46 us), eight rows in flight a warp leave fewer warps (52 us).
 #include "gdn_attn.h"
 
 namespace {
