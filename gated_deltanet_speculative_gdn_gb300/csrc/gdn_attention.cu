@@ -23,7 +23,8 @@
 // to 2^-22 of the largest keep their relative half step, and smaller ones are off by
 // 2^-33 of it at most.  (16,384 positions that stand 18 nats below one other with a
 // hundredth of their value: 9 to 17 times the roundings' bound with m at the maximum
-// itself, 0.3 to 0.4 of it so; chunks of up to 701 tokens in fp16 262 and 265 us.)
+// itself, 0.3 to 0.4 of it so.  Mixed chunks in fp16 took 262 us and take 265, trees in fp16 and
+// bf16 the same to 2 % with flat scores and with peaked ones.)
 //
 // Work.  The h_q / h_kv heads that share a key/value head are rows of one tile:
 // row r is (token i0 + r / G, head r % G), 128 / G tokens a tile, so keys and
@@ -57,9 +58,9 @@
 //           are set to 0 and remembered, since 0 * NaN in P V would reach rows that
 //           do not see them; rows that do get them back at the end
 //
-// Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 185-189 us, 6.3-6.4 TB/s, HBM;
+// Measured (16/2 heads of 256, bf16): 64 single tokens over up to 16,384 positions 184-189 us, 6.3-6.4 TB/s, HBM;
 // 64 trees of 16 nodes over up to 8,192 119-122 us, 5.0-5.1 TB/s, HBM and the parts' way through memory; 4,096 tokens over
-// 12,288 positions 533-610 us, 1.6-1.8 PFLOP/s, tensor cores under the power cap; one token over 777 positions
+// 12,288 positions 533-616 us, 1.56-1.8 PFLOP/s, tensor cores under the power cap; one token over 777 positions
 // 14 us, latency.
 //
 // Every mbarrier completes once per use, so a counter gives every wait's phase; a
