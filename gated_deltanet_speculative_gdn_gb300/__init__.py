@@ -31,12 +31,15 @@ GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_PARENT, GDN_DEV_BAD_SLOT = 1, 2, 3
 GDN_DEV_DUP_SLOT, GDN_DEV_BAD_ACCEPTED, GDN_DEV_TIMEOUT = 4, 5, 6
 GDN_DEV_BAD_WINDOW, GDN_DEV_BAD_PAGE, GDN_DEV_BAD_LEN = 7, 8, 9
 GDN_DEV_BAD_AXIS, GDN_DEV_BAD_TOKEN = 10, 11
-GDN_BF16, GDN_FP16 = 0, 1
+GDN_DEV_BAD_BIAS, GDN_DEV_BAD_MASK = 12, 13
+GDN_BF16, GDN_FP16, GDN_FP32 = 0, 1, 2
 
 EXPORTED_SYMBOLS = ("gdn_conv_tree_step", "gdn_tree_verify", "gdn_chain_verify", "gdn_commit",
                     "gdn_conv_tree_step_compact", "gdn_commit_compact", "gdn_gated_rmsnorm",
                     "gdn_decode_step", "gdn_rope_append", "gdn_paged_attention",
                     "gdn_attention_workspace_bytes", "gdn_kv_commit", "gdn_tree_accept",
+                    "gdn_kv4_block_bytes", "gdn_kv4_append", "gdn_kv4_read", "gdn_kv4_commit",
+                    "gdn_logits_probs", "gdn_token_commit",
                     "gdn_test_stall_next_verify", "gdn_test_stall_next_attention",
                     "gdn_status_str", "gdn_replay_row_floats")
 
@@ -77,6 +80,16 @@ class AttnDims(ctypes.Structure):
         return cls(n_seqs, n_tokens, max_seq_tokens, h_q, h_kv, d_head, dtype, n_pages, page_size, table_width,
                    page, token, head)
 
+    @classmethod
+    def make_kv4(cls, n_seqs, n_tokens, max_seq_tokens, h_q, h_kv, d_head, dtype, n_pages, page_size, table_width,
+                 page_stride=None, head_stride=None):
+        """Dims of a 4-bit cache: strides in bytes, by default those of a dense one of [page][head][block]."""
+        block = page_size * d_head // 16 * 9
+        head = block if head_stride is None else head_stride
+        page = h_kv * head if page_stride is None else page_stride
+        return cls(n_seqs, n_tokens, max_seq_tokens, h_q, h_kv, d_head, dtype, n_pages, page_size, table_width,
+                   page, 0, head)
+
 
 class GdnError(RuntimeError):
     def __init__(self, fn: str, code: int):
@@ -111,7 +124,17 @@ lib.gdn_attention_workspace_bytes.argtypes = [_AP]
 lib.gdn_attention_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_kv_commit.argtypes = [_AP, _INT, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]
 lib.gdn_tree_accept.argtypes = [_DP, _INT, _P, _I64, _P, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]
-for _f in ("gdn_rope_append", "gdn_paged_attention", "gdn_kv_commit", "gdn_tree_accept"):
+_F = ctypes.c_float
+lib.gdn_kv4_block_bytes.argtypes = [_AP]
+lib.gdn_kv4_block_bytes.restype = ctypes.c_size_t
+lib.gdn_kv4_append.argtypes = [_AP, _P, _I64, _P, _I64, _F, _F, _P, _P, _P, _P, _P, _P, _P]
+lib.gdn_kv4_read.argtypes = [_AP, _INT, _I64, _P, _P, _F, _F, _P, _P, _P, _P, _P, _I64, _P, _P]
+lib.gdn_kv4_commit.argtypes = lib.gdn_kv_commit.argtypes
+lib.gdn_logits_probs.argtypes = [_DP, _INT, _INT, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _I64, _P,
+                                 _INT, _P, _I64, _P, _P]
+lib.gdn_token_commit.argtypes = [_DP, _INT, _P, _P, _P, _P, _P, _INT, _P, _I64, _P, _P]
+for _f in ("gdn_rope_append", "gdn_paged_attention", "gdn_kv_commit", "gdn_tree_accept", "gdn_kv4_append", "gdn_kv4_read",
+           "gdn_kv4_commit", "gdn_logits_probs", "gdn_token_commit"):
     getattr(lib, _f).restype = ctypes.c_int
 for _f in ("gdn_conv_tree_step", "gdn_tree_verify", "gdn_chain_verify", "gdn_commit", "gdn_conv_tree_step_compact",
            "gdn_commit_compact", "gdn_gated_rmsnorm", "gdn_decode_step"):
@@ -257,6 +280,53 @@ def gdn_kv_commit(dims: AttnDims, n_layers: int, layer_stride: int, accepted, pa
                            _ptr(node_off), _ptr(ctx_len), _ptr(page_table), _ptr(k_pool), _ptr(v_pool),
                            _ptr(new_len), _ptr(status), _stream(stream))
     return _check("gdn_kv_commit", rc, raise_on_error)
+
+
+def gdn_kv4_block_bytes(dims: AttnDims) -> int:
+    return int(lib.gdn_kv4_block_bytes(ctypes.byref(dims)))
+
+
+def gdn_kv4_append(dims: AttnDims, k, k_stride: int, v, v_stride: int, k_unit: float, v_unit: float, node_off, ctx_len,
+                   page_table, k_pool, v_pool, status, stream=None, raise_on_error: bool = True) -> int:
+    rc = lib.gdn_kv4_append(ctypes.byref(dims), _ptr(k), int(k_stride), _ptr(v), int(v_stride), float(k_unit), float(v_unit),
+                            _ptr(node_off), _ptr(ctx_len), _ptr(page_table), _ptr(k_pool), _ptr(v_pool), _ptr(status),
+                            _stream(stream))
+    return _check("gdn_kv4_append", rc, raise_on_error)
+
+
+def gdn_kv4_read(dims: AttnDims, n_layers: int, layer_stride: int, k_pool, v_pool, k_unit: float, v_unit: float, node_off,
+                 start, page_table, k, v, row_stride: int, status, stream=None, raise_on_error: bool = True) -> int:
+    rc = lib.gdn_kv4_read(ctypes.byref(dims), int(n_layers), int(layer_stride), _ptr(k_pool), _ptr(v_pool), float(k_unit),
+                          float(v_unit), _ptr(node_off), _ptr(start), _ptr(page_table), _ptr(k), _ptr(v), int(row_stride),
+                          _ptr(status), _stream(stream))
+    return _check("gdn_kv4_read", rc, raise_on_error)
+
+
+def gdn_kv4_commit(dims: AttnDims, n_layers: int, layer_stride: int, accepted, parents, node_off, ctx_len, page_table,
+                   k_pool, v_pool, new_len, status, stream=None, raise_on_error: bool = True) -> int:
+    rc = lib.gdn_kv4_commit(ctypes.byref(dims), int(n_layers), int(layer_stride), _ptr(accepted), _ptr(parents),
+                            _ptr(node_off), _ptr(ctx_len), _ptr(page_table), _ptr(k_pool), _ptr(v_pool), _ptr(new_len),
+                            _ptr(status), _stream(stream))
+    return _check("gdn_kv4_commit", rc, raise_on_error)
+
+
+def gdn_logits_probs(dims: GdnDims, vocab: int, dtype: int, logits, logits_stride: int, tokens, parents, node_off, slot_map,
+                     history, history_stride: int, repetition, frequency, presence, temperature, bias_off, bias_token,
+                     bias_value, n_bias: int, mask, mask_stride: int, mask_row, n_masks: int, p, p_stride: int, status,
+                     stream=None, raise_on_error: bool = True) -> int:
+    rc = lib.gdn_logits_probs(ctypes.byref(dims), int(vocab), int(dtype), _ptr(logits), int(logits_stride), _ptr(tokens),
+                              _ptr(parents), _ptr(node_off), _ptr(slot_map), _ptr(history), int(history_stride),
+                              _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(temperature), _ptr(bias_off),
+                              _ptr(bias_token), _ptr(bias_value), int(n_bias), _ptr(mask), int(mask_stride), _ptr(mask_row),
+                              int(n_masks), _ptr(p), int(p_stride), _ptr(status), _stream(stream))
+    return _check("gdn_logits_probs", rc, raise_on_error)
+
+
+def gdn_token_commit(dims: GdnDims, vocab: int, tokens, accepted, parents, node_off, slot_map, prompt: int, history,
+                     history_stride: int, status, stream=None, raise_on_error: bool = True) -> int:
+    rc = lib.gdn_token_commit(ctypes.byref(dims), int(vocab), _ptr(tokens), _ptr(accepted), _ptr(parents), _ptr(node_off),
+                              _ptr(slot_map), int(prompt), _ptr(history), int(history_stride), _ptr(status), _stream(stream))
+    return _check("gdn_token_commit", rc, raise_on_error)
 
 
 def gdn_tree_accept(dims: GdnDims, vocab: int, p, p_stride: int, q, q_stride: int, replacement: int, tokens, parents,

@@ -24,6 +24,8 @@ extern "C" const char *gdn_status_str(int code) {
         case GDN_DEV_BAD_LEN: return "GDN_DEV_BAD_LEN";
         case GDN_DEV_BAD_AXIS: return "GDN_DEV_BAD_AXIS";
         case GDN_DEV_BAD_TOKEN: return "GDN_DEV_BAD_TOKEN";
+        case GDN_DEV_BAD_BIAS: return "GDN_DEV_BAD_BIAS";
+        case GDN_DEV_BAD_MASK: return "GDN_DEV_BAD_MASK";
         default: return "unknown";
     }
 }

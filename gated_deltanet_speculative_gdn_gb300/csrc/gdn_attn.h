@@ -11,7 +11,8 @@
 
 namespace gdn {
 
-inline int check_attn_dims(const gdn_attn_dims *d) {
+// All but the strides.
+inline int check_attn_shape(const gdn_attn_dims *d) {
     if (!d) return GDN_ERR_NULL;
     if (d->n_seqs < 0 || d->n_seqs > 65535 || d->n_tokens < 0 || d->max_seq_tokens < 1) return GDN_ERR_DIMS;
     if (d->h_kv < 1 || d->h_kv > 65535 || d->h_q < d->h_kv || d->h_q % d->h_kv != 0 || d->h_q / d->h_kv > 128 || d->h_q > 65535)
@@ -23,6 +24,12 @@ inline int check_attn_dims(const gdn_attn_dims *d) {
     // positions are int32
     if (static_cast<int64_t>(d->table_width) * d->page_size > INT32_MAX - 65536) return GDN_ERR_DIMS;
     if (static_cast<int64_t>(d->n_tokens) * d->h_q * d->d_head > (int64_t(1) << 40)) return GDN_ERR_DIMS;
+    return GDN_OK;
+}
+
+inline int check_attn_dims(const gdn_attn_dims *d) {
+    const int rc = check_attn_shape(d);
+    if (rc) return rc;
     const int64_t s[3] = {d->page_stride, d->token_stride, d->head_stride};
     for (int64_t x : s)
         if (x < d->d_head || x % 8 != 0 || x > (int64_t(1) << 38)) return GDN_ERR_STRIDE;

@@ -14,7 +14,10 @@
 // *status, the move writes nothing unless it is zero.  Bound by latency: a
 // round's rows are a few MB at most, and the floor is three dependent round trips
 // (path, page table, rows).  12 layers of 64 sequences take 4.7 us in a graph.
-#include "gdn_attn.h"
+//
+// The 4-bit cache moves in the same way, its codes and its scales as words of four
+// bytes (a head's scales of one token are 4, 8 or 16 bytes).
+#include "gdn_kv4.h"
 
 namespace {
 
@@ -67,6 +70,19 @@ __global__ void __launch_bounds__(256) kv_preflight_kernel(const KvArgs a) {
     if (err && lane == 0) gdn::record_status(a.status, err);
 }
 
+// The path root .. acc of the nodes from n0 on, as a mask of nodes (a whole warp, which the preflight has let through).
+__device__ __forceinline__ unsigned long long path_mask(const KvArgs &a, int n0, int acc) {
+    const int lane = threadIdx.x & 31;
+    const int p_lo = lane <= acc ? a.parents[n0 + lane] : -1;
+    const int p_hi = lane + 32 <= acc ? a.parents[n0 + lane + 32] : -1;
+    unsigned long long path = 0;
+    for (int cur = acc; cur >= 0;) {
+        path |= 1ull << cur;
+        cur = __shfl_sync(0xffffffffu, cur < 32 ? p_lo : p_hi, cur & 31);
+    }
+    return path;
+}
+
 __global__ void __launch_bounds__(256) kv_move_kernel(const KvArgs a) {
     __shared__ int64_t from[gdn::kMaxSeqNodes], to[gdn::kMaxSeqNodes];
     __shared__ int m_s;
@@ -79,13 +95,7 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const KvArgs a) {
         // the path, leaf first by shuffles, as a mask of nodes: rank in the mask = place
         int m = 0;
         if (acc >= 0) {
-            const int p_lo = lane <= acc ? a.parents[n0 + lane] : -1;
-            const int p_hi = lane + 32 <= acc ? a.parents[n0 + lane + 32] : -1;
-            unsigned long long path = 0;
-            for (int cur = acc; cur >= 0;) {
-                path |= 1ull << cur;
-                cur = __shfl_sync(0xffffffffu, cur < 32 ? p_lo : p_hi, cur & 31);
-            }
+            const unsigned long long path = path_mask(a, n0, acc);
             m = __popcll(path);
             for (int x = lane; x <= acc; x += 32) {
                 if (!((path >> x) & 1)) continue;
@@ -119,19 +129,82 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const KvArgs a) {
     }
 }
 
+// The same for the 4-bit cache: a column is one word of a head's codes or scales.
+__global__ void __launch_bounds__(256) kv4_move_kernel(const KvArgs a, const gdn::Kv4Layout pl) {
+    __shared__ int64_t from[gdn::kMaxSeqNodes], to[gdn::kMaxSeqNodes];  // bytes to the page; -1: in place already
+    __shared__ int from_at[gdn::kMaxSeqNodes], to_at[gdn::kMaxSeqNodes];  // the place in it
+    __shared__ int m_s;
+    gdn::grid_dep_launch();
+    const int s = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    gdn::grid_dep_wait();
+    if (*reinterpret_cast<volatile int32_t *>(a.status) != 0) return;
+    const int acc = a.accepted[s], n0 = a.node_off[s], ctx = a.ctx_len[s];
+    if (tid < 32) {
+        int m = 0;
+        if (acc >= 0) {
+            const unsigned long long path = path_mask(a, n0, acc);
+            m = __popcll(path);
+            const int in_page = (1 << pl.shift) - 1;
+            for (int x = lane; x <= acc; x += 32) {
+                if (!((path >> x) & 1)) continue;
+                const int j = __popcll(path & ((1ull << x) - 1));
+                from[j] = j == x ? -1 : int64_t(gdn::kv4_page(pl, s, ctx + x)) * pl.page_stride;
+                to[j] = int64_t(gdn::kv4_page(pl, s, ctx + j)) * pl.page_stride;
+                from_at[j] = (ctx + x) & in_page;
+                to_at[j] = (ctx + j) & in_page;
+            }
+        }
+        if (lane == 0) {
+            m_s = m;
+            if (layer == 0 && blockIdx.z == 0) a.new_len[s] = ctx + m;
+        }
+    }
+    __syncthreads();
+    const int m = m_s;
+    const int c = blockIdx.z * blockDim.x + tid;
+    if (m == 0 || c >= 2 * a.cols) return;
+    const bool is_v = c >= a.cols;
+    const int col = is_v ? c - a.cols : c;
+    const int codes = pl.code_row / 4, words = codes + pl.scale_row / 4, h = col / words, w = col - h * words;
+    const bool is_scale = w >= codes;
+    const int row = is_scale ? pl.scale_row : pl.code_row;
+    unsigned char *base = static_cast<unsigned char *>(is_v ? a.v_pool : a.k_pool) + layer * a.layer_stride + int64_t(h) * pl.head_stride +
+                          (is_scale ? (int64_t(pl.code_row) << pl.shift) + 4 * (w - codes) : 4 * w);
+    for (int j0 = 0; j0 < m; j0 += 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < m && from[j0 + j] >= 0)
+                r[j] = *reinterpret_cast<const uint32_t *>(base + from[j0 + j] + from_at[j0 + j] * row);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < m && from[j0 + j] >= 0) *reinterpret_cast<uint32_t *>(base + to[j0 + j] + to_at[j0 + j] * row) = r[j];
+    }
+}
+
 // Whether no two layers share a row: a thread moves its layer's rows in place, so a row of another layer must not
 // be among them.  What has a smaller stride than the layers' lies within it, what has a larger one beyond all layers.
-bool layers_apart(const gdn_attn_dims *d, int n_layers, int64_t layer_stride) {
-    const int64_t stride[3] = {d->page_stride, d->token_stride, d->head_stride};
-    const int64_t count[3] = {d->n_pages, d->page_size, d->h_kv};
-    double span = d->d_head;  // (an int64 may not hold what dims of no real cache give)
-    for (int k = 0; k < 3; ++k)
+// `span`: of what lies in one piece.
+template <int n>
+bool strides_apart(double span, const int64_t (&stride)[n], const int64_t (&count)[n], int n_layers, int64_t layer_stride) {
+    // (an int64 may not hold what dims of no real cache give)
+    for (int k = 0; k < n; ++k)
         if (count[k] > 1 && stride[k] < layer_stride) span += double(count[k] - 1) * double(stride[k]);
     if (double(layer_stride) < span) return false;
     span += double(n_layers - 1) * double(layer_stride);
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < n; ++k)
         if (count[k] > 1 && stride[k] >= layer_stride && double(stride[k]) < span) return false;
     return true;
+}
+bool layers_apart(const gdn_attn_dims *d, int n_layers, int64_t layer_stride) {
+    const int64_t stride[3] = {d->page_stride, d->token_stride, d->head_stride};
+    const int64_t count[3] = {d->n_pages, d->page_size, d->h_kv};
+    return strides_apart(d->d_head, stride, count, n_layers, layer_stride);
+}
+bool layers_apart_kv4(const gdn_attn_dims *d, int n_layers, int64_t layer_stride) {
+    const int64_t stride[2] = {d->page_stride, d->head_stride};
+    const int64_t count[2] = {d->n_pages, d->h_kv};
+    return strides_apart(double(gdn::kv4_block(d)), stride, count, n_layers, layer_stride);
 }
 
 }  // namespace
@@ -173,4 +246,45 @@ extern "C" int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t la
     const dim3 grid(unsigned(S), unsigned(n_layers), unsigned((2 * cols + threads - 1) / threads));
     return gdn::launch_pdl(kv_move_kernel, grid, dim3(unsigned(threads)), 0, st, a) == cudaSuccess ? GDN_OK
                                                                                                      : GDN_ERR_LAUNCH;
+}
+
+extern "C" int gdn_kv4_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const int32_t *accepted,
+                              const int32_t *parents, const int32_t *node_off, const int32_t *ctx_len,
+                              const int32_t *page_table, void *k_pool, void *v_pool, int32_t *new_len, int32_t *status,
+                              void *stream) {
+    int rc = gdn::check_kv4_dims(dims);
+    if (rc) return rc;
+    if (!status) return GDN_ERR_NULL;
+    if (dims->max_seq_tokens > gdn::kMaxSeqNodes) return GDN_ERR_DIMS;
+    if (n_layers < 0 || n_layers > 65535) return GDN_ERR_ARG;
+    const int64_t S = dims->n_seqs, N = dims->n_tokens;
+    if (S == 0 || n_layers == 0) return GDN_OK;
+    if (!accepted || !node_off || !ctx_len || !page_table || !k_pool || !v_pool || !new_len || (N > 0 && !parents))
+        return GDN_ERR_NULL;
+    if (layer_stride < 0 || layer_stride % 16 != 0 || layer_stride > (int64_t(1) << 38)) return GDN_ERR_STRIDE;
+    if (n_layers > 1 && !layers_apart_kv4(dims, n_layers, layer_stride)) return GDN_ERR_STRIDE;
+    if (!gdn::aligned16(k_pool) || !gdn::aligned16(v_pool)) return GDN_ERR_ALIGN;
+    const size_t pool = size_t(layer_stride) * size_t(n_layers - 1) + gdn::kv4_pool_bytes(dims);
+    const gdn::Span ins[] = {{accepted, size_t(S * 4)},
+                             {parents, size_t(N * 4)},
+                             {node_off, size_t((S + 1) * 4)},
+                             {ctx_len, size_t(S * 4)},
+                             {page_table, size_t(S * int64_t(dims->table_width) * 4)},
+                             {status, 4}};
+    const gdn::Span ko[] = {{k_pool, pool}, {new_len, size_t(S * 4)}}, vo[] = {{v_pool, pool}, {new_len, size_t(S * 4)}};
+    if ((rc = gdn::check_alias(ko, 2, ins, 6)) || (rc = gdn::check_alias(vo, 2, ins, 6))) return rc;
+
+    const gdn::Kv4Layout pl = gdn::kv4_layout(dims, page_table);
+    const int cols = dims->h_kv * (pl.code_row + pl.scale_row) / 4;
+    // (the preflight reads the table's shape alone)
+    const gdn::PagedLayout pages{page_table, pl.width, pl.n_pages, pl.shift, pl.page_stride, 0, pl.head_stride};
+    KvArgs a{accepted, parents, node_off, ctx_len, pages, k_pool, v_pool, layer_stride,
+             new_len, status, int(S), int(N), dims->max_seq_tokens, dims->h_kv, cols, 0};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (gdn::launch_pdl(kv_preflight_kernel, dim3(unsigned((S + 7) / 8)), dim3(256), 0, st, a) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    const int threads = 2 * cols < 256 ? ((2 * cols + 31) & ~31) : 256;
+    const dim3 grid(unsigned(S), unsigned(n_layers), unsigned((2 * cols + threads - 1) / threads));
+    return gdn::launch_pdl(kv4_move_kernel, grid, dim3(unsigned(threads)), 0, st, a, pl) == cudaSuccess ? GDN_OK
+                                                                                                          : GDN_ERR_LAUNCH;
 }

@@ -17,8 +17,10 @@
  *                       root-to-node path, on the device, as one transaction.
  *
  * and what stands around it in a hybrid model's round: the full-attention
- * layers (gdn_rope_append, gdn_paged_attention, gdn_kv_commit) and the decision
- * on the drafted tokens (gdn_tree_accept).
+ * layers (gdn_rope_append, gdn_paged_attention, gdn_kv_commit), the same over a
+ * cache held in 4 bits (gdn_kv4_append, gdn_kv4_commit),
+ * the way from logits to probabilities (gdn_logits_probs, gdn_token_commit) and
+ * the decision on the drafted tokens (gdn_tree_accept).
  *
  * Sources (page title, section):
  *   lucebox PR #707 "perf(qwen35): fuse the DFlash2 concurrent verify Gated
@@ -130,7 +132,9 @@ enum {
     GDN_DEV_BAD_PAGE = 8,      /* a page index outside [0, n_pages)               */
     GDN_DEV_BAD_LEN = 9,       /* ctx_len[s] < 0, or the new tokens pass the table */
     GDN_DEV_BAD_AXIS = 10,     /* axis[i] outside [0, n_axes) (rope)              */
-    GDN_DEV_BAD_TOKEN = 11     /* a drafted token outside [0, vocab)              */
+    GDN_DEV_BAD_TOKEN = 11,    /* a token outside [0, vocab), or (bias) out of order */
+    GDN_DEV_BAD_BIAS = 12,     /* bias_off not 0 <= .. <= n_bias, non-decreasing  */
+    GDN_DEV_BAD_MASK = 13      /* mask_row[n] outside [-1, n_masks)               */
 };
 
 /* Conv tree step (lucebox PR #707, Optimizations: fused convolution
@@ -305,7 +309,7 @@ int gdn_decode_step(const gdn_dims *dims, const float *x, int64_t x_stride, cons
  * 16-bit tensors hold bf16 or fp16 (dims->dtype).  Both pools have the same
  * strides, in elements, so a cache of [page][token][head][d], of
  * [page][head][token][d] or one that interleaves keys and values all work. */
-enum { GDN_BF16 = 0, GDN_FP16 = 1 };
+enum { GDN_BF16 = 0, GDN_FP16 = 1, GDN_FP32 = 2 };  /* FP32: gdn_logits_probs only */
 
 typedef struct {
     int32_t n_seqs;          /* S                                                   */
@@ -404,6 +408,132 @@ int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
                   const int32_t *accepted, const int32_t *parents, const int32_t *node_off,
                   const int32_t *ctx_len, const int32_t *page_table, void *k_pool, void *v_pool,
                   int32_t *new_len, int32_t *status, void *stream);
+
+/* Attention layers over a cache held in 4 bits
+ * --------------------------------------------
+ * The same paged cache with 4-bit values: 4.5 bits an element instead of 16, so as
+ * many sequences and positions more in the same memory, and as many fewer bytes for a
+ * step that reads a long context.  The 16 elements 16 b .. 16 b + 15 of a key (or
+ * value) row of a head share a scale:
+ *     s    = e4m3(max |x| / (6 unit))             at most 448
+ *     code = e2m1(x / (s unit))                   at most 6; 0 where s = 0
+ *     x   ~= code * s * unit
+ * both to nearest, a tie to the even code, of the exact quotients.  unit is a power
+ * of two of the caller's choice for all of a layer's keys (k_unit) and one for its
+ * values (v_unit), the same in every call on a cache: 1 serves elements of 2^-5 to
+ * 2^11, and below 2^-10 unit a block loses precision, above 2688 unit it saturates.
+ * 16 elements of which one is not finite get the scale NaN: all 16 read as NaN.
+ * Every stored row is a function of that row alone, so a token that was verified in
+ * a tree and one that was decoded by itself leave the same cache.
+ *   A block (page, head) of gdn_kv4_block_bytes(dims) bytes is page_size rows of
+ * d_head / 2 bytes of codes (element 2 i in the low half of byte i), then page_size
+ * rows of d_head / 16 scales.  dims are those of the 16-bit cache with the strides in
+ * BYTES, multiples of 16: page_stride and head_stride lie between blocks and are at
+ * least a block each; token_stride is not used.  dims->dtype is that of the 16-bit
+ * rows and of q and o.  k and v rows come from anywhere; gdn_rope_append turns keys
+ * into such rows when its pool is one of [N][h_kv * d_head] rows: n_seqs = 1,
+ * node_off = {0, N}, ctx_len = {0}, page_table = {0, 1, 2, ..}. */
+
+/* Bytes of a block (0 for dims that the calls refuse). */
+size_t gdn_kv4_block_bytes(const gdn_attn_dims *dims);
+
+/* Quantises the new tokens' rows into the cache, token i of sequence s at position
+ * ctx_len[s] + i.
+ *   k [N][k_stride], v [N][v_stride]   in, 16-bit, strides in elements, multiples of 8
+ *   k_unit, v_unit   powers of two, 2^-24 .. 2^24
+ *   node_off, ctx_len, page_table      in;  k_pool, v_pool  in/out
+ * Host errors: GDN_ERR_ARG for a unit.
+ * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_LEN, GDN_DEV_BAD_PAGE (the
+ * token's rows are not written). */
+int gdn_kv4_append(const gdn_attn_dims *dims, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, float k_unit, float v_unit, const int32_t *node_off,
+                   const int32_t *ctx_len, const int32_t *page_table, void *k_pool, void *v_pool,
+                   int32_t *status, void *stream);
+
+/* The other way: what the cache holds at positions start[s] + i, for token i of
+ * sequence s and n_layers layers at once (pool of layer l at k_pool + l *
+ * layer_stride BYTES), as 16-bit rows, rounded to dims->dtype (in range of it nothing
+ * is lost: a stored value has 6 significant bits).
+ *   k, v [n_layers][N][row_stride] out, row_stride in elements, a multiple of 8
+ * Host errors and device errors as gdn_kv4_append (the token's rows of k and v are
+ * then not written). */
+int gdn_kv4_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const void *k_pool,
+                 const void *v_pool, float k_unit, float v_unit, const int32_t *node_off,
+                 const int32_t *start, const int32_t *page_table, void *k, void *v,
+                 int64_t row_stride, int32_t *status, void *stream);
+
+/* gdn_kv_commit for the 4-bit cache: codes and scales of the accepted path move as
+ * they are.  layer_stride in BYTES, a multiple of 16, one that keeps the layers'
+ * blocks apart; otherwise its arguments, checks and errors. */
+int gdn_kv4_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
+                   const int32_t *accepted, const int32_t *parents, const int32_t *node_off,
+                   const int32_t *ctx_len, const int32_t *page_table, void *k_pool, void *v_pool,
+                   int32_t *new_len, int32_t *status, void *stream);
+
+/* From logits to the probabilities that gdn_tree_accept takes (the target's p, and
+ * a draft's q), for every node of the trees.  logits[n] is the model's row after
+ * node n, so what has been produced before it is the sequence's history and the
+ * tokens on the path root .. n, n's own included.  For row n of sequence s and
+ * token y, with c(y) the times y was produced (history's count and the path's,
+ * 32767 at most) and `seen` for c(y) > 0 or y in the prompt:
+ *     x = logits[n][y]
+ *     x = x > 0 ? x / repetition[s] : x * repetition[s]            where seen
+ *     x = x - frequency[s] * c(y);  x = x - presence[s] where c(y) > 0
+ *     x = x + bias(y)
+ *     x = -infinity                                  where the mask forbids y
+ *     p[n][y] = exp((x - max) / temperature[s]) / sum               temperature > 0
+ *     p[n][y] = 1 for the largest x (the lowest y among equals), else 0   otherwise
+ * in fp32, each step rounded on its own.  A finite logit stays finite through the
+ * penalties (at fp32's largest).  A row in which every x is -infinity becomes all
+ * zeros, one with a NaN that the mask lets through all NaN.  What the mask forbids
+ * has no influence, whatever it holds.
+ *   dims     n_seqs, n_nodes, n_slots, max_seq_nodes
+ *   vocab    1 .. 2^28
+ *   dtype    of logits: GDN_BF16, GDN_FP16 or GDN_FP32
+ *   logits   [N][logits_stride] in, stride in elements, a multiple of 8 and at least
+ *            vocab rounded up to one; what a row holds past vocab is not used
+ *   tokens [N], parents [N], node_off [S+1] in (node 0's token is read here); the
+ *            tokens are read only where a penalty array is given
+ *   history  [n_slots][history_stride] in, or NULL (nothing produced): bits 0..14 how
+ *            often the token was produced, bit 15 that it is in the prompt; sequence
+ *            s has row slot_map[s].  Stride as for logits.  slot_map is used only here
+ *   repetition, frequency, presence, temperature   [S] in, or NULL (1, 0, 0, 1).
+ *            Without the first three neither tokens nor history is read
+ *   bias_off [S+1], bias_token, bias_value [n_bias]  in, or all NULL: sequence s has
+ *            entries bias_off[s] .. bias_off[s+1] - 1, tokens in ascending order
+ *   mask     [n_masks][mask_stride] words in, or NULL: bit y % 32 of word y / 32 set
+ *            where y is allowed;  mask_row [N]: node n's row, -1 for none; NULL: n
+ *   p        [N][p_stride] out, stride a multiple of 4 and at least vocab rounded up
+ *            to one; what a row holds past vocab is left as it was
+ * Host errors: GDN_ERR_ARG for vocab, dtype, n_bias or n_masks.
+ * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_PARENT, GDN_DEV_BAD_SLOT,
+ * GDN_DEV_BAD_TOKEN (a token of the path, or a bias's), GDN_DEV_BAD_BIAS,
+ * GDN_DEV_BAD_MASK; the row is then not written. */
+int gdn_logits_probs(const gdn_dims *dims, int vocab, int dtype, const void *logits,
+                     int64_t logits_stride, const int32_t *tokens, const int32_t *parents,
+                     const int32_t *node_off, const int32_t *slot_map, const uint16_t *history,
+                     int64_t history_stride, const float *repetition, const float *frequency,
+                     const float *presence, const float *temperature, const int32_t *bias_off,
+                     const int32_t *bias_token, const float *bias_value, int n_bias,
+                     const uint32_t *mask, int64_t mask_stride, const int32_t *mask_row,
+                     int n_masks, float *p, int64_t p_stride, int32_t *status, void *stream);
+
+/* The round's commit of the token history: the tokens of the path root ..
+ * accepted[s] (of all of a sequence's tokens, whatever their number, where accepted is
+ * NULL) are counted once each in history[slot_map[s]], or with prompt = 1 marked as
+ * the prompt's.  A count stops at 32767.  As for gdn_commit, a preflight checks every
+ * sequence first; if a check fails, or *status is already non-zero, nothing is
+ * written.  A new sequence's row is zeroed by the caller.
+ *   accepted [S] or NULL, parents [N] (not read without accepted), tokens [N],
+ *            node_off, slot_map in; history as above in/out
+ *   dims     as above; with accepted NULL max_seq_nodes is no bound
+ * Host errors: GDN_ERR_ARG for vocab or prompt.
+ * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_ACCEPTED, GDN_DEV_BAD_PARENT,
+ * GDN_DEV_BAD_SLOT, GDN_DEV_DUP_SLOT, GDN_DEV_BAD_TOKEN. */
+int gdn_token_commit(const gdn_dims *dims, int vocab, const int32_t *tokens,
+                     const int32_t *accepted, const int32_t *parents, const int32_t *node_off,
+                     const int32_t *slot_map, int prompt, uint16_t *history,
+                     int64_t history_stride, int32_t *status, void *stream);
 
 /* Acceptance of drafted trees on the device (lucebox PR #707 leaves it to the
  * host between verify and commit).  Node 0 of a sequence is its last sampled
