@@ -257,9 +257,9 @@ def prepare(c, seed):
               "k_out": torch.empty(layers, N, hkv * d, device="cuda", dtype=t), "v_out": torch.empty(layers, N, hkv * d, device="cuda", dtype=t),
               "new_len": torch.empty(S, dtype=torch.int32, device="cuda")}
     if own:
-        s["dims"] = G.AttnDims.make_kv4(S, N, max(new), c.get("hq", hkv), hkv, d, G.GDN_BF16 if c["type"] == "bf16" else G.GDN_FP16, pages, page, width)
+        s["dims"] = G.AttnDims.make_kvq(S, N, max(new), c.get("hq", hkv), hkv, d, G.GDN_BF16 if c["type"] == "bf16" else G.GDN_FP16, pages, page, width)
         if c["op"] == "attend":
-            s["work"] = torch.empty(G.gdn_attention_kv4_workspace_bytes(s["dims"]), dtype=torch.uint8, device="cuda")
+            s["work"] = torch.empty(G.gdn_attention_kvq_workspace_bytes(s["dims"]), dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -284,7 +284,7 @@ def _read(s):
     """The new tokens' rows as the cache holds them."""
     c = s["case"]
     if own:
-        s["G"].gdn_kv4_read(s["dims"], s["layers"], s["k_pool"].stride(0), s["k_pool"], s["v_pool"], c["unit"], c["unit"], s["node_off"], s["ctx_len"],
+        s["G"].gdn_kvq_read(s["dims"], s["layers"], s["k_pool"].stride(0), s["k_pool"], s["v_pool"], c["unit"], c["unit"], s["node_off"], s["ctx_len"],
                             s["table"], s["k_out"], s["v_out"], c["hkv"] * c["d"], s["status"])
         return s["k_out"], s["v_out"]
     page, at = _places(s)[2:]
@@ -298,7 +298,7 @@ def _read(s):
 def _append(s):
     c = s["case"]
     if own:
-        s["G"].gdn_kv4_append(s["dims"], s["k"], c["hkv"] * c["d"], s["v"], c["hkv"] * c["d"], c["unit"], c["unit"], s["node_off"], s["ctx_len"], s["table"],
+        s["G"].gdn_kvq_append(s["dims"], s["k"], c["hkv"] * c["d"], s["v"], c["hkv"] * c["d"], c["unit"], c["unit"], s["node_off"], s["ctx_len"], s["table"],
                               s["k_pool"], s["v_pool"], s["status"])
         return _read(s)
     page, at = _places(s)[2:]
@@ -324,7 +324,7 @@ def _attend(s):
     d, hq, hkv, page = c["d"], c["hq"], c["hkv"], c["page"]
     scale = d ** -0.5
     if own:
-        s["G"].gdn_paged_attention_kv4(s["dims"], s["q"], hq * d, s["k_pool"], s["v_pool"], c["unit"], c["unit"], s["table"], s["ctx_len"], s["node_off"],
+        s["G"].gdn_paged_attention_kvq(s["dims"], s["q"], hq * d, s["k_pool"], s["v_pool"], c["unit"], c["unit"], s["table"], s["ctx_len"], s["node_off"],
                                        s["parents"] if c["tree"] else None, scale, s["o"], s["work"], s["work"].numel(), s["status"])
         return s["o"]
     S, T, G = c["seqs"], max(s["new"]), hq // hkv
@@ -359,7 +359,7 @@ def _attend(s):
 def _move(s):
     c = s["case"]
     if own:
-        s["G"].gdn_kv4_commit(s["dims"], s["layers"], s["k_pool"].stride(0), s["accepted"], s["parents"], s["node_off"], s["ctx_len"], s["table"], s["k_pool"],
+        s["G"].gdn_kvq_commit(s["dims"], s["layers"], s["k_pool"].stride(0), s["accepted"], s["parents"], s["node_off"], s["ctx_len"], s["table"], s["k_pool"],
                               s["v_pool"], s["new_len"], s["status"])
         return _read(s) + (s["new_len"],)
     seq, i, page, place = _places(s)
