@@ -38,7 +38,7 @@ EXPORTED_SYMBOLS = ("gdn_conv_tree_step", "gdn_tree_verify", "gdn_chain_verify",
                     "gdn_conv_tree_step_compact", "gdn_commit_compact", "gdn_gated_rmsnorm",
                     "gdn_decode_step", "gdn_rope_append", "gdn_paged_attention",
                     "gdn_attention_workspace_bytes", "gdn_kv_commit", "gdn_tree_accept",
-                    "gdn_kv4_block_bytes", "gdn_kv4_append", "gdn_kv4_read", "gdn_kv4_commit",
+                    "gdn_kvq_block_bytes", "gdn_kvq_append", "gdn_kvq_read", "gdn_kvq_commit",
                     "gdn_logits_probs", "gdn_token_commit",
                     "gdn_test_stall_next_verify", "gdn_test_stall_next_attention",
                     "gdn_status_str", "gdn_replay_row_floats")
@@ -81,7 +81,7 @@ class AttnDims(ctypes.Structure):
                    page, token, head)
 
     @classmethod
-    def make_kv4(cls, n_seqs, n_tokens, max_seq_tokens, h_q, h_kv, d_head, dtype, n_pages, page_size, table_width,
+    def make_kvq(cls, n_seqs, n_tokens, max_seq_tokens, h_q, h_kv, d_head, dtype, n_pages, page_size, table_width,
                  page_stride=None, head_stride=None):
         """Dims of a 4-bit cache: strides in bytes, by default those of a dense one of [page][head][block]."""
         block = page_size * d_head // 16 * 9
@@ -125,16 +125,16 @@ lib.gdn_attention_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_kv_commit.argtypes = [_AP, _INT, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]
 lib.gdn_tree_accept.argtypes = [_DP, _INT, _P, _I64, _P, _I64, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]
 _F = ctypes.c_float
-lib.gdn_kv4_block_bytes.argtypes = [_AP]
-lib.gdn_kv4_block_bytes.restype = ctypes.c_size_t
-lib.gdn_kv4_append.argtypes = [_AP, _P, _I64, _P, _I64, _F, _F, _P, _P, _P, _P, _P, _P, _P]
-lib.gdn_kv4_read.argtypes = [_AP, _INT, _I64, _P, _P, _F, _F, _P, _P, _P, _P, _P, _I64, _P, _P]
-lib.gdn_kv4_commit.argtypes = lib.gdn_kv_commit.argtypes
+lib.gdn_kvq_block_bytes.argtypes = [_AP]
+lib.gdn_kvq_block_bytes.restype = ctypes.c_size_t
+lib.gdn_kvq_append.argtypes = [_AP, _P, _I64, _P, _I64, _F, _F, _P, _P, _P, _P, _P, _P, _P]
+lib.gdn_kvq_read.argtypes = [_AP, _INT, _I64, _P, _P, _F, _F, _P, _P, _P, _P, _P, _I64, _P, _P]
+lib.gdn_kvq_commit.argtypes = lib.gdn_kv_commit.argtypes
 lib.gdn_logits_probs.argtypes = [_DP, _INT, _INT, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _I64, _P,
                                  _INT, _P, _I64, _P, _P]
 lib.gdn_token_commit.argtypes = [_DP, _INT, _P, _P, _P, _P, _P, _INT, _P, _I64, _P, _P]
-for _f in ("gdn_rope_append", "gdn_paged_attention", "gdn_kv_commit", "gdn_tree_accept", "gdn_kv4_append", "gdn_kv4_read",
-           "gdn_kv4_commit", "gdn_logits_probs", "gdn_token_commit"):
+for _f in ("gdn_rope_append", "gdn_paged_attention", "gdn_kv_commit", "gdn_tree_accept", "gdn_kvq_append", "gdn_kvq_read",
+           "gdn_kvq_commit", "gdn_logits_probs", "gdn_token_commit"):
     getattr(lib, _f).restype = ctypes.c_int
 for _f in ("gdn_conv_tree_step", "gdn_tree_verify", "gdn_chain_verify", "gdn_commit", "gdn_conv_tree_step_compact",
            "gdn_commit_compact", "gdn_gated_rmsnorm", "gdn_decode_step"):
@@ -282,32 +282,32 @@ def gdn_kv_commit(dims: AttnDims, n_layers: int, layer_stride: int, accepted, pa
     return _check("gdn_kv_commit", rc, raise_on_error)
 
 
-def gdn_kv4_block_bytes(dims: AttnDims) -> int:
-    return int(lib.gdn_kv4_block_bytes(ctypes.byref(dims)))
+def gdn_kvq_block_bytes(dims: AttnDims) -> int:
+    return int(lib.gdn_kvq_block_bytes(ctypes.byref(dims)))
 
 
-def gdn_kv4_append(dims: AttnDims, k, k_stride: int, v, v_stride: int, k_unit: float, v_unit: float, node_off, ctx_len,
+def gdn_kvq_append(dims: AttnDims, k, k_stride: int, v, v_stride: int, k_unit: float, v_unit: float, node_off, ctx_len,
                    page_table, k_pool, v_pool, status, stream=None, raise_on_error: bool = True) -> int:
-    rc = lib.gdn_kv4_append(ctypes.byref(dims), _ptr(k), int(k_stride), _ptr(v), int(v_stride), float(k_unit), float(v_unit),
+    rc = lib.gdn_kvq_append(ctypes.byref(dims), _ptr(k), int(k_stride), _ptr(v), int(v_stride), float(k_unit), float(v_unit),
                             _ptr(node_off), _ptr(ctx_len), _ptr(page_table), _ptr(k_pool), _ptr(v_pool), _ptr(status),
                             _stream(stream))
-    return _check("gdn_kv4_append", rc, raise_on_error)
+    return _check("gdn_kvq_append", rc, raise_on_error)
 
 
-def gdn_kv4_read(dims: AttnDims, n_layers: int, layer_stride: int, k_pool, v_pool, k_unit: float, v_unit: float, node_off,
+def gdn_kvq_read(dims: AttnDims, n_layers: int, layer_stride: int, k_pool, v_pool, k_unit: float, v_unit: float, node_off,
                  start, page_table, k, v, row_stride: int, status, stream=None, raise_on_error: bool = True) -> int:
-    rc = lib.gdn_kv4_read(ctypes.byref(dims), int(n_layers), int(layer_stride), _ptr(k_pool), _ptr(v_pool), float(k_unit),
+    rc = lib.gdn_kvq_read(ctypes.byref(dims), int(n_layers), int(layer_stride), _ptr(k_pool), _ptr(v_pool), float(k_unit),
                           float(v_unit), _ptr(node_off), _ptr(start), _ptr(page_table), _ptr(k), _ptr(v), int(row_stride),
                           _ptr(status), _stream(stream))
-    return _check("gdn_kv4_read", rc, raise_on_error)
+    return _check("gdn_kvq_read", rc, raise_on_error)
 
 
-def gdn_kv4_commit(dims: AttnDims, n_layers: int, layer_stride: int, accepted, parents, node_off, ctx_len, page_table,
+def gdn_kvq_commit(dims: AttnDims, n_layers: int, layer_stride: int, accepted, parents, node_off, ctx_len, page_table,
                    k_pool, v_pool, new_len, status, stream=None, raise_on_error: bool = True) -> int:
-    rc = lib.gdn_kv4_commit(ctypes.byref(dims), int(n_layers), int(layer_stride), _ptr(accepted), _ptr(parents),
+    rc = lib.gdn_kvq_commit(ctypes.byref(dims), int(n_layers), int(layer_stride), _ptr(accepted), _ptr(parents),
                             _ptr(node_off), _ptr(ctx_len), _ptr(page_table), _ptr(k_pool), _ptr(v_pool), _ptr(new_len),
                             _ptr(status), _stream(stream))
-    return _check("gdn_kv4_commit", rc, raise_on_error)
+    return _check("gdn_kvq_commit", rc, raise_on_error)
 
 
 def gdn_logits_probs(dims: GdnDims, vocab: int, dtype: int, logits, logits_stride: int, tokens, parents, node_off, slot_map,

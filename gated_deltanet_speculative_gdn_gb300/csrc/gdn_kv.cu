@@ -248,7 +248,7 @@ extern "C" int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t la
                                                                                                      : GDN_ERR_LAUNCH;
 }
 
-extern "C" int gdn_kv4_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const int32_t *accepted,
+extern "C" int gdn_kvq_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const int32_t *accepted,
                               const int32_t *parents, const int32_t *node_off, const int32_t *ctx_len,
                               const int32_t *page_table, void *k_pool, void *v_pool, int32_t *new_len, int32_t *status,
                               void *stream) {

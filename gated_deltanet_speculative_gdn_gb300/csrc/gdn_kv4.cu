@@ -191,11 +191,11 @@ Kv4Args common_args(const gdn_attn_dims *dims, float k_unit, float v_unit, const
 
 }  // namespace
 
-extern "C" size_t gdn_kv4_block_bytes(const gdn_attn_dims *dims) {
+extern "C" size_t gdn_kvq_block_bytes(const gdn_attn_dims *dims) {
     return gdn::check_attn_shape(dims) == GDN_OK ? static_cast<size_t>(gdn::kv4_block(dims)) : 0;
 }
 
-extern "C" int gdn_kv4_append(const gdn_attn_dims *dims, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+extern "C" int gdn_kvq_append(const gdn_attn_dims *dims, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                               float k_unit, float v_unit, const int32_t *node_off, const int32_t *ctx_len,
                               const int32_t *page_table, void *k_pool, void *v_pool, int32_t *status, void *stream) {
     bool empty = false;
@@ -227,7 +227,7 @@ extern "C" int gdn_kv4_append(const gdn_attn_dims *dims, const void *k, int64_t 
     return e == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
-extern "C" int gdn_kv4_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const void *k_pool,
+extern "C" int gdn_kvq_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const void *k_pool,
                             const void *v_pool, float k_unit, float v_unit, const int32_t *node_off, const int32_t *start,
                             const int32_t *page_table, void *k, void *v, int64_t row_stride, int32_t *status, void *stream) {
     bool empty = false;

@@ -18,7 +18,7 @@
  *
  * and what stands around it in a hybrid model's round: the full-attention
  * layers (gdn_rope_append, gdn_paged_attention, gdn_kv_commit), the same over a
- * cache held in 4 bits (gdn_kv4_append, gdn_kv4_commit),
+ * cache held in 4 bits (gdn_kvq_append, gdn_kvq_commit),
  * the way from logits to probabilities (gdn_logits_probs, gdn_token_commit) and
  * the decision on the drafted tokens (gdn_tree_accept).
  *
@@ -425,7 +425,7 @@ int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
  * 16 elements of which one is not finite get the scale NaN: all 16 read as NaN.
  * Every stored row is a function of that row alone, so a token that was verified in
  * a tree and one that was decoded by itself leave the same cache.
- *   A block (page, head) of gdn_kv4_block_bytes(dims) bytes is page_size rows of
+ *   A block (page, head) of gdn_kvq_block_bytes(dims) bytes is page_size rows of
  * d_head / 2 bytes of codes (element 2 i in the low half of byte i), then page_size
  * rows of d_head / 16 scales.  dims are those of the 16-bit cache with the strides in
  * BYTES, multiples of 16: page_stride and head_stride lie between blocks and are at
@@ -435,7 +435,7 @@ int gdn_kv_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
  * node_off = {0, N}, ctx_len = {0}, page_table = {0, 1, 2, ..}. */
 
 /* Bytes of a block (0 for dims that the calls refuse). */
-size_t gdn_kv4_block_bytes(const gdn_attn_dims *dims);
+size_t gdn_kvq_block_bytes(const gdn_attn_dims *dims);
 
 /* Quantises the new tokens' rows into the cache, token i of sequence s at position
  * ctx_len[s] + i.
@@ -445,7 +445,7 @@ size_t gdn_kv4_block_bytes(const gdn_attn_dims *dims);
  * Host errors: GDN_ERR_ARG for a unit.
  * Device errors: GDN_DEV_BAD_NODE_OFF, GDN_DEV_BAD_LEN, GDN_DEV_BAD_PAGE (the
  * token's rows are not written). */
-int gdn_kv4_append(const gdn_attn_dims *dims, const void *k, int64_t k_stride, const void *v,
+int gdn_kvq_append(const gdn_attn_dims *dims, const void *k, int64_t k_stride, const void *v,
                    int64_t v_stride, float k_unit, float v_unit, const int32_t *node_off,
                    const int32_t *ctx_len, const int32_t *page_table, void *k_pool, void *v_pool,
                    int32_t *status, void *stream);
@@ -455,9 +455,9 @@ int gdn_kv4_append(const gdn_attn_dims *dims, const void *k, int64_t k_stride, c
  * layer_stride BYTES), as 16-bit rows, rounded to dims->dtype (in range of it nothing
  * is lost: a stored value has 6 significant bits).
  *   k, v [n_layers][N][row_stride] out, row_stride in elements, a multiple of 8
- * Host errors and device errors as gdn_kv4_append (the token's rows of k and v are
+ * Host errors and device errors as gdn_kvq_append (the token's rows of k and v are
  * then not written). */
-int gdn_kv4_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const void *k_pool,
+int gdn_kvq_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, const void *k_pool,
                  const void *v_pool, float k_unit, float v_unit, const int32_t *node_off,
                  const int32_t *start, const int32_t *page_table, void *k, void *v,
                  int64_t row_stride, int32_t *status, void *stream);
@@ -465,7 +465,7 @@ int gdn_kv4_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, 
 /* gdn_kv_commit for the 4-bit cache: codes and scales of the accepted path move as
  * they are.  layer_stride in BYTES, a multiple of 16, one that keeps the layers'
  * blocks apart; otherwise its arguments, checks and errors. */
-int gdn_kv4_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
+int gdn_kvq_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride,
                    const int32_t *accepted, const int32_t *parents, const int32_t *node_off,
                    const int32_t *ctx_len, const int32_t *page_table, void *k_pool, void *v_pool,
                    int32_t *new_len, int32_t *status, void *stream);

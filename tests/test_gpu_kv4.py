@@ -26,7 +26,7 @@ def offsets(new):
 
 
 def dims4(cache, new, dtype, hq=None, max_tokens=None):
-    return G.AttnDims.make_kv4(len(new), int(sum(new)), max_tokens or max([1, *new]), hq or cache.h_kv, cache.h_kv, cache.d,
+    return G.AttnDims.make_kvq(len(new), int(sum(new)), max_tokens or max([1, *new]), hq or cache.h_kv, cache.h_kv, cache.d,
                                G.GDN_BF16 if dtype == torch.bfloat16 else G.GDN_FP16, cache.n_pages, cache.page_size,
                                cache.table.shape[1], *cache.strides)
 
@@ -63,12 +63,12 @@ def test_append_and_read(k):
     N, w = sum(new), hkv * d
     kr, vr = (rows16(g, N, w, pad, dtype, std) for _ in range(2))
     dm = dims4(cache, new, dtype)
-    assert G.gdn_kv4_block_bytes(dm) == page * d * 9 // 16
+    assert G.gdn_kvq_block_bytes(dm) == page * d * 9 // 16
     kp, vp, st = cache.k.cuda(), cache.v.cuda(), status()
     off, ctxt, table = i32(offsets(new)), i32(ctx), i32(cache.table)
-    G.gdn_kv4_append(dm, kr.cuda(), w + pad, vr.cuda(), w + pad, *units, off, ctxt, table, kp, vp, st)
+    G.gdn_kvq_append(dm, kr.cuda(), w + pad, vr.cuda(), w + pad, *units, off, ctxt, table, kp, vp, st)
     ko, vo = (torch.full((1, N, w + pad), 7.0, dtype=dtype, device="cuda") for _ in range(2))
-    G.gdn_kv4_read(dm, 1, 0, kp, vp, *units, off, ctxt, table, ko, vo, w + pad, st)
+    G.gdn_kvq_read(dm, 1, 0, kp, vp, *units, off, ctxt, table, ko, vo, w + pad, st)
     torch.cuda.synchronize()
     assert int(st) == 0
     for buf, rows, unit in ((cache.k, kr, units[0]), (cache.v, vr, units[1])):
@@ -101,7 +101,7 @@ def test_every_value_and_tie():
         dm = dims4(cache, [n], dtype)
         kp, vp, st = cache.k.cuda(), cache.v.cuda(), status()
         xc = x.cuda()
-        G.gdn_kv4_append(dm, xc, 64, -xc, 64, 1.0, 1.0, i32([0, n]), i32([0]), i32(cache.table), kp, vp, st)
+        G.gdn_kvq_append(dm, xc, 64, -xc, 64, 1.0, 1.0, i32([0, n]), i32([0]), i32(cache.table), kp, vp, st)
         for i in range(n):
             cache.put(cache.k, 0, i, x[i].view(1, 64), 1.0)
             cache.put(cache.v, 0, i, -x[i].view(1, 64), 1.0)
@@ -117,9 +117,9 @@ def test_not_finite():
         x[0, 3], x[1, 20], x[2, 127], x[4, 64] = float("nan"), float("inf"), -float("inf"), float("nan")
         dm, st = dims4(cache, [6], dtype), status()
         kp, vp = cache.k.cuda(), cache.v.cuda()
-        G.gdn_kv4_append(dm, x.cuda(), 128, x.cuda(), 128, 1.0, 1.0, i32([0, 6]), i32([0]), i32(cache.table), kp, vp, st)
+        G.gdn_kvq_append(dm, x.cuda(), 128, x.cuda(), 128, 1.0, 1.0, i32([0, 6]), i32([0]), i32(cache.table), kp, vp, st)
         ko, vo = (torch.zeros(6, 128, dtype=dtype, device="cuda") for _ in range(2))
-        G.gdn_kv4_read(dm, 1, 0, kp, vp, 1.0, 1.0, i32([0, 6]), i32([0]), i32(cache.table), ko, vo, 128, st)
+        G.gdn_kvq_read(dm, 1, 0, kp, vp, 1.0, 1.0, i32([0, 6]), i32([0]), i32(cache.table), ko, vo, 128, st)
         for i in range(6):
             cache.put(cache.k, 0, i, x[i].view(2, 64), 1.0)
         assert int(st) == 0 and torch.equal(kp.cpu(), cache.k)
@@ -137,8 +137,8 @@ def test_rows_in_one_buffer():
     out = torch.zeros(n, 2 * w + 16, dtype=dtype, device="cuda")
     dm, st, kp, vp = dims4(cache, [n], dtype), status(), cache.k.cuda(), cache.v.cuda()
     args = (i32([0, n]), i32([0]), i32(cache.table))
-    G.gdn_kv4_append(dm, x, 2 * w + 16, x.data_ptr() + 2 * w, 2 * w + 16, 1.0, 1.0, *args, kp, vp, st)
-    G.gdn_kv4_read(dm, 1, 0, kp, vp, 1.0, 1.0, *args, out, out.data_ptr() + 2 * w, 2 * w + 16, st)
+    G.gdn_kvq_append(dm, x, 2 * w + 16, x.data_ptr() + 2 * w, 2 * w + 16, 1.0, 1.0, *args, kp, vp, st)
+    G.gdn_kvq_read(dm, 1, 0, kp, vp, 1.0, 1.0, *args, out, out.data_ptr() + 2 * w, 2 * w + 16, st)
     assert int(st) == 0
     for i in range(n):
         cache.put(cache.k, 0, i, x[i, :w].cpu().view(hkv, d), 1.0)
@@ -180,8 +180,8 @@ def test_commit(d, page, layout, layers, spread):
         strides, ls = c0.strides, size + pad
     kp, vp, st = pack([c.k for c in caches]), pack([c.v for c in caches]), status()
     new_len = torch.full((len(new),), -5, dtype=torch.int32, device="cuda")
-    dm = G.AttnDims.make_kv4(len(new), sum(new), 64, hkv, hkv, d, G.GDN_BF16, c0.n_pages, page, c0.table.shape[1], *strides)
-    G.gdn_kv4_commit(dm, layers, ls, i32(acc), i32([x for p in parents for x in p]), i32(offsets(new)), i32(ctx), i32(c0.table),
+    dm = G.AttnDims.make_kvq(len(new), sum(new), 64, hkv, hkv, d, G.GDN_BF16, c0.n_pages, page, c0.table.shape[1], *strides)
+    G.gdn_kvq_commit(dm, layers, ls, i32(acc), i32([x for p in parents for x in p]), i32(offsets(new)), i32(ctx), i32(c0.table),
                      kp, vp, new_len, st)
     torch.cuda.synchronize()
     assert int(st) == 0
@@ -217,10 +217,10 @@ def test_device_errors_write_nothing():
         else:
             k2, v2 = kp, vp
         st = status()
-        G.gdn_kv4_append(dm, x, 64, x, 64, 1.0, 1.0, i32(off), i32(ctx), i32(table), k2, v2, st)
+        G.gdn_kvq_append(dm, x, 64, x, 64, 1.0, 1.0, i32(off), i32(ctx), i32(table), k2, v2, st)
         assert int(st) == code
         st.zero_()
-        G.gdn_kv4_read(dm, 1, 0, kp, vp, 1.0, 1.0, i32(off), i32(ctx), i32(table), out[0], out[1], 64, st)
+        G.gdn_kvq_read(dm, 1, 0, kp, vp, 1.0, 1.0, i32(off), i32(ctx), i32(table), out[0], out[1], 64, st)
         assert int(st) == code
     assert torch.equal(kp.cpu(), cache.k) and torch.equal(vp.cpu(), cache.v)
     par, new_len = [-1, 0, 1, 2] * 2, torch.full((2,), -5, dtype=torch.int32, device="cuda")
@@ -230,10 +230,10 @@ def test_device_errors_write_nothing():
                                           ([0, 4, 8], [0, 0], cache.table, [4, 3], par, G.GDN_DEV_BAD_ACCEPTED),
                                           ([0, 4, 8], [0, 0], cache.table, [3, 3], [-1, 0, 1, 2, -1, 1, 1, 2], G.GDN_DEV_BAD_PARENT)):
         st = status()
-        G.gdn_kv4_commit(dm, 1, 0, i32(acc), i32(p), i32(off), i32(ctx), i32(table), kp, vp, new_len, st)
+        G.gdn_kvq_commit(dm, 1, 0, i32(acc), i32(p), i32(off), i32(ctx), i32(table), kp, vp, new_len, st)
         assert int(st) == code, G.gdn_status_str(code)
     st.fill_(G.GDN_DEV_TIMEOUT)   # after another call's error nothing is written either
-    G.gdn_kv4_commit(dm, 1, 0, i32([3, 3]), i32([-1, 0, 0, 0] * 2), i32([0, 4, 8]), i32([0, 0]), i32(cache.table), kp, vp, new_len, st)
+    G.gdn_kvq_commit(dm, 1, 0, i32([3, 3]), i32([-1, 0, 0, 0] * 2), i32([0, 4, 8]), i32([0, 0]), i32(cache.table), kp, vp, new_len, st)
     assert new_len.tolist() == [-5, -5]
     assert torch.equal(kp.cpu(), cache.k) and torch.equal(vp.cpu(), cache.v)
 
@@ -245,22 +245,22 @@ def test_far_places_in_a_large_pool():
     n_pages = 6
     pool = torch.zeros((n_pages - 1) * stride + 288, dtype=torch.uint8, device="cuda")
     pool2 = torch.zeros_like(pool)
-    dm = G.AttnDims.make_kv4(1, 10, 10, hkv, hkv, d, G.GDN_BF16, n_pages, page, 2, stride, 288)
+    dm = G.AttnDims.make_kvq(1, 10, 10, hkv, hkv, d, G.GDN_BF16, n_pages, page, 2, stride, 288)
     g = torch.Generator().manual_seed(6)
     x, y = (torch.randn(10, 64, generator=g).bfloat16() for _ in range(2))
     table, st = i32([[5, 4]]), status()
     args = (i32([0, 10]), i32([0]), table)
-    G.gdn_kv4_append(dm, x.cuda(), 64, y.cuda(), 64, 1.0, 1.0, *args, pool, pool2, st)
+    G.gdn_kvq_append(dm, x.cuda(), 64, y.cuda(), 64, 1.0, 1.0, *args, pool, pool2, st)
     ko, vo = (torch.zeros(10, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-    G.gdn_kv4_read(dm, 1, 0, pool, pool2, 1.0, 1.0, *args, ko, vo, 64, st)
+    G.gdn_kvq_read(dm, 1, 0, pool, pool2, 1.0, 1.0, *args, ko, vo, 64, st)
     assert int(st) == 0
     for got, want, p in ((ko, x, pool), (vo, y, pool2)):
         c, sc = Q.quantise(want.view(10, 1, 64), 1.0)
         assert torch.equal(got.cpu().double(), Q.values(c, sc, 1.0).view(10, 64))
         assert torch.equal(p[5 * stride:5 * stride + 256].cpu(), c[:8].flatten())
     new_len = torch.zeros(1, dtype=torch.int32, device="cuda")
-    G.gdn_kv4_commit(dm, 1, 0, i32([9]), i32([-1, 0, 0, 0, 0, 0, 0, 0, 0, 0]), *args, pool, pool2, new_len, st)
-    G.gdn_kv4_read(dm, 1, 0, pool, pool2, 1.0, 1.0, *args, ko, vo, 64, st)
+    G.gdn_kvq_commit(dm, 1, 0, i32([9]), i32([-1, 0, 0, 0, 0, 0, 0, 0, 0, 0]), *args, pool, pool2, new_len, st)
+    G.gdn_kvq_read(dm, 1, 0, pool, pool2, 1.0, 1.0, *args, ko, vo, 64, st)
     assert int(st) == 0 and new_len.tolist() == [2]
     c, sc = Q.quantise(x[9].view(1, 64), 1.0)
     assert torch.equal(ko[1].cpu().double(), Q.values(c, sc, 1.0).view(64))
