@@ -38,7 +38,8 @@ EXPORTED_SYMBOLS = ("gdn_conv_tree_step", "gdn_tree_verify", "gdn_chain_verify",
                     "gdn_conv_tree_step_compact", "gdn_commit_compact", "gdn_gated_rmsnorm",
                     "gdn_decode_step", "gdn_rope_append", "gdn_paged_attention",
                     "gdn_attention_workspace_bytes", "gdn_kv_commit", "gdn_tree_accept",
-                    "gdn_kvq_block_bytes", "gdn_kvq_append", "gdn_kvq_read", "gdn_kvq_commit",
+                    "gdn_kvq_block_bytes", "gdn_kvq_append", "gdn_paged_attention_kvq",
+                    "gdn_attention_kvq_workspace_bytes", "gdn_kvq_read", "gdn_kvq_commit",
                     "gdn_logits_probs", "gdn_token_commit",
                     "gdn_test_stall_next_verify", "gdn_test_stall_next_attention",
                     "gdn_status_str", "gdn_replay_row_floats")
@@ -129,12 +130,15 @@ lib.gdn_kvq_block_bytes.argtypes = [_AP]
 lib.gdn_kvq_block_bytes.restype = ctypes.c_size_t
 lib.gdn_kvq_append.argtypes = [_AP, _P, _I64, _P, _I64, _F, _F, _P, _P, _P, _P, _P, _P, _P]
 lib.gdn_kvq_read.argtypes = [_AP, _INT, _I64, _P, _P, _F, _F, _P, _P, _P, _P, _P, _I64, _P, _P]
+lib.gdn_paged_attention_kvq.argtypes = [_AP, _P, _I64, _P, _P, _F, _F, _P, _P, _P, _P, _F, _P, _P, _I64, _P, _P]
+lib.gdn_attention_kvq_workspace_bytes.argtypes = [_AP]
+lib.gdn_attention_kvq_workspace_bytes.restype = ctypes.c_size_t
 lib.gdn_kvq_commit.argtypes = lib.gdn_kv_commit.argtypes
 lib.gdn_logits_probs.argtypes = [_DP, _INT, _INT, _P, _I64, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _I64, _P,
                                  _INT, _P, _I64, _P, _P]
 lib.gdn_token_commit.argtypes = [_DP, _INT, _P, _P, _P, _P, _P, _INT, _P, _I64, _P, _P]
 for _f in ("gdn_rope_append", "gdn_paged_attention", "gdn_kv_commit", "gdn_tree_accept", "gdn_kvq_append", "gdn_kvq_read",
-           "gdn_kvq_commit", "gdn_logits_probs", "gdn_token_commit"):
+           "gdn_paged_attention_kvq", "gdn_kvq_commit", "gdn_logits_probs", "gdn_token_commit"):
     getattr(lib, _f).restype = ctypes.c_int
 for _f in ("gdn_conv_tree_step", "gdn_tree_verify", "gdn_chain_verify", "gdn_commit", "gdn_conv_tree_step_compact",
            "gdn_commit_compact", "gdn_gated_rmsnorm", "gdn_decode_step"):
@@ -300,6 +304,19 @@ def gdn_kvq_read(dims: AttnDims, n_layers: int, layer_stride: int, k_pool, v_poo
                           float(v_unit), _ptr(node_off), _ptr(start), _ptr(page_table), _ptr(k), _ptr(v), int(row_stride),
                           _ptr(status), _stream(stream))
     return _check("gdn_kvq_read", rc, raise_on_error)
+
+
+def gdn_paged_attention_kvq(dims: AttnDims, q, q_stride: int, k_pool, v_pool, k_unit: float, v_unit: float, page_table, ctx_len,
+                            node_off, parents, scale: float, o, workspace, workspace_bytes: int, status, stream=None,
+                            raise_on_error: bool = True) -> int:
+    rc = lib.gdn_paged_attention_kvq(ctypes.byref(dims), _ptr(q), int(q_stride), _ptr(k_pool), _ptr(v_pool), float(k_unit),
+                                     float(v_unit), _ptr(page_table), _ptr(ctx_len), _ptr(node_off), _ptr(parents),
+                                     float(scale), _ptr(o), _ptr(workspace), int(workspace_bytes), _ptr(status), _stream(stream))
+    return _check("gdn_paged_attention_kvq", rc, raise_on_error)
+
+
+def gdn_attention_kvq_workspace_bytes(dims: AttnDims) -> int:
+    return int(lib.gdn_attention_kvq_workspace_bytes(ctypes.byref(dims)))
 
 
 def gdn_kvq_commit(dims: AttnDims, n_layers: int, layer_stride: int, accepted, parents, node_off, ctx_len, page_table,

@@ -28,7 +28,8 @@ LIB = os.path.join(PKG, "libgdn_gb300.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["gdn_api.cpp", "gdn_conv.cu", "gdn_verify.cu", "gdn_chain.cu", "gdn_chain_tc.cu", "gdn_commit.cu", "gdn_norm.cu", "gdn_decode.cu",
-           "gdn_rope.cu", "gdn_attention.cu", "gdn_kv.cu", "gdn_accept.cu", "gdn_kv4.cu", "gdn_probs.cu"]
+           "gdn_rope.cu", "gdn_attention.cu", "gdn_kv.cu", "gdn_accept.cu", "gdn_kv4.cu",
+           "gdn_attention_kvq.cu", "gdn_probs.cu"]
 
 
 def _nvcc() -> str:

@@ -68,6 +68,9 @@ int launch_chain_tc(const gdn_dims *dims, const float *xc, const float *ba, int6
 // it clears it, so exactly one tensor-core verify launch receives it.
 uint64_t take_test_stall_ns();
 
+// The pending test stall of gdn_test_stall_next_attention (ns, 0: none) and the role it is for; taking it clears it.
+uint64_t take_attention_stall(int *role);
+
 // Bytes of a [rows][stride] float tensor of which the last row holds `width`.
 inline size_t strided_bytes(int64_t rows, int64_t stride, int64_t width) {
     return rows <= 0 ? 0 : static_cast<size_t>(((rows - 1) * stride + width) * 4);

@@ -18,7 +18,7 @@
  *
  * and what stands around it in a hybrid model's round: the full-attention
  * layers (gdn_rope_append, gdn_paged_attention, gdn_kv_commit), the same over a
- * cache held in 4 bits (gdn_kvq_append, gdn_kvq_commit),
+ * cache held in 4 bits (gdn_kvq_append, gdn_paged_attention_kvq, gdn_kvq_commit),
  * the way from logits to probabilities (gdn_logits_probs, gdn_token_commit) and
  * the decision on the drafted tokens (gdn_tree_accept).
  *
@@ -462,6 +462,21 @@ int gdn_kvq_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, 
                  const int32_t *start, const int32_t *page_table, void *k, void *v,
                  int64_t row_stride, int32_t *status, void *stream);
 
+/* gdn_paged_attention over the 4-bit cache: the same formula, arguments, masks and
+ * errors, with keys and values as the cache holds them.  The products run in fp16
+ * with fp32 sums, in which codes times scales are exact; for bf16 a q row is first
+ * scaled by a power of two, so that its largest element is in [2^14, 2^15) (what is
+ * below 2^-39 of that is lost, and put back afterwards is the factor).
+ *   workspace  at least gdn_attention_kvq_workspace_bytes(dims) bytes
+ * Host errors: also GDN_ERR_ARG for a unit. */
+int gdn_paged_attention_kvq(const gdn_attn_dims *dims, const void *q, int64_t q_stride,
+                            const void *k_pool, const void *v_pool, float k_unit, float v_unit,
+                            const int32_t *page_table, const int32_t *ctx_len,
+                            const int32_t *node_off, const int32_t *parents, float scale, void *o,
+                            void *workspace, int64_t workspace_bytes, int32_t *status, void *stream);
+
+size_t gdn_attention_kvq_workspace_bytes(const gdn_attn_dims *dims);
+
 /* gdn_kv_commit for the 4-bit cache: codes and scales of the accepted path move as
  * they are.  layer_stride in BYTES, a multiple of 16, one that keeps the layers'
  * blocks apart; otherwise its arguments, checks and errors. */
@@ -593,8 +608,10 @@ void gdn_test_stall_next_verify(uint64_t wait_ns);
  * of its first CTA wait for wait_ns (capped at 2 s) on a barrier that nothing
  * ever completes, then give up; the CTA's other roles wait out their own limits
  * (about 2 s), drain and leave, and the call reports GDN_DEV_TIMEOUT.
+ * gdn_paged_attention_kvq takes it in the same way.
  *   role  0 softmax and results, 1 copies, 2 scores, 3 values' products,
- *         4 cleaning of values; any other is ignored */
+ *         4 cleaning of values (with the 4-bit cache 1 and 4 are its conversion);
+ *         any other is ignored */
 void gdn_test_stall_next_attention(uint64_t wait_ns, int role);
 
 /* Name of a host or device status code ("GDN_OK", "GDN_DEV_DUP_SLOT", ...);
