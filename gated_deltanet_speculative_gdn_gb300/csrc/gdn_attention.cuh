@@ -46,10 +46,10 @@ struct Cfg {
     static constexpr uint32_t kTile = TK * D * 2;         // 32, 16, 8 KB
     static constexpr uint32_t kRing = k4 ? 131072 : 196608;
     static constexpr int kStages = kRing / kTile;
-    // 4-bit rows on their way: tiles of keys or of values, a warp's 1024 bytes of codes and 128 of scales in each
+    // a second ring, of tiles of codes and scales as they lie in memory
     static constexpr int kAhead = D == 256 ? 8 : 16;
-    static constexpr uint32_t kConvBytes = 1152;
-    static constexpr size_t kSmem = 1024 + kRing + (k4 ? size_t(kAhead) * kConvWarps * kConvBytes : 0);
+    static constexpr uint32_t kCodeRow = D / 2, kScaleRow = D / 16, kRawTile = TK * (kCodeRow + kScaleRow);
+    static constexpr size_t kSmem = 1024 + kRing + (k4 ? kAhead * kRawTile : 0);
     // tensor-memory columns
     static constexpr int kSBufs = kStreams;
     static constexpr uint32_t kO = 0, kQ = kStreams * D, kS = kQ + D / 2, kP = kS + kSBufs * TK;
@@ -308,12 +308,6 @@ __device__ __forceinline__ const unsigned char *scale_bytes(const Args &a, int s
            (int64_t(D / 2) << a.pl.shift) + (x & ((1 << a.pl.shift) - 1)) * (D / 16);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
 // Eight codes times a scale, as fp16: exact.
 __device__ __forceinline__ uint4 convert8(uint32_t codes, uint32_t scale2) {
     uint32_t r[4];
@@ -327,111 +321,154 @@ __device__ __forceinline__ uint4 convert8(uint32_t codes, uint32_t scale2) {
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// ---- the 4-bit cache's tiles as fp16 in the ring ------------------------------------------
+// A raw tile holds its positions in runs, a page's or all 64: a run's codes, then its scales, as a block does.
+__device__ __forceinline__ int raw_run(int shift) { return min(1 << shift, TK); }
+
+// ---- the 4-bit cache's codes and scales into the ring of raw tiles -------------------------
+// A page's keys (or values) of a head are one piece of memory and one copy; of a page larger than a tile codes and
+// scales are two.
+template <typename T, typename C>
+__device__ __forceinline__ void copy_role(const Args &a, Walk &walk, unsigned char *raw, uint64_t *raw_full, uint64_t *raw_empty,
+                                          volatile int *abort_flag, bool ok) {
+    asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
+    const unsigned full = 0xffffffffu;
+    const int lane = threadIdx.x & 31, ps = 1 << a.pl.shift, run = raw_run(a.pl.shift), runs = TK / run;
+    const uint32_t codes = run * C::kCodeRow, scales = run * C::kScaleRow;
+    int st = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool bad_page = false;
+    Segment g;
+    while (ok && walk.next(g)) {
+        // (the first role to come to a segment: its Q rows are on their way into L2)
+        for (int u = lane; u < g.rows * C::kChunks; u += 32) {
+            const int r = u / C::kChunks;
+            const T *src = static_cast<const T *>(a.q) + (int64_t(g.q.n0) + g.i0 + r / a.G) * a.q_stride +
+                           (int64_t(g.h) * a.G + r % a.G) * C::D + 64 * (u % C::kChunks);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        }
+        // page-table entries, 32 in each of two registers, loaded ahead
+        const int32_t *table = a.pl.table + int64_t(g.s) * a.pl.width;
+        const int last = (g.limit - 1) >> a.pl.shift;
+        int base = (g.tile0 * TK) >> a.pl.shift;
+        auto entry = [&](int o) { return o <= last ? table[o] : -1; };
+        int cur = entry(base + lane), nxt = entry(base + 32 + lane);
+        const int64_t head = int64_t(g.h) * a.pl.head_stride;
+        auto load = [&](const void *pool, int page, int at) {
+            if (!wait_bar(raw_empty + st, phase ^ 1, abort_flag)) return false;
+            const bool mine = lane < runs && page >= 0;
+            const unsigned m = __ballot_sync(full, mine);
+            if (lane == 0) gdn::mbar_arrive_expect_tx(raw_full + st, __popc(m) * (codes + scales));
+            __syncwarp();
+            if (mine) {
+                unsigned char *dst = raw + st * C::kRawTile + lane * (codes + scales);
+                const unsigned char *block = static_cast<const unsigned char *>(pool) + int64_t(page) * a.pl.page_stride + head;
+                if (ps == run) {
+                    gdn::bulk_load(dst, block, codes + scales, raw_full + st);
+                } else {
+                    gdn::bulk_load(dst, block + at * C::kCodeRow, codes, raw_full + st);
+                    gdn::bulk_load(dst + codes, block + (int64_t(C::kCodeRow) << a.pl.shift) + at * C::kScaleRow, scales, raw_full + st);
+                }
+            }
+            ++issued;
+            if (++st == C::kAhead) {
+                st = 0;
+                phase ^= 1;
+            }
+            return true;
+        };
+        int v_page = -1;
+        for (int t = g.tile0; t <= g.tile1 && ok; ++t) {
+            int page = -1;
+            if (t < g.tile1) {
+                const int first = (t * TK) >> a.pl.shift;
+                if (first - base >= 32) {
+                    cur = nxt;
+                    base += 32;
+                    nxt = entry(base + 32 + lane);
+                }
+                const int o = first + min(lane, runs - 1) - base;
+                const int lo = __shfl_sync(full, cur, o & 31), hi = __shfl_sync(full, nxt, o & 31);
+                page = o < 32 ? lo : hi;
+                if (page < 0 || page >= a.pl.n_pages) {
+                    bad_page |= o + base <= last;
+                    page = -1;
+                }
+                ok = load(a.k_pool, page, (t * TK) & (ps - 1));
+            }
+            if (ok && t > g.tile0) ok = load(a.v_pool, v_page, ((t - 1) * TK) & (ps - 1));
+            v_page = page;
+        }
+    }
+    if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
+    // the last copies into each stage are waited for whatever has happened: none is under way when the CTA leaves
+    const int n = int(min(issued, (long long)C::kAhead));
+    for (int k = 0; k < n; ++k) {
+        if (st == 0) {
+            st = C::kAhead;
+            phase ^= 1;
+        }
+        --st;
+        gdn::mbar_wait_bounded(raw_full + st, phase);
+    }
+}
+
+// The order of a segment's n tiles of keys and n of values in the rings: K_0 K_1 V_0 K_2 V_1 ... V_{n-1}.
+__device__ __forceinline__ bool values_at(int j, int n) { return j == 2 * n - 1 || (j > 0 && !(j & 1)); }
+__device__ __forceinline__ int tile_at(int j, int n) { return j == 2 * n - 1 ? n - 1 : j == 0 ? 0 : (j & 1) ? (j + 1) / 2 : j / 2 - 1; }
+
+// ---- raw tiles as fp16 in the ring of tiles ------------------------------------------------
 // A thread takes two units of a tile of keys or values, 32 elements (16 bytes of codes, two
-// scales) of a position each, from memory to the ring: it copies them into a place of its
-// own kAhead tiles early (so a wait is only for its own copies, and the warp's for the
-// scales), and writes them out as fp16 in the 128-byte swizzle.  The lanes of a unit are
-// rows first, so that a sector is read whole by one instruction and eight lanes' 16-byte
-// stores go to eight rows, whose places in the swizzle differ.
+// scales) of a position each: a warp reads 512 consecutive bytes, and writes each unit as four
+// 16-byte pieces in the 128-byte swizzle.  A position's units lie in its 64-column chunks, whose
+// equal pieces share banks, so the lanes of chunk c begin at piece c.
 template <typename C>
-__device__ __forceinline__ void convert_role(const Args &a, const Start &start, Walk &walk, unsigned char *tiles, uint64_t *full_bar,
-                                             uint64_t *empty_bar, uint32_t (*nf)[4], volatile int *abort_flag, bool ok) {
-    constexpr int D = C::D, A = C::kAhead;
-    constexpr int kCols = D / 32 < 4 ? D / 32 : 4, kRowsU = 32 / kCols;  // columns and rows of a warp's unit
-    constexpr bool kSameRow = D == 256;                                  // the second unit: 4 columns on, or kRowsU rows
-    constexpr int kRowsW = kSameRow ? kRowsU : 2 * kRowsU;               // rows of a warp
+__device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned char *tiles, uint64_t *full_bar, uint64_t *empty_bar,
+                                             const unsigned char *raw, uint64_t *raw_full, uint64_t *raw_empty, uint32_t (*nf)[4],
+                                             volatile int *abort_flag, bool ok) {
+    constexpr int D = C::D, kCols = D / 32;  // units of a position
     const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - C::kConv;
     if (cw >= C::kConvWarps) return;
-    const int row = cw * kRowsW + lane % kRowsU, col = lane / kRowsU;
-    const int srow = cw * kRowsW + lane % kRowsW, sword = lane / kRowsW;  // the word of scales that this lane copies
-    const bool second = !kSameRow && lane % kRowsW >= kRowsU;             // it is of the second unit's rows
-    unsigned char *mine = tiles + C::kRing + cw * C::kConvBytes;
-    const uint32_t mine_s = gdn::smem_addr(mine);
-    constexpr uint32_t kStep = C::kConvWarps * C::kConvBytes;
-    const int in_page = (1 << a.pl.shift) - 1;
-    bool bad_page = false;
-
-    // item j of a segment of n tiles, in the ring's order
-    auto values_at = [](int j, int n) { return j == 2 * n - 1 || (j > 0 && !(j & 1)); };
-    auto tile_at = [](int j, int n) { return j == 2 * n - 1 ? n - 1 : j == 0 ? 0 : (j & 1) ? (j + 1) / 2 : j / 2 - 1; };
-
-    // ---- copies: the next item's page-table entries are looked up one item early
-    Walk feed(a, start);
-    Segment fg;
-    int fj = 0, fn = 0, ft = 0, page0 = -1, page1 = -1;
-    bool more = true, fv = false;
-    auto look = [&] {
-        if (fj == 2 * fn) {
-            more = more && feed.next(fg);
-            if (!more) return;
-            fn = fg.tile1 - fg.tile0;
-            fj = 0;
-        }
-        fv = values_at(fj, fn);
-        ft = fg.tile0 + tile_at(fj, fn);
-        ++fj;
-        const int32_t *table = a.pl.table + int64_t(fg.s) * a.pl.width;
-        const int x = ft * TK + row;
-        page0 = x < fg.limit ? table[x >> a.pl.shift] : -1;
-        if (page0 < 0 || page0 >= a.pl.n_pages) bad_page |= x < fg.limit;
-        if (!kSameRow) {
-            const int x1 = x + kRowsU;
-            page1 = x1 < fg.limit ? table[x1 >> a.pl.shift] : -1;
-            if (page1 < 0 || page1 >= a.pl.n_pages) bad_page |= x1 < fg.limit;
-        }
-    };
-    auto request = [&](int st) {
-        if (more) {
-            const unsigned char *pool = static_cast<const unsigned char *>(fv ? a.v_pool : a.k_pool) + int64_t(fg.h) * a.pl.head_stride;
-            const uint32_t dst = mine_s + st * kStep;
-            auto place = [&](int page, int r) {  // the block's start, and the row in it
-                return pool + int64_t(page) * a.pl.page_stride + int64_t((ft * TK + r) & in_page) * (D / 2);
-            };
-            const bool ok0 = page0 >= 0 && page0 < a.pl.n_pages;
-            const bool ok1 = kSameRow ? ok0 : page1 >= 0 && page1 < a.pl.n_pages;
-            if (ok0) copy16(dst + 16 * lane, place(page0, row) + 16 * col);
-            if (ok1) copy16(dst + 512 + 16 * lane, kSameRow ? place(page0, row) + 16 * (col + 4) : place(page1, row + kRowsU) + 16 * col);
-            if (second ? ok1 : ok0)
-                copy4(dst + 1024 + 4 * lane, pool + int64_t(second ? page1 : page0) * a.pl.page_stride + (int64_t(D / 2) << a.pl.shift) +
-                                                 int64_t((ft * TK + srow) & in_page) * (D / 16) + 4 * sword);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        look();
-    };
-    look();
-#pragma unroll 1
-    for (int i = 0; i < A; ++i) request(i);
-
-    // ---- conversion
+    const int run = raw_run(a.pl.shift), piece_bytes = run * int(C::kCodeRow + C::kScaleRow);
+    const int chunk = (lane % kCols) >> 1;   // the same for both units
+    int row[2];
+    uint32_t from[2], scale[2], to[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int u = cw * 64 + 32 * k + lane, col = u % kCols;
+        row[k] = u / kCols;
+        const uint32_t piece = row[k] / run * piece_bytes, r = row[k] % run;
+        from[k] = piece + r * C::kCodeRow + 16 * col;
+        scale[k] = piece + run * C::kCodeRow + r * C::kScaleRow + 2 * col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            to[k][i] = chunk * C::kChunkBytes + row[k] * 128 + ((((col & 1) * 4 + (i ^ (chunk & 3))) ^ (row[k] & 7)) << 4);
+    }
     int st = 0, stage = 0;
-    uint32_t phase = 0, seg = 0;
+    uint32_t raw_phase = 0, phase = 0, seg = 0;
     Segment g;
     while (ok && walk.next(g)) {
         const int n = g.tile1 - g.tile0;
         // (flags of a segment eight on: no warp is further ahead of this one, and none that far behind)
         if (cw == 0 && lane < 4) nf[(seg + 8) % kNfBufs][lane] = 0;
 #pragma unroll 1
-        for (int j = 0; j < 2 * n && ok; ++j) {
-            const bool is_v = values_at(j, n);
-            const int t = g.tile0 + tile_at(j, n);
-            asm volatile("cp.async.wait_group %0;" ::"n"(A - 1) : "memory");
-            __syncwarp();
-            const unsigned char *src = mine + st * kStep;
-            uint4 u[2] = {*reinterpret_cast<const uint4 *>(src + 16 * lane), *reinterpret_cast<const uint4 *>(src + 512 + 16 * lane)};
+        for (int j = 0; j < 2 * n; ++j) {
+            ok = wait_both(raw_full + st, raw_phase, empty_bar + stage, phase ^ 1, abort_flag);
+            if (!ok) break;
+            const unsigned char *src = raw + st * C::kRawTile;
+            uint4 u[2];
             uint32_t sc[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int c = kSameRow ? col + 4 * k : col, r = lane % kRowsU + (kSameRow ? 0 : k * kRowsU);
-                sc[k] = *reinterpret_cast<const uint16_t *>(src + 1024 + 4 * ((c >> 1) * kRowsW + r) + 2 * (c & 1));
+                u[k] = *reinterpret_cast<const uint4 *>(src + from[k]);
+                sc[k] = *reinterpret_cast<const uint16_t *>(src + scale[k]);
             }
-            __syncwarp();
-            request(st);
-            if (++st == A) st = 0;
+            const int t = g.tile0 + tile_at(j, n);
             if ((t + 1) * TK > g.safe) {  // some rows do not see all of the tile
+                const bool is_v = values_at(j, n);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int x = t * TK + row + (kSameRow ? 0 : k * kRowsU);
+                    const int x = t * TK + row[k];
                     if (x >= g.limit) {  // no row sees it
                         sc[k] = 0;
                         u[k] = make_uint4(0, 0, 0, 0);
@@ -447,31 +484,48 @@ __device__ __forceinline__ void convert_role(const Args &a, const Start &start, 
                     }
                 }
             }
-            ok = wait_bar(empty_bar + stage, phase ^ 1, abort_flag);
-            if (!ok) break;
+            unsigned char *tile = tiles + size_t(stage) * C::kTile;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int c = kSameRow ? col + 4 * k : col, r = row + (kSameRow ? 0 : k * kRowsU);
-                unsigned char *to = tiles + size_t(stage) * C::kTile + (c >> 1) * C::kChunkBytes + r * 128;
                 const uint32_t s = gdn::e4m3x2_to_f16x2(sc[k]);
-                const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
-                const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+                uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                if (kCols >= 4 && (chunk & 1)) {  // piece i ^ chunk in the place of piece i
+                    const uint32_t x = w[0], y = w[2];
+                    w[0] = w[1];
+                    w[1] = x;
+                    w[2] = w[3];
+                    w[3] = y;
+                }
+                if (kCols >= 8 && (chunk & 2)) {
+                    const uint32_t x = w[0], y = w[1], z = s0;
+                    w[0] = w[2];
+                    w[1] = w[3];
+                    w[2] = x;
+                    w[3] = y;
+                    s0 = s1;
+                    s1 = z;
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(to + ((((c & 1) * 4 + i) ^ (r & 7)) << 4)) = convert8(w[i], i < 2 ? s0 : s1);
+                for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(tile + to[k][i]) = convert8(w[i], i < 2 ? s0 : s1);
             }
             gdn::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive(full_bar + stage);
+            if (lane == 0) {
+                arrive(full_bar + stage);
+                arrive(raw_empty + st);
+            }
             if (++stage == C::kStages) {
                 stage = 0;
                 phase ^= 1;
             }
+            if (++st == C::kAhead) {
+                st = 0;
+                raw_phase ^= 1;
+            }
         }
         ++seg;
     }
-    if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
-    asm volatile("cp.async.wait_all;" ::: "memory");  // whatever has happened, no copy is under way when the CTA leaves
 }
 
 }  // namespace att
@@ -486,6 +540,7 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     constexpr int kThreads = C::kThreads, kTma = C::kTma;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages];
+    __shared__ uint64_t raw_full[k4 ? C::kAhead : 1], raw_empty[k4 ? C::kAhead : 1];
     __shared__ uint64_t s_bar[2], sfree_bar[2], p_bar[2], pv_bar[2], q_bar, ml_bar, ofree_bar, go_bar[2], clean_bar[2], drain_bar[2], never_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_s;
@@ -506,6 +561,12 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
         for (int i = 0; i < C::kStages; ++i) {
             gdn::mbar_init(full_bar + i, k4 ? C::kConvWarps : 1);
             gdn::mbar_init(empty_bar + i, 1);
+        }
+        if constexpr (k4) {
+            for (int i = 0; i < C::kAhead; ++i) {
+                gdn::mbar_init(raw_full + i, 1);
+                gdn::mbar_init(raw_empty + i, C::kConvWarps);
+            }
         }
         for (int i = 0; i < 2; ++i) {
             gdn::mbar_init(s_bar + i, 1);
@@ -600,8 +661,8 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     Walk walk(a, start);
     Segment g;
     bool ok = true;  // this warp's; false once a wait has run out
-    // (of the 4-bit cache the conversion copies and cleans)
-    const int stalled = a.stall_role == 0 ? 0 : k4 && (a.stall_role == 1 || a.stall_role == 4) ? C::kConv : C::kRowWarps + a.stall_role - 1;
+    // (of the 4-bit cache the conversion cleans)
+    const int stalled = a.stall_role == 0 ? 0 : k4 && a.stall_role == 4 ? C::kConv : C::kRowWarps + a.stall_role - 1;
     if (a.stall_ns && blockIdx.x == 0 && warp == stalled) {
         ok = __all_sync(full, gdn::mbar_wait_bounded(&never_bar, 0, a.stall_ns));
         if (!ok) *abort_flag = 1;
@@ -613,21 +674,13 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     if (k4 && warp >= C::kConv) {
         if constexpr (k4) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-            convert_role<C>(a, start, walk, tiles, full_bar, empty_bar, nf, abort_flag, ok);
+            convert_role<C>(a, walk, tiles, full_bar, empty_bar, tiles + C::kRing, raw_full, raw_empty, nf, abort_flag, ok);
         }
     } else if (warp >= C::kRowWarps) {
         if constexpr (k4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (k4 && (warp == kTma || warp == C::kClean)) {
-            // ---- the Q rows of all segments on their way into L2 ---------------------------
-            if (warp == kTma) {
-                while (walk.next(g))
-                    for (int u = lane; u < g.rows * C::kChunks; u += 32) {
-                        const int r = u / C::kChunks;
-                        const T *src = static_cast<const T *>(a.q) + (int64_t(g.q.n0) + g.i0 + r / a.G) * a.q_stride +
-                                       (int64_t(g.h) * a.G + r % a.G) * D + 64 * (u % C::kChunks);
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
-                    }
-            }
+            if constexpr (k4)
+                if (warp == kTma) copy_role<T, C>(a, walk, tiles + C::kRing, raw_full, raw_empty, abort_flag, ok);
         } else if (warp == kTma) {
             // ---- keys and values by TMA -------------------------------------------------
             asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies

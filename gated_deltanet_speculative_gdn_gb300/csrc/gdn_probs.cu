@@ -10,8 +10,8 @@
 // intrinsics keep products and sums apart), so that equal inputs give equal x and a
 // tie is a tie.
 //
-// Mapping.  A cluster of CTAs takes a row, each CTA a contiguous slice of up to 16384
-// tokens whose x, then 2^(..), stay in registers (four groups of 8 a thread): the row is
+// Mapping.  A cluster of CTAs takes a row, each CTA a slice of up to 16384 tokens
+// whose x, then 2^(..), stay in registers (four groups of 8 a thread): the row is
 // read once and written once, 6 bytes a token with 16-bit logits.  (A larger vocabulary
 // than 16 slices hold reads the rest of each slice again for every pass.)  The logits are
 // requested before the row's sequence is looked up.  Few tokens are touched by a path or
@@ -49,12 +49,12 @@ struct ProbsArgs {
     int64_t p_stride;
     int32_t *status;
     int S, N, P, V, max_nodes, n_bias, n_masks;
-    int groups, per;  // groups of 8 tokens: of a row, of a CTA
+    int groups, per;  // groups of 8 tokens: of a row, of a CTA (a multiple of 32)
 };
 
 // What a row needs beside its logits.
 struct Row {
-    float r, f, g, t;
+    float r, inv_r, f, g, t;
     int slot, mask, b0, b1, n_path;  // slot, mask: -1 for none
     int err;
 };
@@ -92,14 +92,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// One token's penalties; h: its 16 bits of history, not 0.
+// One token's penalties; h: its 16 bits of history.
 __device__ __forceinline__ float penalised(float x, uint32_t h, const Row &row) {
-    const float in = x;
-    x = x > 0.f ? __fdiv_rn(x, row.r) : __fmul_rn(x, row.r);
     const uint32_t c = h & 0x7fffu;
-    x = __fsub_rn(x, __fmul_rn(row.f, float(c)));
-    if (c) x = __fsub_rn(x, row.g);
-    return fabsf(in) <= FLT_MAX ? fminf(fmaxf(x, -FLT_MAX), FLT_MAX) : x;
+    float y = __fmul_rn(x, x > 0.f ? row.inv_r : row.r);
+    // (c as a float: it fits below 2^23)
+    y = __fsub_rn(y, __fmul_rn(row.f, __uint_as_float(0x4b000000u | c) - 8388608.f));
+    y = c ? __fsub_rn(y, row.g) : y;
+    y = fabsf(x) <= FLT_MAX ? fminf(fmaxf(y, -FLT_MAX), FLT_MAX) : y;
+    return h ? y : x;
 }
 
 template <typename T>
@@ -116,7 +117,10 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = int(blockIdx.x) / C;
-    const int g0 = rank * a.per, g1 = min(a.groups, g0 + a.per);
+    // The row's groups in runs of 32, one a warp, dealt out over the cluster's warps: what a part of the vocabulary costs
+    // (frequent tokens, which the history holds, are neighbours as a rule) all of them share.
+    auto group = [&](int local) { return ((local >> 5) * C + rank) * 32 + (local & 31); };
+    const int locals = a.per;
     auto arrived = cl.barrier_arrive();  // every CTA of the cluster runs before one writes to another
     gdn::grid_dep_wait();
 
@@ -124,8 +128,8 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     Raw<T> raw[kGroups];
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        const int g = g0 + k * kThreads + tid;
-        if (g < g1) raw[k] = load_raw<T>(lrow, g);
+        const int g = group(k * kThreads + tid);
+        if (k * kThreads + tid < locals && g < a.groups) raw[k] = load_raw<T>(lrow, g);
     }
 
     // ---- the row's sequence, its path and its lists ---------------------------------
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     if (warp == 0) {
         const int s = gdn::find_sequence(a.node_off, a.S, n);
         const int n0 = a.node_off[s], n1 = a.node_off[s + 1], i = n - n0;
-        Row r{1.f, 0.f, 0.f, 1.f, -1, -1, 0, 0, 0, 0};
+        Row r{1.f, 1.f, 0.f, 0.f, 1.f, -1, -1, 0, 0, 0, 0};
         if (i < 0 || n >= n1 || n1 > a.N || n1 - n0 > a.max_nodes || n0 < 0 || (s == 0 && n0 != 0) || (s == a.S - 1 && n1 != a.N)) {
             r.err = GDN_DEV_BAD_NODE_OFF;
         } else {
@@ -153,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
             }
             if (counts) {
                 if (a.repetition) r.r = a.repetition[s];
+                r.inv_r = __fdiv_rn(1.f, r.r);
                 if (a.frequency) r.f = a.frequency[s];
                 if (a.presence) r.g = a.presence[s];
                 if (a.history) {
@@ -189,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     const Row row = row_s;
     bool bad = false;
     auto touch = [&](int token) {  // marks the group of a token that lies in this slice
-        const int g = (token >> 3) - g0;
-        if (g >= 0 && g < g1 - g0) atomicOr(mark + ((g & (kMarkBits - 1)) >> 5), 1u << (g & 31));
+        const int g = token >> 3, run = g >> 5;
+        if (run % C == rank) atomicOr(mark + (run / C & (kMarkBits / 32 - 1)), 1u << (g & 31));
     };
     if (!row.err) {
         for (int k = tid; k < row.n_path; k += kThreads) touch(path_s[k]);
@@ -212,11 +217,10 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         row.mask >= 0 ? reinterpret_cast<const unsigned char *>(a.mask + int64_t(row.mask) * a.mask_stride) : nullptr;
     const uint4 none = make_uint4(0, 0, 0, 0);
     // x of group g
-    auto form = [&](const Raw<T> &in, uint4 h, uint32_t allowed, int g, float (&x)[8]) {
+    auto form = [&](const Raw<T> &in, uint4 h, uint32_t allowed, int local, int g, float (&x)[8]) {
         unpack_raw<T>(in, x);
         uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-        const int lg = (g - g0) & (kMarkBits - 1);
-        const bool marked = (mark[lg >> 5] >> (lg & 31)) & 1;
+        const bool marked = (mark[(local >> 5) & (kMarkBits / 32 - 1)] >> (local & 31)) & 1;
         if (marked) {
             for (int k = 0; k < row.n_path; ++k) {
                 const int t = path_s[k];
@@ -230,8 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         if (hw[0] | hw[1] | hw[2] | hw[3]) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t he = (hw[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                if (he) x[e] = penalised(x[e], he, row);
+                x[e] = penalised(x[e], (hw[e >> 1] >> (16 * (e & 1))) & 0xffffu, row);
             }
         }
         if (marked && row.b1 > row.b0) {
@@ -262,9 +265,11 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     auto allowed_of = [&](int g) { return mrow ? uint32_t(mrow[g]) : 0xffu; };
     // the groups that registers do not hold
     auto for_rest = [&](auto &&body) {
-        for (int g = g0 + kGroups * kThreads + tid; g < g1; g += kThreads) {
+        for (int local = kGroups * kThreads + tid; local < locals; local += kThreads) {
+            const int g = group(local);
+            if (g >= a.groups) break;
             float x[8];
-            form(load_raw<T>(lrow, g), history_of(g), allowed_of(g), g, x);
+            form(load_raw<T>(lrow, g), history_of(g), allowed_of(g), local, g, x);
             body(g, x);
         }
     };
@@ -275,19 +280,19 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         uint32_t allowed[kGroups];
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
-            const int g = g0 + k * kThreads + tid;
+            const int g = group(k * kThreads + tid);
             h[k] = none;
             allowed[k] = 0;
-            if (g < g1) {
+            if (k * kThreads + tid < locals && g < a.groups) {
                 h[k] = history_of(g);
                 allowed[k] = allowed_of(g);
             }
         }
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
-            const int g = g0 + k * kThreads + tid;
-            if (g < g1) {
-                form(raw[k], h[k], allowed[k], g, x[k]);
+            const int g = group(k * kThreads + tid);
+            if (k * kThreads + tid < locals && g < a.groups) {
+                form(raw[k], h[k], allowed[k], k * kThreads + tid, g, x[k]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[k][e] = -INFINITY;
@@ -315,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
 
     // ---- its exponentials and their sum, or the first place of its maximum ------------------
     const bool greedy = !(row.t > 0.f);
-    const float c = greedy ? 0.f : fminf(__fdiv_rn(1.4426950408889634f, row.t), FLT_MAX);
-    // (x = -inf is 0 even where c is 0, and nothing where the slice's m is -inf; NaN stays NaN)
-    auto weight = [&](float v) { return v == -INFINITY ? 0.f : exp2_fast(__fmul_rn(__fsub_rn(v, m), c)); };
+    // (c is neither 0 nor infinite, and m0 no infinity below, so that x = -inf gives 0; NaN stays NaN)
+    const float c = fminf(fmaxf(__fdiv_rn(1.4426950408889634f, row.t), FLT_MIN), FLT_MAX), m0 = m == -INFINITY ? 0.f : m;
+    auto weight = [&](float v) { return exp2_fast(__fmul_rn(__fsub_rn(v, m0), c)); };
     Part mine{m, 0.f, INT32_MAX, 0};
     if (greedy) {
         auto look = [&](int g, float (&y)[8]) {
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
             }
         };
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) look(g0 + k * kThreads + tid, x[k]);
+        for (int k = 0; k < kGroups; ++k) look(group(k * kThreads + tid), x[k]);
         for_rest(look);
         mine.best = __reduce_min_sync(full, mine.best);
         mine.nan = __reduce_or_sync(full, mine.nan);
@@ -393,7 +398,9 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
             nan |= parts[k].nan;
         }
         const float no = nan ? __uint_as_float(0x7fffffffu) : 0.f, yes = nan ? no : 1.f;
-        for (int g = g0 + tid; g < g1; g += kThreads) {
+        for (int local = tid; local < locals; local += kThreads) {
+            const int g = group(local);
+            if (g >= a.groups) break;
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = 8 * g + e == best ? yes : no;
@@ -408,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     const float f = total == 0.f ? 0.f : m == -INFINITY ? total * 0.f : exp2_fast(__fmul_rn(__fsub_rn(m, M), c)) / total;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-        const int g = g0 + k * kThreads + tid;
-        if (g < g1) {
+        const int g = group(k * kThreads + tid);
+        if (k * kThreads + tid < locals && g < a.groups) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] *= f;
             store(g, x[k]);
@@ -540,7 +547,7 @@ int launch_probs(const ProbsArgs &args, int64_t rows, int vocab, cudaStream_t st
     int C = 1;
     while (C < kMaxCluster && (int64_t(C) * kSlice < vocab || (rows * 2 * C <= 304 && vocab / (2 * C) >= 2048))) C *= 2;
     a.groups = int((int64_t(vocab) + 7) / 8);
-    a.per = (a.groups + C - 1) / C;
+    a.per = ((a.groups + 31) / 32 + C - 1) / C * 32;
     auto k = logits_probs_kernel<T>;
     if (C > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return GDN_ERR_LAUNCH;
     if (rows * C > INT32_MAX) return GDN_ERR_DIMS;

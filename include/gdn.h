@@ -492,7 +492,7 @@ int gdn_kvq_commit(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride
  * token y, with c(y) the times y was produced (history's count and the path's,
  * 32767 at most) and `seen` for c(y) > 0 or y in the prompt:
  *     x = logits[n][y]
- *     x = x > 0 ? x / repetition[s] : x * repetition[s]            where seen
+ *     x = x > 0 ? x * (1 / repetition[s]) : x * repetition[s]      where seen
  *     x = x - frequency[s] * c(y);  x = x - presence[s] where c(y) > 0
  *     x = x + bias(y)
  *     x = -infinity                                  where the mask forbids y
