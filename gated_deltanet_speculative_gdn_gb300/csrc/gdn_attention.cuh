@@ -656,10 +656,9 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
         }
     }
     __syncthreads();
-    const Start start = start_s;
     const uint32_t tmem = tmem_slot;
-    Walk walk(a, start);
-    Segment g;
+    // (Every role makes a walk of its own: one made here for all of them stays in registers through their branches, and
+    // the 4-bit cache's kernel spills 800 bytes a thread.)
     bool ok = true;  // this warp's; false once a wait has run out
     // (of the 4-bit cache the conversion cleans)
     const int stalled = a.stall_role == 0 ? 0 : k4 && a.stall_role == 4 ? C::kConv : C::kRowWarps + a.stall_role - 1;
@@ -674,14 +673,19 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     if (k4 && warp >= C::kConv) {
         if constexpr (k4) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+            Walk walk(a, start_s);
             convert_role<C>(a, walk, tiles, full_bar, empty_bar, tiles + C::kRing, raw_full, raw_empty, nf, abort_flag, ok);
         }
     } else if (warp >= C::kRowWarps) {
         if constexpr (k4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (k4 && (warp == kTma || warp == C::kClean)) {
-            if constexpr (k4)
+            if constexpr (k4) {
+                Walk walk(a, start_s);
                 if (warp == kTma) copy_role<T, C>(a, walk, tiles + C::kRing, raw_full, raw_empty, abort_flag, ok);
+            }
         } else if (warp == kTma) {
+            Walk walk(a, start_s);
+            Segment g;
             // ---- keys and values by TMA -------------------------------------------------
             asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
             const int ps = 1 << a.pl.shift, np = max(1, TK / ps);  // pages of a tile
@@ -767,6 +771,8 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
             constexpr uint32_t fmt = std::is_same<E, __nv_bfloat16>::value ? 1u : 0u;
             constexpr uint32_t kIdS = (1u << 4) | (fmt << 7) | (fmt << 10) | (uint32_t(TK >> 3) << 17) | (8u << 24);
             constexpr uint32_t kIdO = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | (uint32_t(D >> 3) << 17) | (8u << 24);
+            Walk walk(a, start_s);
+            Segment g;
             const bool is_s = warp == C::kMmaS;
             const int rows = k4 ? TK : box_rows(a.pl.shift);
             uint32_t seg = 0, masked = 0, asked = 0;
@@ -845,6 +851,8 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
             gdn::mbar_wait_bounded(drain_bar + (is_s ? 0 : 1), 0);
         } else {
             // ---- values of tiles that not every row sees whole ----------------------------
+            Walk walk(a, start_s);
+            Segment g;
             long long loads = 0;  // ring position of the segment's first load
             uint32_t seg = 0, masked = 0;
             // the exponents of two values, and their lowest bits
@@ -998,6 +1006,8 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
             __syncwarp();
             if (lane == 0) arrive(&q_bar);
         };
+        Walk walk(a, start_s);
+        Segment g;
         bool more = ok && walk.next(g);
         if (more) load_q(g);
         while (ok && more) {
