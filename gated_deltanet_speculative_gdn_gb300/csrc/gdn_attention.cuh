@@ -150,6 +150,74 @@ struct Start {
     long long count;  // units of this CTA
 };
 
+// The schedule: units of all sequences, cut into equal shares; one thread of the CTA writes where its share begins
+// (start_s.count is 0 before).  sync: the CTA's barrier; another has to follow.
+template <int kThreads, typename Sync>
+__device__ __forceinline__ void schedule(const Args &a, long long *wsum, Start &start_s, Sync &&sync) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned full = 0xffffffffu;
+    const int per = (a.S + kThreads - 1) / kThreads;
+    long long mine = 0;
+    Seq q0{0, 0, 0};  // the thread's first sequence (its only one up to kThreads of them)
+    for (int k = 0; k < per; ++k) {
+        const int s = tid * per + k;
+        if (s >= a.S) break;
+        int err;
+        const Seq q = checked(a, s, load_raw(a, s), &err);
+        if (k == 0) q0 = q;
+        if (err && blockIdx.x == 0) gdn::record_status(a.status, err);
+        mine += head_units(q, a.R) * a.Hkv;
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(full, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    sync();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) before = total;
+        total += wsum[w];
+    }
+    before += inc - mine;
+    {
+        const long long active = min((long long)gridDim.x, total);
+        const int b = blockIdx.x;
+        if (b < active) {
+            // (32-bit division where it does: the 64-bit one is a call)
+            const bool small = total < (1 << 23);  // times at most 2^8 CTAs and below 2^31
+            const long long t0 = small && active <= 256 ? unsigned(total) * unsigned(b) / unsigned(active) : total * b / active;
+            const long long t1 =
+                small && active <= 256 ? unsigned(total) * unsigned(b + 1) / unsigned(active) : total * (b + 1) / active;
+            if (mine > 0 && t0 >= before && t0 < before + mine) {  // one thread of the CTA
+                long long x = t0 - before;
+                for (int k = 0; k < per; ++k) {
+                    const int s = tid * per + k;
+                    const Seq q = k == 0 ? q0 : checked(a, s, load_raw(a, s));
+                    const long long ht = head_units(q, a.R);
+                    if (x >= ht * a.Hkv) {
+                        x -= ht * a.Hkv;
+                        continue;
+                    }
+                    const int h = small ? int(unsigned(x) / unsigned(ht)) : int(x / ht);
+                    x -= h * ht;
+                    int lo = 0, hi = (q.n + a.R - 1) / a.R;  // the last row tile with units_before <= x
+                    while (hi - lo > 1) {
+                        const int mid = (lo + hi) / 2;
+                        if (units_before(q, mid, a.R) <= x) lo = mid;
+                        else hi = mid;
+                    }
+                    start_s = Start{q, s, h, lo, int(x - units_before(q, lo, a.R)), t1 - t0};
+                    break;
+                }
+            }
+        }
+    }
+}
+
 // A CTA's run through its share, segment by segment (a segment: consecutive tiles
 // of one item).  Every role walks it for itself.
 struct Segment {
@@ -592,69 +660,11 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     }
     gdn::grid_dep_wait();  // lengths, q, the pools and the workspace
 
-    // ---- the schedule: units of all sequences, cut into equal shares ------------
-    const int per = (a.S + kThreads - 1) / kThreads;
-    long long mine = 0;
-    Seq q0{0, 0, 0};  // the thread's first sequence (its only one up to kThreads of them)
-    for (int k = 0; k < per; ++k) {
-        const int s = tid * per + k;
-        if (s >= a.S) break;
-        int err;
-        const Seq q = checked(a, s, load_raw(a, s), &err);
-        if (k == 0) q0 = q;
-        if (err && blockIdx.x == 0) gdn::record_status(a.status, err);
-        mine += head_units(q, a.R) * a.Hkv;
-    }
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(full, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    gdn::tc_fence_before_sync();
-    __syncthreads();
-    gdn::tc_fence_after_sync();
-    long long total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w == warp) before = total;
-        total += wsum[w];
-    }
-    before += inc - mine;
-    {
-        const long long active = min((long long)gridDim.x, total);
-        const int b = blockIdx.x;
-        if (b < active) {
-            // (32-bit division where it does: the 64-bit one is a call)
-            const bool small = total < (1 << 23);  // times at most 2^8 CTAs and below 2^31
-            const long long t0 = small && active <= 256 ? unsigned(total) * unsigned(b) / unsigned(active) : total * b / active;
-            const long long t1 =
-                small && active <= 256 ? unsigned(total) * unsigned(b + 1) / unsigned(active) : total * (b + 1) / active;
-            if (mine > 0 && t0 >= before && t0 < before + mine) {  // one thread of the CTA
-                long long x = t0 - before;
-                for (int k = 0; k < per; ++k) {
-                    const int s = tid * per + k;
-                    const Seq q = k == 0 ? q0 : checked(a, s, load_raw(a, s));
-                    const long long ht = head_units(q, a.R);
-                    if (x >= ht * a.Hkv) {
-                        x -= ht * a.Hkv;
-                        continue;
-                    }
-                    const int h = small ? int(unsigned(x) / unsigned(ht)) : int(x / ht);
-                    x -= h * ht;
-                    int lo = 0, hi = (q.n + a.R - 1) / a.R;  // the last row tile with units_before <= x
-                    while (hi - lo > 1) {
-                        const int mid = (lo + hi) / 2;
-                        if (units_before(q, mid, a.R) <= x) lo = mid;
-                        else hi = mid;
-                    }
-                    start_s = Start{q, s, h, lo, int(x - units_before(q, lo, a.R)), t1 - t0};
-                    break;
-                }
-            }
-        }
-    }
+    schedule<kThreads>(a, wsum, start_s, [] {
+        gdn::tc_fence_before_sync();
+        __syncthreads();
+        gdn::tc_fence_after_sync();
+    });
     __syncthreads();
     const uint32_t tmem = tmem_slot;
     // (Every role makes a walk of its own: one made here for all of them stays in registers through their branches, and
