@@ -38,7 +38,7 @@ struct Cfg {
     static constexpr int kRowWarps = 4 * kStreams;
     static constexpr int kTma = kRowWarps, kMmaS = kTma + 1, kMmaO = kTma + 2, kClean = kTma + 3;
     // 8 or 12 warps: two or three to a scheduler; with the 4-bit cache 16, the last of them its conversion
-    static constexpr int kConv = kRowWarps + 4, kConvWarps = D / 32;
+    static constexpr int kConv = kRowWarps + 4, kConvWarps = D / 32, kConvGroup = kConvWarps / 2;
     static constexpr int kThreads = k4 ? 512 : 32 * (kRowWarps + 4);
     static_assert(!k4 || kConv + kConvWarps <= kThreads / 32, "warps");
     static constexpr int kChunks = D / 64;                // 128-byte columns of a row
@@ -47,9 +47,9 @@ struct Cfg {
     static constexpr uint32_t kRing = k4 ? 131072 : 196608;
     static constexpr int kStages = kRing / kTile;
     // a second ring, of tiles of codes and scales as they lie in memory
-    static constexpr int kAhead = D == 256 ? 8 : 16;
+    static constexpr int kAhead = D == 256 ? 8 : D == 128 ? 12 : 16;
     static constexpr uint32_t kCodeRow = D / 2, kScaleRow = D / 16, kRawTile = TK * (kCodeRow + kScaleRow);
-    static constexpr size_t kSmem = 1024 + kRing + (k4 ? kAhead * kRawTile : 0);
+    static constexpr size_t kSmem = 1024 + kRing + (k4 ? kAhead * kRawTile + kRowWarps * 4096 : 0);  // (4096: q's turn)
     // tensor-memory columns
     static constexpr int kSBufs = kStreams;
     static constexpr uint32_t kO = 0, kQ = kStreams * D, kS = kQ + D / 2, kP = kS + kSBufs * TK;
@@ -486,48 +486,48 @@ __device__ __forceinline__ bool values_at(int j, int n) { return j == 2 * n - 1 
 __device__ __forceinline__ int tile_at(int j, int n) { return j == 2 * n - 1 ? n - 1 : j == 0 ? 0 : (j & 1) ? (j + 1) / 2 : j / 2 - 1; }
 
 // ---- raw tiles as fp16 in the ring of tiles ------------------------------------------------
-// A thread takes two units of a tile of keys or values, 32 elements (16 bytes of codes, two
-// scales) of a position each: a warp reads 512 consecutive bytes, and writes each unit as four
-// 16-byte pieces in the 128-byte swizzle.  A position's units lie in its 64-column chunks, whose
-// equal pieces share banks, so the lanes of chunk c begin at piece c.
+// Two groups of warps take the tiles (of keys and of values) in turn: a tile's way through a
+// warp is a chain of ~1300 cycles, mostly waits, which two tiles at a time share.
+// A thread takes four units of a tile, 32 elements (16 bytes of codes, two scales) of a position
+// each: a warp reads 512 consecutive bytes, and writes each unit as four 16-byte pieces in the
+// 128-byte swizzle.  A position's units lie in its 64-column chunks, whose equal pieces share
+// banks, so the lanes of chunk c begin at piece c.
 template <typename C>
 __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned char *tiles, uint64_t *full_bar, uint64_t *empty_bar,
                                              const unsigned char *raw, uint64_t *raw_full, uint64_t *raw_empty, uint32_t (*nf)[4],
                                              volatile int *abort_flag, bool ok) {
-    constexpr int D = C::D, kCols = D / 32;  // units of a position
-    const int lane = threadIdx.x & 31, cw = (threadIdx.x >> 5) - C::kConv;
-    if (cw >= C::kConvWarps) return;
+    constexpr int D = C::D, kCols = D / 32, kUnits = 4;
+    static_assert(C::kConvGroup * 32 * kUnits == TK * kCols && C::kStages % 2 == 0 && C::kAhead % 2 == 0, "units of a tile");
+    const int lane = threadIdx.x & 31, all = (threadIdx.x >> 5) - C::kConv;
+    if (all >= C::kConvWarps) return;
+    const int group = all / C::kConvGroup, cw = all % C::kConvGroup;
     const int run = raw_run(a.pl.shift), piece_bytes = run * int(C::kCodeRow + C::kScaleRow);
-    const int chunk = (lane % kCols) >> 1;   // the same for both units
-    int row[2];
-    uint32_t from[2], scale[2], to[2][4];
+    const int col = lane % kCols, chunk = col >> 1;   // the same for all units
+    int row[kUnits];
+    uint32_t from[kUnits], scale[kUnits];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int u = cw * 64 + 32 * k + lane, col = u % kCols;
-        row[k] = u / kCols;
+    for (int k = 0; k < kUnits; ++k) {
+        row[k] = (cw * 32 * kUnits + 32 * k + lane) / kCols;
         const uint32_t piece = row[k] / run * piece_bytes, r = row[k] % run;
         from[k] = piece + r * C::kCodeRow + 16 * col;
         scale[k] = piece + run * C::kCodeRow + r * C::kScaleRow + 2 * col;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            to[k][i] = chunk * C::kChunkBytes + row[k] * 128 + ((((col & 1) * 4 + (i ^ (chunk & 3))) ^ (row[k] & 7)) << 4);
     }
-    int st = 0, stage = 0;
+    int st = group, stage = group;
     uint32_t raw_phase = 0, phase = 0, seg = 0;
     Segment g;
     while (ok && walk.next(g)) {
         const int n = g.tile1 - g.tile0;
         // (flags of a segment eight on: no warp is further ahead of this one, and none that far behind)
-        if (cw == 0 && lane < 4) nf[(seg + 8) % kNfBufs][lane] = 0;
+        if (all == 0 && lane < 4) nf[(seg + 8) % kNfBufs][lane] = 0;
 #pragma unroll 1
-        for (int j = 0; j < 2 * n; ++j) {
-            ok = wait_both(raw_full + st, raw_phase, empty_bar + stage, phase ^ 1, abort_flag);
+        for (int j = group; j < 2 * n; j += 2) {
+            ok = wait_bar(raw_full + st, raw_phase, abort_flag);
             if (!ok) break;
             const unsigned char *src = raw + st * C::kRawTile;
-            uint4 u[2];
-            uint32_t sc[2];
+            uint4 u[kUnits];
+            uint32_t sc[kUnits];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < kUnits; ++k) {
                 u[k] = *reinterpret_cast<const uint4 *>(src + from[k]);
                 sc[k] = *reinterpret_cast<const uint16_t *>(src + scale[k]);
             }
@@ -535,7 +535,7 @@ __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned
             if ((t + 1) * TK > g.safe) {  // some rows do not see all of the tile
                 const bool is_v = values_at(j, n);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < kUnits; ++k) {
                     const int x = t * TK + row[k];
                     if (x >= g.limit) {  // no row sees it
                         sc[k] = 0;
@@ -552,9 +552,11 @@ __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned
                     }
                 }
             }
-            unsigned char *tile = tiles + size_t(stage) * C::kTile;
+            ok = wait_bar(empty_bar + stage, phase ^ 1, abort_flag);
+            if (!ok) break;
+            unsigned char *tile = tiles + size_t(stage) * C::kTile + chunk * C::kChunkBytes;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < kUnits; ++k) {
                 const uint32_t s = gdn::e4m3x2_to_f16x2(sc[k]);
                 uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
                 uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
@@ -574,8 +576,10 @@ __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned
                     s0 = s1;
                     s1 = z;
                 }
+                unsigned char *to = tile + row[k] * 128;
+                const int first = ((col & 1) * 4) ^ (chunk & 3) ^ (row[k] & 7);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(tile + to[k][i]) = convert8(w[i], i < 2 ? s0 : s1);
+                for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(to + ((first ^ i) << 4)) = convert8(w[i], i < 2 ? s0 : s1);
             }
             gdn::fence_proxy_async_smem();
             __syncwarp();
@@ -583,17 +587,96 @@ __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned
                 arrive(full_bar + stage);
                 arrive(raw_empty + st);
             }
-            if (++stage == C::kStages) {
-                stage = 0;
+            if ((stage += 2) >= C::kStages) {
+                stage = group;
                 phase ^= 1;
             }
-            if (++st == C::kAhead) {
-                st = 0;
+            if ((st += 2) >= C::kAhead) {
+                st = group;
                 raw_phase ^= 1;
             }
         }
         ++seg;
     }
+}
+
+// The 4-bit cache's kernel: a warp's 32 rows of q into its lanes of tensor memory (column `to` on), as fp16; returns what a
+// row's scores are to be multiplied by, to its lane.  fp16 does not hold every bf16: such a row is scaled by a power of
+// two that brings its largest element to 2^14 .. 2^15.  (Infinities and NaN stay what they are.)  Four rows at a time, an
+// eighth of a warp to 128 bytes of one, then through shared memory (`turn`, 4 KB) to the rows' own lanes.
+// One copy of little code: unrolled and in line at both places where it is called it is 40 KB, which a CTA runs through
+// once or twice, at the pace at which instructions come in (30,000 cycles each time; so 6,000).
+template <typename T, typename C>
+__device__ __noinline__ float load_q_rows(const T *q, int64_t q_stride, int64_t token, int head, int G, int rows, unsigned char *turn,
+                                          float *back, uint32_t to) {
+    constexpr bool scaled = !std::is_same<T, __half>::value;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, stream = threadIdx.x >> 7;
+    const T *src[8];
+    int row = 32 * w + lane / 8, tok = row / G, hd = row % G;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        src[i] = row < rows ? q + (token + tok) * q_stride + (int64_t(head) * G + hd) * C::D + (lane % 8) * 8 : nullptr;
+        row += 4;
+        for (hd += 4; hd >= G; hd -= G) ++tok;
+    }
+    float f[8];
+    if constexpr (scaled) {
+        uint32_t top[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = 0;
+#pragma unroll 1
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = src[i] ? *reinterpret_cast<const uint4 *>(src[i] + 64 * ch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                top[i] = __vmaxu2(top[i], __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                                   __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t x = max(top[i] & 0xffffu, top[i] >> 16);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+            const int e = int(x >> 7), s = e == 255 ? 0 : min(14 + 127 - e, 100);
+            f[i] = __uint_as_float(uint32_t(127 + s) << 23);
+            if (lane % 8 == 0) back[4 * i + lane / 8] = __uint_as_float(uint32_t(127 - s) << 23);
+        }
+        __syncwarp();
+    }
+#pragma unroll 1
+    for (int ch = C::kStreams == 2 ? stream : 0; ch < C::kChunks; ch += C::kStreams) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = src[i] ? *reinterpret_cast<const uint4 *>(src[i] + 64 * ch) : make_uint4(0, 0, 0, 0);
+        const int place = (lane % 8) << 4, x0 = (lane / 8) << 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (scaled) {
+                float y[8];
+                gdn::unpack8<T>(v[i], y);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) y[z] *= f[i];
+                v[i] = gdn::pack8<__half>(y);
+            }
+            *reinterpret_cast<uint4 *>(turn + (4 * i + lane / 8) * 128 + (place ^ x0 ^ ((i & 1) << 6))) = v[i];
+        }
+        __syncwarp();
+        uint32_t r[32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(turn + lane * 128 + ((k ^ (lane & 7)) << 4));
+            r[4 * k] = x.x;
+            r[4 * k + 1] = x.y;
+            r[4 * k + 2] = x.z;
+            r[4 * k + 3] = x.w;
+        }
+        tmem_st32(to + 32 * ch, r);
+        __syncwarp();
+    }
+    tmem_wait_st();
+    return scaled ? back[lane] : 1.f;
 }
 
 }  // namespace att
@@ -616,6 +699,7 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     __shared__ long long wsum[kThreads / 32];
     __shared__ int tree_par[C::kRowWarps][gdn::kMaxSeqNodes];
     __shared__ float2 ml[2][C::kStreams][kRows];  // by segment: m and l of each stream's rows
+    __shared__ float back[k4 ? C::kRowWarps : 1][32];  // factors of q's rows
     __shared__ uint32_t nf[kNfBufs][4];  // by segment: positions from `safe` on with values that are not finite
     volatile int *abort_flag = &abort_s;
     unsigned char *tiles =
@@ -627,13 +711,13 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     gdn::grid_dep_launch();
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            gdn::mbar_init(full_bar + i, k4 ? C::kConvWarps : 1);
+            gdn::mbar_init(full_bar + i, k4 ? C::kConvGroup : 1);
             gdn::mbar_init(empty_bar + i, 1);
         }
         if constexpr (k4) {
             for (int i = 0; i < C::kAhead; ++i) {
                 gdn::mbar_init(raw_full + i, 1);
-                gdn::mbar_init(raw_empty + i, C::kConvWarps);
+                gdn::mbar_init(raw_empty + i, C::kConvGroup);
             }
         }
         for (int i = 0; i < 2; ++i) {
@@ -959,27 +1043,20 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
         int line_s = -1;
         // A segment's Q rows into tensor memory, once every S of the segment before has been formed.
         auto load_q = [&](const Segment &sg) {
+            if constexpr (k4) {
+                if (w * 32 < sg.rows)
+                    c_next = a.c * load_q_rows<T, C>(static_cast<const T *>(a.q), a.q_stride, int64_t(sg.q.n0) + sg.i0, sg.h, a.G, sg.rows,
+                                                     tiles + C::kRing + C::kAhead * C::kRawTile + warp * 4096, back[warp], trow + C::kQ);
+                gdn::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive(&q_bar);
+                return;
+            }
             if (w * 32 < sg.rows) {
                 const int hd = sg.h * a.G + row % a.G;
                 const bool live = row < sg.rows;
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) +
                                                                    (int64_t(sg.q.n0) + sg.i0 + row / a.G) * a.q_stride + int64_t(hd) * D);
-                // fp16 does not hold every bf16: the row is scaled by a power of two that brings its largest element to
-                // 2^14 .. 2^15, which c takes back.  (Infinities and NaN stay what they are.)
-                float f = 1.f;
-                if constexpr (k4 && !std::is_same<T, E>::value) {
-                    uint32_t top = 0;
-#pragma unroll 8
-                    for (int k = 0; k < D / 8; ++k) {
-                        const uint4 v = live ? src[k] : make_uint4(0, 0, 0, 0);
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-                    }
-                    const int e = int(max(top & 0xffffu, top >> 16) >> 7);
-                    const int s = e == 255 ? 0 : min(14 + 127 - e, 100);
-                    f = __uint_as_float(uint32_t(127 + s) << 23);
-                    c_next = a.c * __uint_as_float(uint32_t(127 - s) << 23);
-                }
                 constexpr int kAhead = C::kStreams == 2 ? 1 : 2;  // chunks whose loads go out before the first is waited for
 #pragma unroll
                 for (int z0 = 0; z0 < (C::kChunks + C::kStreams - 1) / C::kStreams; z0 += kAhead) {
@@ -989,14 +1066,7 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
                         const int cc = (z0 + z) * C::kStreams + (C::kStreams == 2 ? stream : 0);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            uint4 v = live && cc < C::kChunks ? src[8 * cc + k] : make_uint4(0, 0, 0, 0);
-                            if constexpr (k4 && !std::is_same<T, E>::value) {
-                                float y[8];
-                                gdn::unpack8<T>(v, y);
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) y[x] *= f;
-                                v = gdn::pack8<E>(y);
-                            }
+                            const uint4 v = live && cc < C::kChunks ? src[8 * cc + k] : make_uint4(0, 0, 0, 0);
                             q[z][4 * k] = v.x;
                             q[z][4 * k + 1] = v.y;
                             q[z][4 * k + 2] = v.z;

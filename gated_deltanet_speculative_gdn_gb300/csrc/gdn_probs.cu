@@ -103,7 +103,8 @@ __device__ __forceinline__ float penalised(float x, uint32_t h, const Row &row) 
     return h ? y : x;
 }
 
-template <typename T>
+// kRest: the vocabulary is larger than the cluster's registers.
+template <typename T, bool kRest>
 __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsArgs a) {
     __shared__ Row row_s;
     __shared__ int path_s[gdn::kMaxSeqNodes];
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         row.mask >= 0 ? reinterpret_cast<const unsigned char *>(a.mask + int64_t(row.mask) * a.mask_stride) : nullptr;
     const uint4 none = make_uint4(0, 0, 0, 0);
     // x of group g
-    auto form = [&](const Raw<T> &in, uint4 h, uint32_t allowed, int local, int g, float (&x)[8]) {
+    auto form = [&](const Raw<T> &in, uint4 h, uint32_t allowed, int local, int g, float (&x)[8]) __attribute__((always_inline)) {
         unpack_raw<T>(in, x);
         uint32_t hw[4] = {h.x, h.y, h.z, h.w};
         const bool marked = (mark[(local >> 5) & (kMarkBits / 32 - 1)] >> (local & 31)) & 1;
@@ -227,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
                 if (t >> 3 != g) continue;
                 const int sh = 16 * (t & 1);
 #pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    if (z == ((t & 7) >> 1) && ((hw[z] >> sh) & 0x7fffu) != 0x7fffu) hw[z] += 1u << sh;
+                for (int z = 0; z < 4; ++z)  // (as a sum for all: a choice of one would put them in memory)
+                    hw[z] += z == ((t & 7) >> 1) && ((hw[z] >> sh) & 0x7fffu) != 0x7fffu ? 1u << sh : 0u;
             }
         }
         if (hw[0] | hw[1] | hw[2] | hw[3]) {
@@ -249,8 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
                 if (t >> 3 != g) break;
                 const float b = a.bias_value[lo];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e == (t & 7)) x[e] = __fadd_rn(x[e], b);
+                for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(x[e], e == (t & 7) ? b : 0.f);
             }
         }
         const int left = a.V - 8 * g;  // tokens of the group
@@ -265,12 +265,15 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     auto allowed_of = [&](int g) { return mrow ? uint32_t(mrow[g]) : 0xffu; };
     // the groups that registers do not hold
     auto for_rest = [&](auto &&body) {
-        for (int local = kGroups * kThreads + tid; local < locals; local += kThreads) {
-            const int g = group(local);
-            if (g >= a.groups) break;
-            float x[8];
-            form(load_raw<T>(lrow, g), history_of(g), allowed_of(g), local, g, x);
-            body(g, x);
+        if constexpr (kRest) {
+#pragma unroll 1
+            for (int local = kGroups * kThreads + tid; local < locals; local += kThreads) {
+                const int g = group(local);
+                if (g >= a.groups) break;
+                float x[8];
+                form(load_raw<T>(lrow, g), history_of(g), allowed_of(g), local, g, x);
+                body(g, x);
+            }
         }
     };
 
@@ -548,7 +551,7 @@ int launch_probs(const ProbsArgs &args, int64_t rows, int vocab, cudaStream_t st
     while (C < kMaxCluster && (int64_t(C) * kSlice < vocab || (rows * 2 * C <= 304 && vocab / (2 * C) >= 2048))) C *= 2;
     a.groups = int((int64_t(vocab) + 7) / 8);
     a.per = ((a.groups + 31) / 32 + C - 1) / C * 32;
-    auto k = logits_probs_kernel<T>;
+    auto k = int64_t(C) * kSlice < vocab ? logits_probs_kernel<T, true> : logits_probs_kernel<T, false>;
     if (C > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return GDN_ERR_LAUNCH;
     if (rows * C > INT32_MAX) return GDN_ERR_DIMS;
     cudaLaunchConfig_t cfg = {};
