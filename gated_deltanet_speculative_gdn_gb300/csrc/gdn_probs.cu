@@ -3,10 +3,10 @@
 // softmax), and the commit of the accepted path's tokens to the history that the
 // penalties read.
 //
-// Mathematics.  p_y = 2^(c (x_y - m)) f with m the slice's largest x, c = log2(e) / T
-// and f = 2^(c (m - M)) / sum over all slices: one exponential an element, taken
-// against the slice's own maximum and kept, so that the slices exchange their (m, sum)
-// only once.  x is formed in the documented order with one rounding a step (the
+// Mathematics.  p_y = 2^(c (x_y - m)) f with m the largest x of a warp's tokens, c =
+// log2(e) / T and f = 2^(c (m - M)) / sum over all of them: one exponential an element,
+// taken against the warp's own maximum and kept, so that the row's warps exchange their
+// (m, sum) only once, through distributed shared memory.  x is formed in the documented order with one rounding a step (the
 // intrinsics keep products and sums apart), so that equal inputs give equal x and a
 // tie is a tie.
 //
@@ -59,7 +59,7 @@ struct Row {
     int err;
 };
 
-// A CTA's (m, sum, place, NaN) as its cluster sees it.
+// A warp's (m, sum, place, NaN) as its cluster sees it.
 struct Part {
     float m, sum;
     int best, nan;
@@ -109,9 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     __shared__ Row row_s;
     __shared__ int path_s[gdn::kMaxSeqNodes];
     __shared__ uint32_t mark[kMarkBits / 32];
-    __shared__ float red[2][kWarps];
-    __shared__ int red_i[kWarps];
-    __shared__ Part parts[kMaxCluster];
+    __shared__ Part parts[kMaxCluster * kWarps];
     const unsigned full = 0xffffffffu;
     cg::cluster_group cl = cg::this_cluster();
     gdn::grid_dep_launch();
@@ -193,6 +191,24 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     }
     __syncthreads();
     const Row row = row_s;
+    const uint16_t *hrow = row.slot >= 0 ? a.history + int64_t(row.slot) * a.h_stride : nullptr;
+    const unsigned char *mrow =
+        row.mask >= 0 ? reinterpret_cast<const unsigned char *>(a.mask + int64_t(row.mask) * a.mask_stride) : nullptr;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    auto history_of = [&](int g) { return hrow ? *reinterpret_cast<const uint4 *>(hrow + int64_t(g) * 8) : none; };
+    auto allowed_of = [&](int g) { return mrow ? uint32_t(mrow[g]) : 0xffu; };
+    uint4 h[kGroups];
+    uint32_t allowed[kGroups];
+    if (!row.err) {
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int g = group(k * kThreads + tid);
+            const bool there = k * kThreads + tid < locals && g < a.groups;
+            h[k] = there ? history_of(g) : none;
+            allowed[k] = there ? allowed_of(g) : 0;
+        }
+    }
+
     bool bad = false;
     auto touch = [&](int token) {  // marks the group of a token that lies in this slice
         const int g = token >> 3, run = g >> 5;
@@ -213,10 +229,6 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         return;  // the cluster's other CTAs have read the same and leave too
     }
 
-    const uint16_t *hrow = row.slot >= 0 ? a.history + int64_t(row.slot) * a.h_stride : nullptr;
-    const unsigned char *mrow =
-        row.mask >= 0 ? reinterpret_cast<const unsigned char *>(a.mask + int64_t(row.mask) * a.mask_stride) : nullptr;
-    const uint4 none = make_uint4(0, 0, 0, 0);
     // x of group g
     auto form = [&](const Raw<T> &in, uint4 h, uint32_t allowed, int local, int g, float (&x)[8]) __attribute__((always_inline)) {
         unpack_raw<T>(in, x);
@@ -233,9 +245,11 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
             }
         }
         if (hw[0] | hw[1] | hw[2] | hw[3]) {
+            // (few tokens have a history, so a warp skips most of the eight)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x[e] = penalised(x[e], (hw[e >> 1] >> (16 * (e & 1))) & 0xffffu, row);
+                const uint32_t he = (hw[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                if (__builtin_expect(he != 0, 0)) x[e] = penalised(x[e], he, row);
             }
         }
         if (marked && row.b1 > row.b0) {
@@ -261,8 +275,6 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
                 if (!((allowed >> e) & 1)) x[e] = -INFINITY;
         }
     };
-    auto history_of = [&](int g) { return hrow ? *reinterpret_cast<const uint4 *>(hrow + int64_t(g) * 8) : none; };
-    auto allowed_of = [&](int g) { return mrow ? uint32_t(mrow[g]) : 0xffu; };
     // the groups that registers do not hold
     auto for_rest = [&](auto &&body) {
         if constexpr (kRest) {
@@ -278,32 +290,18 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     };
 
     float x[kGroups][8];
-    {
-        uint4 h[kGroups];
-        uint32_t allowed[kGroups];
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            const int g = group(k * kThreads + tid);
-            h[k] = none;
-            allowed[k] = 0;
-            if (k * kThreads + tid < locals && g < a.groups) {
-                h[k] = history_of(g);
-                allowed[k] = allowed_of(g);
-            }
-        }
+    for (int k = 0; k < kGroups; ++k) {
+        const int g = group(k * kThreads + tid);
+        if (k * kThreads + tid < locals && g < a.groups) {
+            form(raw[k], h[k], allowed[k], k * kThreads + tid, g, x[k]);
+        } else {
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            const int g = group(k * kThreads + tid);
-            if (k * kThreads + tid < locals && g < a.groups) {
-                form(raw[k], h[k], allowed[k], k * kThreads + tid, g, x[k]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][e] = -INFINITY;
-            }
+            for (int e = 0; e < 8; ++e) x[k][e] = -INFINITY;
         }
     }
 
-    // ---- the slice's maximum ----------------------------------------------------------
+    // ---- a warp's maximum; its exponentials and their sum, or the first place of its maximum -----
     float m = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k)
@@ -315,13 +313,6 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
-    if (lane == 0) red[0][warp] = m;
-    __syncthreads();
-    m = red[0][lane & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
-
-    // ---- its exponentials and their sum, or the first place of its maximum ------------------
     const bool greedy = !(row.t > 0.f);
     // (c is neither 0 nor infinite, and m0 no infinity below, so that x = -inf gives 0; NaN stays NaN)
     const float c = fminf(fmaxf(__fdiv_rn(1.4426950408889634f, row.t), FLT_MIN), FLT_MAX), m0 = m == -INFINITY ? 0.f : m;
@@ -340,10 +331,6 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         for_rest(look);
         mine.best = __reduce_min_sync(full, mine.best);
         mine.nan = __reduce_or_sync(full, mine.nan);
-        if (lane == 0) {
-            red[1][warp] = mine.nan ? 1.f : 0.f;
-            red_i[warp] = mine.best;
-        }
     } else {
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -359,27 +346,25 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
 #pragma unroll
             for (int e = 0; e < 8; ++e) s0 += weight(y[e]);
         });
-        const float s = gdn::warp_sum(s0 + s1);
-        if (lane == 0) red[1][warp] = s;
-    }
-    __syncthreads();
-    {
-        float s = red[1][lane & (kWarps - 1)];
-#pragma unroll
-        for (int o = kWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(full, s, o);
-        mine.sum = s;
-        if (greedy) {
-            mine.nan = s > 0.f;
-            mine.best = __reduce_min_sync(full, red_i[lane & (kWarps - 1)]);
-        }
+        mine.sum = gdn::warp_sum(s0 + s1);
     }
 
-    // ---- the cluster's, in rank order -----------------------------------------------------
+    // ---- the row's, from every warp of the cluster in a fixed order ------------------------
     cl.barrier_wait(std::move(arrived));
-    if (tid < C) *cl.map_shared_rank(parts + rank, tid) = mine;
+    if (lane < C) *cl.map_shared_rank(parts + rank * kWarps + warp, lane) = mine;
     cl.sync();
-    float M = -INFINITY;
-    for (int k = 0; k < C; ++k) M = fmaxf(M, parts[k].m);
+    Part all{-INFINITY, 0.f, INT32_MAX, 0};
+    for (int k = lane; k < C * kWarps; k += 32) all.m = fmaxf(all.m, parts[k].m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all.m = fmaxf(all.m, __shfl_xor_sync(full, all.m, o));
+    const float M = all.m;
+    for (int k = lane; k < C * kWarps; k += 32) {
+        const Part q = parts[k];
+        if (q.m == M) all.best = min(all.best, q.best);
+        all.nan |= q.nan;
+        all.sum += q.m == -INFINITY ? q.sum : q.sum * exp2_fast(__fmul_rn(__fsub_rn(q.m, M), c));
+    }
+    const float total = gdn::warp_sum(all.sum);
     float *prow = a.p + int64_t(n) * a.p_stride;
     auto store = [&](int g, const float (&y)[8]) {
         const int left = a.V - 8 * g;
@@ -395,11 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         }
     };
     if (greedy) {
-        int best = INT32_MAX, nan = 0;
-        for (int k = 0; k < C; ++k) {
-            if (parts[k].m == M) best = min(best, parts[k].best);
-            nan |= parts[k].nan;
-        }
+        const int best = __reduce_min_sync(full, all.best), nan = __reduce_or_sync(full, all.nan);
         const float no = nan ? __uint_as_float(0x7fffffffu) : 0.f, yes = nan ? no : 1.f;
         for (int local = tid; local < locals; local += kThreads) {
             const int g = group(local);
@@ -411,9 +392,6 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
         }
         return;
     }
-    float total = 0.f;
-    for (int k = 0; k < C; ++k)
-        total += parts[k].m == -INFINITY ? parts[k].sum : parts[k].sum * exp2_fast(__fmul_rn(__fsub_rn(parts[k].m, M), c));
     // (a NaN total stays; 0: the row has nothing left)
     const float f = total == 0.f ? 0.f : m == -INFINITY ? total * 0.f : exp2_fast(__fmul_rn(__fsub_rn(m, M), c)) / total;
 #pragma unroll
