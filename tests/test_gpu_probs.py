@@ -188,6 +188,54 @@ def test_many_rows():
     c.check()
 
 
+ROWS = [
+    # dtype, vocab, new: rows that CTAs work through one after the other, one to sixteen CTAs to a row
+    ("bf16", 16384, [16] * 21),
+    ("fp16", 65536, [16] * 6),
+    ("bf16", 65544, [7] * 14),
+    ("bf16", 131072, [1] * 90),
+    ("fp16", 140001, [16] * 5),
+    ("fp32", 32769, [10] * 17),
+    ("fp32", 131072, [16] * 4),
+    ("bf16", 262144, [16] * 3),
+]
+
+
+@pytest.mark.parametrize("k", range(len(ROWS)))
+def test_rows_one_after_the_other(k):
+    name, V, new = ROWS[k]
+    c = Probs(120 + k, name, V, new, True)
+    c.temp[3::7] = 0
+    c.biases([(5 * s) % 40 for s in range(c.S)]).masks([n if n % 3 else -1 for n in range(c.N)])
+    c.mask[6] = 0                                                 # (row 6 has nothing left)
+    c.logits[8, V // 2] = float("nan")
+    c.check()
+
+
+def test_rows_with_errors_between():
+    """Rows that are refused, beside others of the same CTAs that are not."""
+    V = 131072
+    c = Probs(140, "bf16", V, [16] * 10, True)
+    c.biases([10] * 10).masks()
+    mrow = np.arange(c.N)
+    bad = [0, 1, 2, 17, 50, 51, 159]
+    mrow[bad] = c.N
+    out = c.call(mrow=i32(mrow)).cpu()
+    assert int(c.status) == G.GDN_DEV_BAD_MASK
+    good = [n for n in range(c.N) if n not in bad]
+    ref = c.call().cpu()
+    assert int(c.status) == 0
+    assert torch.equal(out[good], ref[good]) and bool((out[bad] == 7.0).all())
+    one = Probs(140, "bf16", V, [16], True)                       # the same rows by the other kernel
+    one.biases([10]).masks()
+    for x in ("logits", "tokens"):
+        setattr(one, x, getattr(c, x)[:16])
+    one.par, one.slot, one.history, one.P, one.mask, one.bias = c.par[:1], c.slot, c.history, c.P, c.mask[:16], c.bias[:1]
+    one.rep, one.freq, one.pres, one.temp = c.rep, c.freq, c.pres, c.temp
+    again = one.call().cpu()[:, :V].double()
+    assert float(((again - ref[:16, :V].double()).abs() / (again + 1e-30)).max()) < 1e-5
+
+
 @pytest.mark.parametrize("without", ["rep", "freq", "pres", "temp", "history", "penalties", "all"])
 def test_parts_left_out(without):
     c = Probs(60, "fp16", 2003, [7, 3], True)
