@@ -37,16 +37,19 @@ __global__ void __launch_bounds__(att::Cfg<D, true>::kThreads, 1) kvq_attention_
 //                               out of S^T's layout by movmatrix
 // so a running m and l, and O, are a warp's own until the segment ends.  m moves as in the
 // other kernel.  A ninth warp copies tiles (keys and values of 64 positions, 18 KB at d = 256)
-// into a ring of ~200 KB; four warps take a tile, two tiles are under way.
+// into a ring of ~190 KB; two warps take a tile (four for 16 rows), four tiles are under way.
 template <int D_, int NT_>
 struct Few {
     static constexpr int D = D_, NT = NT_;                  // NT: blocks of 8 rows
-    static constexpr int kWarps = 8, kGroups = kWarps / 4, kThreads = 32 * (kWarps + 4);
+    static constexpr int NS = NT == 1 ? 2 : 1;              // strips of 16 positions that a warp takes at a time
+    static constexpr int kWarps = 8, kOfTile = 4 / NS, kGroups = kWarps / kOfTile, kThreads = 32 * (kWarps + 4);
     static constexpr int kCodeRow = D / 2, kScaleRow = D / 16;
     static constexpr uint32_t kRaw = att::TK * (kCodeRow + kScaleRow), kStage = 2 * kRaw;
     static constexpr int kRegs = D / 4 * NT;                // O of a lane
-    static constexpr uint32_t kJoin = 4 * kRegs * 128;      // four warps' O
-    static constexpr int kFit = int((212992 - kJoin) / kStage), kStages = kFit < 24 ? kFit : 24;
+    static constexpr uint32_t kJoin = kOfTile * kRegs * 128;  // O of a tile's warps
+    // A stage belongs to one group: its warps wait for each of its uses in turn.  (One that waited for every second use only
+    // could come to a use two ahead of what has been copied, whose parity is that of the use before.)
+    static constexpr int kFit = int((212992 - kJoin) / kStage), kStages = (kFit < 24 ? kFit : 24) / kGroups * kGroups;
     static constexpr size_t kSmem = kStages * kStage + kJoin;
     static_assert(kStages >= 4, "ring");
 };
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
     using namespace att;
     using C = Few<D, NT>;
     using Ref = Reference<__half>;
-    constexpr int kThreads = C::kThreads, kWarps = C::kWarps;
+    constexpr int kThreads = C::kThreads, kWarps = C::kWarps, NS = C::NS;
     extern __shared__ __align__(128) unsigned char smem_few[];
     __shared__ uint64_t full_bar[C::kStages], empty_bar[C::kStages], never_bar;
     __shared__ int abort_s;
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             gdn::mbar_init(full_bar + i, 1);
-            gdn::mbar_init(empty_bar + i, 4);
+            gdn::mbar_init(empty_bar + i, C::kOfTile);
         }
         gdn::mbar_init(&never_bar, 1);
         gdn::fence_mbar_init();
@@ -133,7 +136,8 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
     }
     const int ps = 1 << a.pl.shift, run = raw_run(a.pl.shift);
 
-    // 168 registers a thread at launch, 12 x 168 = 2016 of a warp's 32, shared out anew: 8 x 224 + 4 x 56 = 2016
+    // 168 registers a thread at launch, 12 x 168 = 2016 of a warp's 32, shared out anew: 8 x 224 + 4 x 56 = 2016.  (Twelve working
+    // warps of 152 registers gain nothing: 94 us for 87.)
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kWarps) {
@@ -210,30 +214,33 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
             }
         }
     } else {
-        // ---- 16 positions of every second tile -------------------------------------------
+        // ---- 32 positions of every fourth tile (or 16 of every second) --------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         Walk walk(a, start_s);
         Segment g;
         // After a wait that ran out a warp goes on without work and without waits, so that the CTA's barriers match.
         const int gr = lane >> 2, c = lane & 3;       // the row and the pair of columns of a fragment
-        const int strip = 16 * (warp & 3), group = warp >> 2;
+        const int strip = 16 * NS * (warp % C::kOfTile), group = warp / C::kOfTile;
         constexpr int KW = D / 32, VW = D / 64;       // words of codes: of a lane's part of a key, of a value
         constexpr int KS = D >= 64 ? D / 64 : 1, VS = D == 256 ? 2 : 1;  // scales of those parts
         const int piece_bytes = run * (C::kCodeRow + C::kScaleRow);
         auto codes_of = [&](int r) { return r / run * piece_bytes + r % run * C::kCodeRow; };
         auto scales_of = [&](int r) { return r / run * piece_bytes + run * C::kCodeRow + r % run * C::kScaleRow; };
-        int k_at[2], ks_at[2], v_at[4], vs_at[4];
+        int k_at[NS][2], ks_at[NS][2], v_at[NS][4], vs_at[NS][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = strip + gr + 8 * i;
-            k_at[i] = codes_of(r) + c * (C::kCodeRow / 4);
-            ks_at[i] = scales_of(r) + c * KS;
-        }
+        for (int u = 0; u < NS; ++u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = strip + 2 * c + (i & 1) + 8 * (i >> 1);
-            v_at[i] = int(C::kRaw) + codes_of(r) + gr * (C::kCodeRow / 8);
-            vs_at[i] = int(C::kRaw) + scales_of(r) + gr * (D / 8) / 16;
+            for (int i = 0; i < 2; ++i) {
+                const int r = strip + 16 * u + gr + 8 * i;
+                k_at[u][i] = codes_of(r) + c * (C::kCodeRow / 4);
+                ks_at[u][i] = scales_of(r) + c * KS;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = strip + 16 * u + 2 * c + (i & 1) + 8 * (i >> 1);
+                v_at[u][i] = int(C::kRaw) + codes_of(r) + gr * (C::kCodeRow / 8);
+                vs_at[u][i] = int(C::kRaw) + scales_of(r) + gr * (D / 8) / 16;
+            }
         }
         int4 *meta = a.meta + 2 * blockIdx.x;
         bool head_part = false, tail_part = false;
@@ -322,81 +329,96 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
 
             const int n = g.tile1 - g.tile0;
 #pragma unroll 1
-            for (int k = int(tiles_done + group) % C::kGroups; k < n; k += C::kGroups) {
+            for (int k = int(group + C::kGroups - tiles_done % C::kGroups) % C::kGroups; k < n; k += C::kGroups) {  // tile i of group i % kGroups
                 const uint32_t i = tiles_done + k;
                 const int stage = int(i % C::kStages), x0 = (g.tile0 + k) * TK + strip;
                 ok = ok && wait_bar(full_bar + stage, (i / C::kStages) & 1, abort_flag);
                 if (ok && x0 < g.limit) {
                     const unsigned char *src = ring + stage * C::kStage;
-                    const bool masked = x0 + 16 > g.safe;
-                    // ---- scores: positions gr, gr + 8 by rows 2 c, 2 c + 1; two sums, of even and odd steps
-                    float s[2][NT][4];
+                    const bool masked = x0 + 16 * NS > g.safe;
+                    // ---- scores: positions gr, gr + 8 of a strip by rows 2 c, 2 c + 1; two sums, of even and odd steps
+                    float s[NS][2][NT][4];
 #pragma unroll
-                    for (int z = 0; z < 2; ++z)
+                    for (int u = 0; u < NS; ++u)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int z = 0; z < 2; ++z)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) s[z][nt][e] = 0.f;
-                    uint32_t kw[2][KW], ksc[2];
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        load_words(src + k_at[r], kw[r]);
-                        ksc[r] = load_scales<KS>(src + ks_at[r]);
-                    }
-                    uint32_t vw[4][VW], vsc[4];
+                                for (int e = 0; e < 4; ++e) s[u][z][nt][e] = 0.f;
+                    uint32_t kw[NS][2][KW], ksc[NS][2];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        load_words(src + v_at[r], vw[r]);
-                        vsc[r] = load_scales<VS>(src + vs_at[r]);
-                    }
-#pragma unroll
-                    for (int w = 0; w < KW; ++w) {
-                        uint4 f[2];
+                    for (int u = 0; u < NS; ++u)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const uint32_t two = gdn::e4m3x2_to_f16x2((ksc[r] >> (16 * (w / 4))) & 0xffffu);
-                            f[r] = convert8(kw[r][w], __byte_perm(two, two, (w / 2) & 1 ? 0x3232 : 0x1010));
+                            load_words(src + k_at[u][r], kw[u][r]);
+                            ksc[u][r] = load_scales<KS>(src + ks_at[u][r]);
                         }
-                        const uint32_t a0[4] = {f[0].x, f[1].x, f[0].y, f[1].y}, a1[4] = {f[0].z, f[1].z, f[0].w, f[1].w};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_16816(s[0][nt], a0, q[2 * w][nt][0], q[2 * w][nt][1]);
-                            mma_16816(s[1][nt], a1, q[2 * w + 1][nt][0], q[2 * w + 1][nt][1]);
+                    for (int w = 0; w < KW; ++w)
+#pragma unroll
+                        for (int u = 0; u < NS; ++u) {
+                            uint4 f[2];
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const uint32_t two = gdn::e4m3x2_to_f16x2((ksc[u][r] >> (16 * (w / 4))) & 0xffffu);
+                                f[r] = convert8(kw[u][r][w], __byte_perm(two, two, (w / 2) & 1 ? 0x3232 : 0x1010));
+                            }
+                            const uint32_t a0[4] = {f[0].x, f[1].x, f[0].y, f[1].y}, a1[4] = {f[0].z, f[1].z, f[0].w, f[1].w};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_16816(s[u][0][nt], a0, q[2 * w][nt][0], q[2 * w][nt][1]);
+                                mma_16816(s[u][1][nt], a1, q[2 * w + 1][nt][0], q[2 * w + 1][nt][1]);
+                            }
                         }
-                    }
+                    uint32_t vw[NS][4][VW], vsc[NS][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int u = 0; u < NS; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[0][nt][e] += s[1][nt][e];
-                    if (masked) {
+                        for (int r = 0; r < 4; ++r) {
+                            load_words(src + v_at[u][r], vw[u][r]);
+                            vsc[u][r] = load_scales<VS>(src + vs_at[u][r]);
+                        }
+#pragma unroll
+                    for (int u = 0; u < NS; ++u)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int x = x0 + gr + 8 * (e >> 1);
-                                if (x >= g.limit || !sees(nt, e & 1, x)) s[0][nt][e] = -INFINITY;
-                            }
+                            for (int e = 0; e < 4; ++e) s[u][0][nt][e] += s[u][1][nt][e];
+                    if (masked) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int x = x0 + 2 * c + (r & 1) + 8 * (r >> 1);
-                            if (x >= g.limit) {  // no row sees it
-                                vsc[r] = 0;
+                        for (int u = 0; u < NS; ++u) {
 #pragma unroll
-                                for (int w = 0; w < VW; ++w) vw[r][w] = 0;
-                            } else if (x >= g.safe) {
-                                // values that are not finite: 0 here, put back at the end for the rows that see them
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int b = 0; b < VS; ++b)
-                                    if (((vsc[r] >> (8 * b)) & 0x7f) == gdn::kNanScale) {
-                                        vsc[r] &= ~(0xffu << (8 * b));
-                                        atomicOr(&nf[seg & 1], 1u << (x - g.safe));
-                                    }
+                                for (int e = 0; e < 4; ++e) {
+                                    const int x = x0 + 16 * u + gr + 8 * (e >> 1);
+                                    if (x >= g.limit || !sees(nt, e & 1, x)) s[u][0][nt][e] = -INFINITY;
+                                }
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const int x = x0 + 16 * u + 2 * c + (r & 1) + 8 * (r >> 1);
+                                if (x >= g.limit) {  // no row sees it
+                                    vsc[u][r] = 0;
+#pragma unroll
+                                    for (int w = 0; w < VW; ++w) vw[u][r][w] = 0;
+                                } else if (x >= g.safe) {
+                                    // values that are not finite: 0 here, put back at the end for the rows that see them
+#pragma unroll
+                                    for (int b = 0; b < VS; ++b)
+                                        if (((vsc[u][r] >> (8 * b)) & 0x7f) == gdn::kNanScale) {
+                                            vsc[u][r] &= ~(0xffu << (8 * b));
+                                            atomicOr(&nf[seg & 1], 1u << (x - g.safe));
+                                        }
+                                }
                             }
                         }
                     }
                     // ---- weights
                     auto largest = [&](int nt, int e) {
-                        float x = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
+                        float x = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < NS; ++u) x = fmaxf(x, fmaxf(s[u][0][nt][e], s[u][0][nt][e + 2]));
                         x = fmaxf(x, __shfl_xor_sync(full, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(full, x, 8));
                         return cr[nt][e] * fmaxf(x, __shfl_xor_sync(full, x, 16));
@@ -413,17 +435,19 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
                                 if (m[nt][e] == -INFINITY) m[nt][e] = mx - Ref::kLift;
                             }
                     }
-                    float y[NT][4], top = -INFINITY;
+                    float y[NS][NT][4], top;
                     auto exponents = [&] {
                         top = -INFINITY;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int u = 0; u < NS; ++u)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float mu = m[nt][e & 1];
-                                y[nt][e] = fmaf(s[0][nt][e], cr[nt][e & 1], mu == -INFINITY ? 0.f : -mu);
-                                top = fmaxf(top, y[nt][e]);
-                            }
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float mu = m[nt][e & 1];
+                                    y[u][nt][e] = fmaf(s[u][0][nt][e], cr[nt][e & 1], mu == -INFINITY ? 0.f : -mu);
+                                    top = fmaxf(top, y[u][nt][e]);
+                                }
                     };
                     exponents();
                     if (__any_sync(full, top > Ref::kMoveAt)) {
@@ -445,39 +469,44 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
                             }
                         exponents();
                     }
-                    uint32_t pt[NT][2];
+                    uint32_t pt[NS][NT][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float p[4];
+                    for (int u = 0; u < NS; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = exp2_approx(y[nt][e]);
-                        l[nt][0] += p[0] + p[2];
-                        l[nt][1] += p[1] + p[3];
-                        pt[nt][0] = transposed(gdn::pack_f16x2(p[0], p[1]));
-                        pt[nt][1] = transposed(gdn::pack_f16x2(p[2], p[3]));
-                    }
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float p[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) p[e] = exp2_approx(y[u][nt][e]);
+                            l[nt][0] += p[0] + p[2];
+                            l[nt][1] += p[1] + p[3];
+                            pt[u][nt][0] = transposed(gdn::pack_f16x2(p[0], p[1]));
+                            pt[u][nt][1] = transposed(gdn::pack_f16x2(p[2], p[3]));
+                        }
                     // ---- values: rows of the fragment d and d + 1, pairs of positions
-                    uint32_t vs[2][VS];  // scales of positions 2 c, 2 c + 1 and 2 c + 8, 2 c + 9
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        const uint32_t lo = gdn::e4m3x2_to_f16x2(vsc[2 * z]), hi = gdn::e4m3x2_to_f16x2(vsc[2 * z + 1]);
-                        vs[z][0] = __byte_perm(lo, hi, 0x5410);
-                        if constexpr (VS == 2) vs[z][1] = __byte_perm(lo, hi, 0x7632);
-                    }
-#pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        uint4 f[2][2];  // [low, high half of a byte][positions 2 c .., 2 c + 8 ..]
+                    for (int u = 0; u < NS; ++u) {
+                        uint32_t vs[2][VS];  // scales of positions 2 c, 2 c + 1 and 2 c + 8, 2 c + 9
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
-                            const uint32_t w0 = vw[2 * z][w], w1 = vw[2 * z + 1][w], sc = vs[z][VS == 2 ? w / 2 : 0];
-                            f[0][z] = convert8((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), sc);
-                            f[1][z] = convert8(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), sc);
+                            const uint32_t lo = gdn::e4m3x2_to_f16x2(vsc[u][2 * z]), hi = gdn::e4m3x2_to_f16x2(vsc[u][2 * z + 1]);
+                            vs[z][0] = __byte_perm(lo, hi, 0x5410);
+                            if constexpr (VS == 2) vs[z][1] = __byte_perm(lo, hi, 0x7632);
                         }
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const uint32_t va[4] = {(&f[0][0].x)[b], (&f[1][0].x)[b], (&f[0][1].x)[b], (&f[1][1].x)[b]};
+                        for (int w = 0; w < VW; ++w) {
+                            uint4 f[2][2];  // [low, high half of a byte][positions 2 c .., 2 c + 8 ..]
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_16816(o[4 * w + b][nt], va, pt[nt][0], pt[nt][1]);
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t w0 = vw[u][2 * z][w], w1 = vw[u][2 * z + 1][w], sc = vs[z][VS == 2 ? w / 2 : 0];
+                                f[0][z] = convert8((w0 & 0x0f0f0f0fu) | ((w1 << 4) & 0xf0f0f0f0u), sc);
+                                f[1][z] = convert8(((w0 >> 4) & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), sc);
+                            }
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const uint32_t va[4] = {(&f[0][0].x)[b], (&f[1][0].x)[b], (&f[0][1].x)[b], (&f[1][1].x)[b]};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma_16816(o[4 * w + b][nt], va, pt[u][nt][0], pt[u][nt][1]);
+                            }
                         }
                     }
                 }
@@ -523,22 +552,21 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
                     }
                 }
             auto cell = [&](int w, int j, int nt) { return joined + ((w * (D / 16) + j) * NT + nt) * 128 + 4 * lane; };
-            if (warp >= 4) {
+            // group by group, each adds what the one after it has put down
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j)
+            for (int z = C::kGroups - 1; z >= 0; --z) {
+                if (group == z) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        *reinterpret_cast<float4 *>(cell(warp - 4, j, nt)) = make_float4(o[j][nt][0], o[j][nt][1], o[j][nt][2], o[j][nt][3]);
-            }
-            barrier();
-            if (warp < 4) {
+                    for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float4 *at = reinterpret_cast<float4 *>(cell(warp, j, nt)), x = *at;
-                        *at = make_float4(o[j][nt][0] + x.x, o[j][nt][1] + x.y, o[j][nt][2] + x.z, o[j][nt][3] + x.w);
-                    }
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float4 *at = reinterpret_cast<float4 *>(cell(warp % C::kOfTile, j, nt));
+                            float4 x = make_float4(o[j][nt][0], o[j][nt][1], o[j][nt][2], o[j][nt][3]);
+                            if (z < C::kGroups - 1) x = make_float4(x.x + at->x, x.y + at->y, x.z + at->z, x.w + at->w);
+                            *at = x;
+                        }
+                }
+                if (z > 0) barrier();
             }
             const uint32_t bits = nf[seg & 1];  // (set before the barriers)
             if (tid == 0) nf[(seg + 1) & 1] = 0;
@@ -562,7 +590,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
                     for (int j = 0; j < 2; ++j) {
                         v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
+                        for (int w = 0; w < C::kOfTile; ++w) {
                             const float4 x = *reinterpret_cast<const float4 *>(cell(w, 2 * warp + j, nt));
                             v[j] = make_float4(v[j].x + x.x, v[j].y + x.y, v[j].z + x.z, v[j].w + x.w);
                         }
