@@ -392,45 +392,62 @@ __device__ __forceinline__ uint4 convert8(uint32_t codes, uint32_t scale2) {
 // A raw tile holds its positions in runs, a page's or all 64: a run's codes, then its scales, as a block does.
 __device__ __forceinline__ int raw_run(int shift) { return min(1 << shift, TK); }
 
+// The order of a segment's n tiles of keys and n of values in the rings: K_0 K_1 V_0 K_2 V_1 ... V_{n-1}.
+__device__ __forceinline__ bool values_at(int j, int n) { return j == 2 * n - 1 || (j > 0 && !(j & 1)); }
+__device__ __forceinline__ int tile_at(int j, int n) { return j == 2 * n - 1 ? n - 1 : j == 0 ? 0 : (j & 1) ? (j + 1) / 2 : j / 2 - 1; }
+
 // ---- the 4-bit cache's codes and scales into the ring of raw tiles -------------------------
-// A page's keys (or values) of a head are one piece of memory and one copy; of a page larger than a tile codes and
-// scales are two.
+// Two warps in turn.  A page's keys (or values) of a head are one piece of memory and one copy; of a page larger than a
+// tile codes and scales are two.
 template <typename T, typename C>
 __device__ __forceinline__ void copy_role(const Args &a, Walk &walk, unsigned char *raw, uint64_t *raw_full, uint64_t *raw_empty,
                                           volatile int *abort_flag, bool ok) {
     asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
     const unsigned full = 0xffffffffu;
-    const int lane = threadIdx.x & 31, ps = 1 << a.pl.shift, run = raw_run(a.pl.shift), runs = TK / run;
+    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) == C::kTma ? 0 : 1;
+    const int ps = 1 << a.pl.shift, run = raw_run(a.pl.shift), runs = TK / run;
     const uint32_t codes = run * C::kCodeRow, scales = run * C::kScaleRow;
-    int st = 0;
+    int st = half, issued = 0;  // (a stage belongs to one warp; a segment has an even number of tiles)
     uint32_t phase = 0;
-    long long issued = 0;
     bool bad_page = false;
     Segment g;
     while (ok && walk.next(g)) {
-        // (the first role to come to a segment: its Q rows are on their way into L2)
-        for (int u = lane; u < g.rows * C::kChunks; u += 32) {
-            const int r = u / C::kChunks;
-            const T *src = static_cast<const T *>(a.q) + (int64_t(g.q.n0) + g.i0 + r / a.G) * a.q_stride +
-                           (int64_t(g.h) * a.G + r % a.G) * C::D + 64 * (u % C::kChunks);
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        if (half == 0) {  // the first role to come to a segment: its Q rows are on their way into L2
+            for (int u = lane; u < g.rows * C::kChunks; u += 32) {
+                const int r = u / C::kChunks;
+                const T *src = static_cast<const T *>(a.q) + (int64_t(g.q.n0) + g.i0 + r / a.G) * a.q_stride +
+                               (int64_t(g.h) * a.G + r % a.G) * C::D + 64 * (u % C::kChunks);
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+            }
         }
-        // page-table entries, 32 in each of two registers, loaded ahead
         const int32_t *table = a.pl.table + int64_t(g.s) * a.pl.width;
-        const int last = (g.limit - 1) >> a.pl.shift;
-        int base = (g.tile0 * TK) >> a.pl.shift;
-        auto entry = [&](int o) { return o <= last ? table[o] : -1; };
-        int cur = entry(base + lane), nxt = entry(base + 32 + lane);
+        const int last = (g.limit - 1) >> a.pl.shift, n = g.tile1 - g.tile0;
         const int64_t head = int64_t(g.h) * a.pl.head_stride;
-        auto load = [&](const void *pool, int page, int at) {
-            if (!wait_bar(raw_empty + st, phase ^ 1, abort_flag)) return false;
-            const bool mine = lane < runs && page >= 0;
+        auto page_of = [&](int j) {  // this lane's page of the segment's item j; -1: none
+            if (j >= 2 * n) return -1;
+            const int o = (((g.tile0 + tile_at(j, n)) * TK) >> a.pl.shift) + lane;
+            return lane < runs && o <= last ? table[o] : -1;
+        };
+        int page = page_of(half);
+#pragma unroll 1
+        for (int j = half; j < 2 * n; j += 2) {
+            const int next = page_of(j + 2);  // looked up one ahead
+            const int t = g.tile0 + tile_at(j, n);
+            if (page < 0 || page >= a.pl.n_pages) {
+                bad_page |= lane < runs && ((t * TK) >> a.pl.shift) + lane <= last;
+                page = -1;
+            }
+            ok = wait_bar(raw_empty + st, phase ^ 1, abort_flag);
+            if (!ok) break;
+            const bool mine = page >= 0;
             const unsigned m = __ballot_sync(full, mine);
             if (lane == 0) gdn::mbar_arrive_expect_tx(raw_full + st, __popc(m) * (codes + scales));
             __syncwarp();
             if (mine) {
+                const int at = (t * TK) & (ps - 1);
                 unsigned char *dst = raw + st * C::kRawTile + lane * (codes + scales);
-                const unsigned char *block = static_cast<const unsigned char *>(pool) + int64_t(page) * a.pl.page_stride + head;
+                const unsigned char *block =
+                    static_cast<const unsigned char *>(values_at(j, n) ? a.v_pool : a.k_pool) + int64_t(page) * a.pl.page_stride + head;
                 if (ps == run) {
                     gdn::bulk_load(dst, block, codes + scales, raw_full + st);
                 } else {
@@ -438,52 +455,24 @@ __device__ __forceinline__ void copy_role(const Args &a, Walk &walk, unsigned ch
                     gdn::bulk_load(dst + codes, block + (int64_t(C::kCodeRow) << a.pl.shift) + at * C::kScaleRow, scales, raw_full + st);
                 }
             }
+            page = next;
             ++issued;
-            if (++st == C::kAhead) {
-                st = 0;
+            if ((st += 2) >= C::kAhead) {
+                st = half;
                 phase ^= 1;
             }
-            return true;
-        };
-        int v_page = -1;
-        for (int t = g.tile0; t <= g.tile1 && ok; ++t) {
-            int page = -1;
-            if (t < g.tile1) {
-                const int first = (t * TK) >> a.pl.shift;
-                if (first - base >= 32) {
-                    cur = nxt;
-                    base += 32;
-                    nxt = entry(base + 32 + lane);
-                }
-                const int o = first + min(lane, runs - 1) - base;
-                const int lo = __shfl_sync(full, cur, o & 31), hi = __shfl_sync(full, nxt, o & 31);
-                page = o < 32 ? lo : hi;
-                if (page < 0 || page >= a.pl.n_pages) {
-                    bad_page |= o + base <= last;
-                    page = -1;
-                }
-                ok = load(a.k_pool, page, (t * TK) & (ps - 1));
-            }
-            if (ok && t > g.tile0) ok = load(a.v_pool, v_page, ((t - 1) * TK) & (ps - 1));
-            v_page = page;
         }
     }
     if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
     // the last copies into each stage are waited for whatever has happened: none is under way when the CTA leaves
-    const int n = int(min(issued, (long long)C::kAhead));
-    for (int k = 0; k < n; ++k) {
-        if (st == 0) {
-            st = C::kAhead;
+    for (int k = min(issued, C::kAhead / 2); k > 0; --k) {
+        if ((st -= 2) < 0) {
+            st += C::kAhead;
             phase ^= 1;
         }
-        --st;
         gdn::mbar_wait_bounded(raw_full + st, phase);
     }
 }
-
-// The order of a segment's n tiles of keys and n of values in the rings: K_0 K_1 V_0 K_2 V_1 ... V_{n-1}.
-__device__ __forceinline__ bool values_at(int j, int n) { return j == 2 * n - 1 || (j > 0 && !(j & 1)); }
-__device__ __forceinline__ int tile_at(int j, int n) { return j == 2 * n - 1 ? n - 1 : j == 0 ? 0 : (j & 1) ? (j + 1) / 2 : j / 2 - 1; }
 
 // ---- raw tiles as fp16 in the ring of tiles ------------------------------------------------
 // Two groups of warps take the tiles (of keys and of values) in turn: a tile's way through a
@@ -775,7 +764,7 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
         if (k4 && (warp == kTma || warp == C::kClean)) {
             if constexpr (k4) {
                 Walk walk(a, start_s);
-                if (warp == kTma) copy_role<T, C>(a, walk, tiles + C::kRing, raw_full, raw_empty, abort_flag, ok);
+                copy_role<T, C>(a, walk, tiles + C::kRing, raw_full, raw_empty, abort_flag, ok);
             }
         } else if (warp == kTma) {
             Walk walk(a, start_s);

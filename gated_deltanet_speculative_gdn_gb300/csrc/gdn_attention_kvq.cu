@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(att::Cfg<D, true>::kThreads, 1) kvq_attention_
 //                               two words put into one byte before the conversion; P^T comes
 //                               out of S^T's layout by movmatrix
 // so a running m and l, and O, are a warp's own until the segment ends.  m moves as in the
-// other kernel.  A ninth warp copies tiles (keys and values of 64 positions, 18 KB at d = 256)
+// other kernel.  Four more warps copy tiles (keys and values of 64 positions, 18 KB at d = 256)
 // into a ring of ~190 KB; two warps take a tile (four for 16 rows), four tiles are under way.
 template <int D_, int NT_>
 struct Few {
@@ -49,9 +49,9 @@ struct Few {
     static constexpr uint32_t kJoin = kOfTile * kRegs * 128;  // O of a tile's warps
     // A stage belongs to one group: its warps wait for each of its uses in turn.  (One that waited for every second use only
     // could come to a use two ahead of what has been copied, whose parity is that of the use before.)
-    static constexpr int kFit = int((212992 - kJoin) / kStage), kStages = (kFit < 24 ? kFit : 24) / kGroups * kGroups;
+    static constexpr int kFit = int((212992 - kJoin) / kStage), kStages = (kFit < 24 ? kFit : 24) / 4 * 4;
     static constexpr size_t kSmem = kStages * kStage + kJoin;
-    static_assert(kStages >= 4, "ring");
+    static_assert(kStages >= 4 && kStages % kGroups == 0, "ring");
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
     schedule<kThreads>(a, wsum, start_s, [] { __syncthreads(); });
     __syncthreads();
     bool ok = true;
-    // (the test hook: role 1 the copies, the others one of the working warps)
+    // (the test hook: role 1 the first of the copies, the others one of the working warps)
     const int stalled = a.stall_role == 1 ? kWarps : a.stall_role;
     if (a.stall_ns && blockIdx.x == 0 && warp == stalled) {
         ok = __all_sync(full, gdn::mbar_wait_bounded(&never_bar, 0, a.stall_ns));
@@ -140,78 +140,71 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
     // warps of 152 registers gain nothing: 94 us for 87.)
     if (warp >= kWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == kWarps) {
-            Walk walk(a, start_s);
-            Segment g;
-            // ---- tiles, page by page -----------------------------------------------------
-            asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
-            const int runs = TK / run;
-            const uint32_t codes = run * C::kCodeRow, scales = run * C::kScaleRow;
-            int st = 0;
-            uint32_t phase = 0;
-            long long issued = 0;
-            bool bad_page = false;
-            while (ok && walk.next(g)) {
-                const int32_t *table = a.pl.table + int64_t(g.s) * a.pl.width;
-                const int last = (g.limit - 1) >> a.pl.shift;
-                int base = (g.tile0 * TK) >> a.pl.shift;
-                auto entry = [&](int o) { return o <= last ? table[o] : -1; };
-                int cur = entry(base + lane), nxt = entry(base + 32 + lane);
-                const int64_t head = int64_t(g.h) * a.pl.head_stride;
-                for (int t = g.tile0; t < g.tile1; ++t) {
-                    const int first = (t * TK) >> a.pl.shift;
-                    if (first - base >= 32) {
-                        cur = nxt;
-                        base += 32;
-                        nxt = entry(base + 32 + lane);
-                    }
-                    const int o = first + min(lane, runs - 1) - base;
-                    const int lo = __shfl_sync(full, cur, o & 31), hi = __shfl_sync(full, nxt, o & 31);
-                    int page = o < 32 ? lo : hi;
-                    if (page < 0 || page >= a.pl.n_pages) {
-                        bad_page |= o + base <= last;
-                        page = -1;
-                    }
-                    ok = wait_bar(empty_bar + st, phase ^ 1, abort_flag);
-                    if (!ok) break;
-                    const bool mine = lane < runs && page >= 0;
-                    const unsigned m = __ballot_sync(full, mine);
-                    if (lane == 0) gdn::mbar_arrive_expect_tx(full_bar + st, __popc(m) * 2 * (codes + scales));
-                    __syncwarp();
-                    if (mine) {
-                        const int at = (t * TK) & (ps - 1);
+        // ---- tiles, page by page, four warps in turn (one takes ~700 cycles for a tile) ------
+        Walk walk(a, start_s);
+        Segment g;
+        asm volatile("fence.proxy.async;" ::: "memory");  // what earlier kernels wrote, for the copies
+        const int runs = TK / run;
+        const uint32_t codes = run * C::kCodeRow, scales = run * C::kScaleRow;
+        uint32_t tiles_done = 0;
+        int issued = 0, st = warp - kWarps;  // (a stage belongs to one warp)
+        uint32_t phase = 0;
+        bool bad_page = false;
+        while (ok && walk.next(g)) {
+            const int32_t *table = a.pl.table + int64_t(g.s) * a.pl.width;
+            const int last = (g.limit - 1) >> a.pl.shift, n = g.tile1 - g.tile0;
+            const int64_t head = int64_t(g.h) * a.pl.head_stride;
+            auto page_of = [&](int k) {  // this lane's page of the segment's tile k; -1: none
+                const int o = (((g.tile0 + k) * TK) >> a.pl.shift) + lane;
+                return lane < runs && k < n && o <= last ? table[o] : -1;
+            };
+            int k = int(st % 4 + 4 - tiles_done % 4) % 4, page = page_of(k);
+            for (; k < n; k += 4) {
+                const int next = page_of(k + 4);  // looked up one ahead
+                const int t = g.tile0 + k;
+                if (page < 0 || page >= a.pl.n_pages) {
+                    bad_page |= lane < runs && ((t * TK) >> a.pl.shift) + lane <= last;
+                    page = -1;
+                }
+                ok = wait_bar(empty_bar + st, phase ^ 1, abort_flag);
+                if (!ok) break;
+                const bool mine = page >= 0;
+                const unsigned m = __ballot_sync(full, mine);
+                if (lane == 0) gdn::mbar_arrive_expect_tx(full_bar + st, __popc(m) * 2 * (codes + scales));
+                __syncwarp();
+                if (mine) {
+                    const int at = (t * TK) & (ps - 1);
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            unsigned char *dst = ring + st * C::kStage + v * C::kRaw + lane * (codes + scales);
-                            const unsigned char *block =
-                                static_cast<const unsigned char *>(v ? a.v_pool : a.k_pool) + int64_t(page) * a.pl.page_stride + head;
-                            if (ps == run) {
-                                gdn::bulk_load(dst, block, codes + scales, full_bar + st);
-                            } else {
-                                gdn::bulk_load(dst, block + at * C::kCodeRow, codes, full_bar + st);
-                                gdn::bulk_load(dst + codes, block + (int64_t(C::kCodeRow) << a.pl.shift) + at * C::kScaleRow, scales,
-                                               full_bar + st);
-                            }
+                    for (int v = 0; v < 2; ++v) {
+                        unsigned char *dst = ring + st * C::kStage + v * C::kRaw + lane * (codes + scales);
+                        const unsigned char *block =
+                            static_cast<const unsigned char *>(v ? a.v_pool : a.k_pool) + int64_t(page) * a.pl.page_stride + head;
+                        if (ps == run) {
+                            gdn::bulk_load(dst, block, codes + scales, full_bar + st);
+                        } else {
+                            gdn::bulk_load(dst, block + at * C::kCodeRow, codes, full_bar + st);
+                            gdn::bulk_load(dst + codes, block + (int64_t(C::kCodeRow) << a.pl.shift) + at * C::kScaleRow, scales,
+                                           full_bar + st);
                         }
                     }
-                    ++issued;
-                    if (++st == C::kStages) {
-                        st = 0;
-                        phase ^= 1;
-                    }
                 }
-            }
-            if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
-            // no copy is under way when the CTA leaves
-            const int n = int(min(issued, (long long)C::kStages));
-            for (int k = 0; k < n; ++k) {
-                if (st == 0) {
-                    st = C::kStages;
+                page = next;
+                ++issued;
+                if ((st += 4) >= C::kStages) {
+                    st -= C::kStages;
                     phase ^= 1;
                 }
-                --st;
-                gdn::mbar_wait_bounded(full_bar + st, phase);
             }
+            tiles_done += n;
+        }
+        if (bad_page) gdn::record_status(a.status, GDN_DEV_BAD_PAGE);
+        // no copy is under way when the CTA leaves
+        for (int z = min(issued, C::kStages / 4); z > 0; --z) {
+            if ((st -= 4) < 0) {
+                st += C::kStages;
+                phase ^= 1;
+            }
+            gdn::mbar_wait_bounded(full_bar + st, phase);
         }
     } else {
         // ---- 32 positions of every fourth tile (or 16 of every second) --------------------------
