@@ -37,10 +37,10 @@ struct Cfg {
     static constexpr int kStreams = D == 256 ? 1 : 2;     // softmax warpgroups, each with an O of its own
     static constexpr int kRowWarps = 4 * kStreams;
     static constexpr int kTma = kRowWarps, kMmaS = kTma + 1, kMmaO = kTma + 2, kClean = kTma + 3;
-    // 8 or 12 warps: two or three to a scheduler; with the 4-bit cache 16, the last of them its conversion
-    static constexpr int kConv = kRowWarps + 4, kConvWarps = D / 32, kConvGroup = kConvWarps / 2;
-    static constexpr int kThreads = k4 ? 512 : 32 * (kRowWarps + 4);
-    static_assert(!k4 || kConv + kConvWarps <= kThreads / 32, "warps");
+    // 8 or 12 warps: two or three to a scheduler; with the 4-bit cache 8 more for its conversion (at D = 128 four took 331 us
+    // for chunks of up to 701 tokens, eight 310, though the rows' warps have 160 registers then for 176)
+    static constexpr int kConv = kRowWarps + 4, kConvWarps = D == 64 ? 4 : 8, kConvGroup = kConvWarps / 2;
+    static constexpr int kThreads = 32 * (kRowWarps + 4 + (k4 ? 8 : 0));
     static constexpr int kChunks = D / 64;                // 128-byte columns of a row
     static constexpr uint32_t kChunkBytes = TK * 128;
     static constexpr uint32_t kTile = TK * D * 2;         // 32, 16, 8 KB
@@ -477,7 +477,7 @@ __device__ __forceinline__ void copy_role(const Args &a, Walk &walk, unsigned ch
 // ---- raw tiles as fp16 in the ring of tiles ------------------------------------------------
 // Two groups of warps take the tiles (of keys and of values) in turn: a tile's way through a
 // warp is a chain of ~1300 cycles, mostly waits, which two tiles at a time share.
-// A thread takes four units of a tile, 32 elements (16 bytes of codes, two scales) of a position
+// A thread takes two or four units of a tile, 32 elements (16 bytes of codes, two scales) of a position
 // each: a warp reads 512 consecutive bytes, and writes each unit as four 16-byte pieces in the
 // 128-byte swizzle.  A position's units lie in its 64-column chunks, whose equal pieces share
 // banks, so the lanes of chunk c begin at piece c.
@@ -485,8 +485,8 @@ template <typename C>
 __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned char *tiles, uint64_t *full_bar, uint64_t *empty_bar,
                                              const unsigned char *raw, uint64_t *raw_full, uint64_t *raw_empty, uint32_t (*nf)[4],
                                              volatile int *abort_flag, bool ok) {
-    constexpr int D = C::D, kCols = D / 32, kUnits = 4;
-    static_assert(C::kConvGroup * 32 * kUnits == TK * kCols && C::kStages % 2 == 0 && C::kAhead % 2 == 0, "units of a tile");
+    constexpr int D = C::D, kCols = D / 32, kUnits = TK * kCols / (C::kConvGroup * 32);
+    static_assert(C::kStages % 2 == 0 && C::kAhead % 2 == 0, "units of a tile");
     const int lane = threadIdx.x & 31, all = (threadIdx.x >> 5) - C::kConv;
     if (all >= C::kConvWarps) return;
     const int group = all / C::kConvGroup, cw = all % C::kConvGroup;
@@ -750,17 +750,19 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
         if (!ok) *abort_flag = 1;
     }
 
-    // The 4-bit cache's kernel: 128 registers a thread at launch, which the roles share out anew, whole groups of four
-    // warps, 16 x 128 = 2048 in all: 4 x 240 + 4 x 56 + 8 x 104 = 2016 for D = 256, 8 x 176 + 4 x 56 + 4 x 104 = 2048 else.
+    // The 4-bit cache's kernel: the registers at launch, 16 warps x 128 = 2048 for D = 256 and 20 x 96 = 1920 else, are shared
+    // out anew among whole groups of four warps: 4 x 240 + 4 x 56 + 8 x 104 = 2016, and 8 x 160 + 4 x 48 + 8 x 56 = 1920.
     // (Each at the head of its role, so that the compiler sees what holds there.)
     if (k4 && warp >= C::kConv) {
         if constexpr (k4) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+            if constexpr (D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+            else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
             Walk walk(a, start_s);
             convert_role<C>(a, walk, tiles, full_bar, empty_bar, tiles + C::kRing, raw_full, raw_empty, nf, abort_flag, ok);
         }
     } else if (warp >= C::kRowWarps) {
-        if constexpr (k4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if constexpr (k4 && D == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        else if constexpr (k4) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (k4 && (warp == kTma || warp == C::kClean)) {
             if constexpr (k4) {
                 Walk walk(a, start_s);
@@ -1018,7 +1020,7 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     } else {
         // ---- rows ------------------------------------------------------------------------
         if constexpr (k4 && D == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
-        else if constexpr (k4) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        else if constexpr (k4) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         const int w = warp & 3, stream = warp >> 2;        // lanes 32 w .. of tensor memory; the warpgroup
         const uint32_t trow = tmem + (uint32_t(w) << 21);  // this warp's lanes
         const int row = 32 * w + lane;
