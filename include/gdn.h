@@ -610,8 +610,9 @@ void gdn_test_stall_next_verify(uint64_t wait_ns);
  * (about 2 s), drain and leave, and the call reports GDN_DEV_TIMEOUT.
  * gdn_paged_attention_kvq takes it in the same way.
  *   role  0 softmax and results, 1 copies, 2 scores, 3 values' products,
- *         4 cleaning of values (with the 4-bit cache 1 and 4 are its conversion);
- *         any other is ignored */
+ *         4 cleaning of values (with the 4-bit cache its conversion; where a call
+ *         of that has 16 query rows a head at most, 1 is one of the copying warps
+ *         and the others are working warps); any other is ignored */
 void gdn_test_stall_next_attention(uint64_t wait_ns, int role);
 
 /* Name of a host or device status code ("GDN_OK", "GDN_DEV_DUP_SLOT", ...);

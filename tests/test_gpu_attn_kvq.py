@@ -299,6 +299,21 @@ def test_waits_run_out(d, role):
     check(o, ref, A, sum_of_values(cache, [300], [40], 16), big, torch.bfloat16, d)
 
 
+@pytest.mark.parametrize("role", [0, 1, 2, 3, 4])
+@pytest.mark.parametrize("d,new", [(256, 1), (128, 2), (64, 1)])
+def test_waits_run_out_few_rows(d, new, role):
+    cache, q, _ = case(20, torch.bfloat16, d, 16, 2, 16, "dense", (1, 1), [3000], [new], False)
+    ref, A, big = R.attention(q.double(), cache, [3000], [new], None, d ** -0.5)
+    a = Attn4(cache, q, [3000], [new], None, torch.bfloat16, d ** -0.5)
+    G.gdn_test_stall_next_attention(20_000_000, role)
+    a.out()
+    assert int(a.status) == G.GDN_DEV_TIMEOUT
+    a.status.zero_()
+    o = a.out()
+    assert int(a.status) == 0
+    check(o, ref, A, sum_of_values(cache, [3000], [new], 16), big, torch.bfloat16, d)
+
+
 def test_streams_and_graphs():
     """Another stream, and two captured graphs with workspaces of their own replayed one after the other."""
     cache, q, par = case(23, torch.bfloat16, 256, 16, 2, 16, "dense", (1, 1), [500, 33], [16, 9], True)
@@ -321,3 +336,20 @@ def test_streams_and_graphs():
             g.replay()
     torch.cuda.synchronize()
     assert torch.equal(a.o.cpu(), want) and torch.equal(b.o.cpu(), want) and int(a.status) == 0
+
+
+def test_graph_of_few_rows_follows_the_lengths():
+    """A captured call of single tokens, replayed while the lengths grow page by page, gives what calls give."""
+    ctx, new = [500, 33, 0, 64], [1, 1, 1, 1]
+    cache, q, _ = case(24, torch.bfloat16, 256, 16, 2, 16, "dense", (1, 1), [700, 233, 200, 264], new, False)
+    a, b = (Attn4(cache, q, ctx, new, None, torch.bfloat16, 1 / 16) for _ in range(2))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b()
+    for _ in range(12):
+        want = a.out()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(b.o.cpu(), want) and int(a.status) == int(b.status) == 0
+        a.ctx += 17
+        b.ctx += 17

@@ -359,6 +359,27 @@ def test_equal_calls_and_streams():
     assert torch.equal(a, b) and int(c.status) == 0
 
 
+@pytest.mark.parametrize("V,new", [(131072, [16] * 32), (131072, [16] * 3), (1000, [5, 0, 64, 1])])
+def test_in_a_graph(V, new):
+    """A captured call sees the inputs of each replay, and gives the bits of a plain call."""
+    c = Probs(7, "bf16", V, new, True)
+    a = Probs(8, "bf16", V, new, True)
+    want = [x.call() for x in (c, a)]
+    dims = G.GdnDims.make(c.S, c.N, c.P, 1, 1, 128, max(new))
+    x = [t.clone() for t in c.keep[:10]]
+    out = torch.zeros(c.N, c.stride, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        G.gdn_logits_probs(dims, V, c.code, x[0], c.stride, *x[1:6], c.stride, *x[6:], None, None, None, 0, None, 0, None, 0, out, c.stride, st)
+    for k in (0, 1, 0):
+        for t, y in zip(x, (c, a)[k].keep):
+            t.copy_(y)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(st) == 0 and torch.equal(out[:, :V].cpu(), want[k][:, :V].cpu())
+
+
 # ---- the history's commit ---------------------------------------------------------------
 
 
