@@ -28,7 +28,13 @@ constexpr int TK = 64;       // positions of a tile
 // short items the last (chunks of up to 701 tokens: 4 289 us, 8 263, 10 266; 64 trees 122.6, 119.5, 120.6),
 // too much those with few long ones (64 single tokens: 186.9, 187.0, 187.2; 24 191.1).  Not measured for D = 64.
 constexpr int kItemUnits = 10;
-constexpr int kNfBufs = 16;  // the ring holds the values of 12 segments at most, and one may still be going out
+// Flags of values that are not finite, by segment.  The ring holds the values of 12 segments at most (8 with the 4-bit cache),
+// and one may still be going out.
+constexpr int kNfBufs = 32;
+// The 4-bit cache's converting warps set bits, which one of them clears as it comes to a segment kNfAhead before.  A warp of the
+// other group is at most 9 segments before that one, and the rows 11 behind it (8 in the ring, two of scores, one going out).
+constexpr int kNfAhead = 12;
+static_assert(kNfAhead > 9 && kNfBufs - kNfAhead > 11, "flags that are not in use");
 
 template <int D_, bool k4_ = false>
 struct Cfg {
@@ -506,8 +512,7 @@ __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned
     Segment g;
     while (ok && walk.next(g)) {
         const int n = g.tile1 - g.tile0;
-        // (flags of a segment eight on: no warp is further ahead of this one, and none that far behind)
-        if (all == 0 && lane < 4) nf[(seg + 8) % kNfBufs][lane] = 0;
+        if (all == 0 && lane < 4) nf[(seg + kNfAhead) % kNfBufs][lane] = 0;
 #pragma unroll 1
         for (int j = group; j < 2 * n; j += 2) {
             ok = wait_bar(raw_full + st, raw_phase, abort_flag);

@@ -168,6 +168,25 @@ def test_nan_stays_where_it_is_seen(d, hq, n):
     assert torch.equal(torch.isnan(o), want)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_nan_in_many_short_sequences(d):
+    """As above for a CTA's many segments of one tile, of which several are under way at once."""
+    rng = np.random.default_rng(d)
+    S, n, hq, hkv = 1600, 7, 8, 2
+    ctx, new = [int(x) for x in rng.integers(0, 50, S)], [n] * S
+    cache, q, par = case(12, torch.float16, d, hq, hkv, 16, "dense", (1, 1), ctx, new, True)
+    want = torch.zeros(S, n, hq, d, dtype=torch.bool)
+    for s in range(S):
+        node = int(rng.integers(0, n))
+        cache.v[cache.scales_at(s, ctx[s] + node)[1, 1]] = 0x7f      # head 1, columns 16 .. 31
+        for i in range(n):
+            if node in R.path_of(par[s], i):
+                want[s, i, hq // 2:, 16:32] = True
+    a = Attn4(cache, q, ctx, new, par, torch.float16, d ** -0.5)
+    o = a.out()
+    assert int(a.status) == 0 and torch.equal(torch.isnan(o).view(S, n, hq, d), want)
+
+
 @pytest.mark.parametrize("d,new", [(256, [1, 1]), (128, [5, 2]), (256, [16, 20])])
 def test_infinite_and_nan_queries(d, new):
     """A row of q that is not finite spoils its own output only."""
