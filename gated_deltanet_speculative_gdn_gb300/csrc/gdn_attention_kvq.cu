@@ -7,11 +7,20 @@
 // as for an fp16 cache.  fp16 q rows go in as they are, bf16 rows scaled by a power of two
 // by row.  The units are factors of the scores and of the result.
 //
-// Mapping.  Beside the rows' warps (4, or 8 for d <= 128) and the two that issue products
-// stand d / 32 warps that take the place of TMA: every thread copies the codes and scales of
-// its own 64 elements of a tile kAhead tiles early (cp.async), converts them (one cvt and one
-// product for two elements) and writes them to the ring of tiles as fp16 in the 128-byte
-// swizzle.
+// Mapping.  The kernel of gdn_attention.cuh with two warps that bring pages in, as they lie in
+// memory, by one bulk copy each into a ring of raw tiles (the place of TMA and of cleaning), and 8
+// more (4 of them working for d = 64) that convert tile after tile into the ring of fp16 tiles, in the
+// 128-byte swizzle.  One conversion takes two codes and gives about 37 pairs a cycle and SM; with the
+// product by the scale 72 codes a cycle and SM were measured, so a tile of keys and values at d = 256
+// is ~460 cycles of conversion beside ~1,000 of products for 128 rows.  16-bit q rows go to tensor
+// memory through registers.  Sequences of few rows take the second kernel.
+//
+// Measured: 64 trees of 16 nodes over up to 8,192 (d = 256) 97-106 us, chunks of up to 701 over up to
+// 3,001 (d = 128) 309 (the 16-bit cache 119-122 and 262-266), 64 single tokens over up to 16,384 79
+// (184-189).  Why not faster: the trees' 128 items are dealt out over 152 SMs as in the 16-bit form, so
+// each SM has a start, an end and parts to write and join beside its tiles; and a tile passes conversion,
+// scores, softmax and values one after the other, with few tiles under way at once (the rings hold two of
+// fp16 keys and values at d = 256).
 #include <type_traits>
 
 #include "gdn_attention.cuh"
@@ -23,11 +32,11 @@ __global__ void __launch_bounds__(att::Cfg<D, true>::kThreads, 1) kvq_attention_
     attention_body<T, D, true>(nullptr, nullptr, a);
 }
 
-// ---- few rows: sequences whose query rows of a key/value head are 16 at most ---------------
+// ---- few rows: sequences of 16 query rows of a key/value head at most, 8 for d = 256 ---------
 //
 // One token of a group of 8 is 8 of the 128 rows that a tensor-memory tile has, and the way
-// through the roles above costs a tile ~2500 cycles whatever its rows: 64 single tokens over
-// up to 16,384 positions took 171 us against 49 of memory.  Here eight warps work each by
+// through the roles above costs a tile as much whatever its rows: 64 single tokens over up to
+// 16,384 positions take 148 us so, against 50 of memory.  Here eight warps work each by
 // itself on 16 positions at a time, with the products by mma.sync on the codes as they come
 // out of shared memory, converted in registers:
 //     S^T[16 x rows] = K Q^T    A: keys, a lane's elements of a position one after the other
@@ -36,7 +45,11 @@ __global__ void __launch_bounds__(att::Cfg<D, true>::kThreads, 1) kvq_attention_
 //                               two words put into one byte before the conversion; P^T comes
 //                               out of S^T's layout by movmatrix
 // so a running m and l, and O, are a warp's own until the segment ends.  m moves as in the
-// other kernel.  Four more warps copy tiles (keys and values of 64 positions, 18 KB at d = 256)
+// other kernel.  64 single tokens take 79 us so (heads of 128: 84, of 64: 63), against a floor of 50:
+// HBM at 63 %.  A warp's tile is a chain of
+// shared-memory reads, conversions and products; more warps (12 of 152 registers) did not help.
+// (Where it is used stands at its launch: at d = 256 a lane's q and O of 16 rows leave no registers for 32
+// positions at a time.)  Four more warps copy tiles (keys and values of 64 positions, 18 KB at d = 256)
 // into a ring of ~190 KB; two warps take a tile (four for 16 rows), four tiles are under way.
 template <int D_, int NT_>
 struct Few {
@@ -645,10 +658,12 @@ int launch(const gdn_attn_dims *dims, att::Args a, void *workspace, int ctas, cu
     a.meta = static_cast<int4 *>(workspace);
     a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);
     a.stall_ns = gdn::take_attention_stall(&a.stall_role);
-    // few rows
+    // Few rows (single tokens, 64 at d = 256 and 32 below, over up to 16,384 positions, 8 rows a head: 79 us at d = 256, 84 at 128,
+    // 63 at 64; the other kernel 148, 228, 181.  16 rows: 126 at 128, 95 at 64; the other 230, 181, and at d = 256 149 for 168.)
     const int64_t rows = int64_t(a.G) * dims->max_seq_tokens;
     if (rows <= 8) return launch_few<T, D, 1>(dims, a, ctas, st);
-    if (rows <= 16) return launch_few<T, D, 2>(dims, a, ctas, st);
+    if constexpr (D < 256)
+        if (rows <= 16) return launch_few<T, D, 2>(dims, a, ctas, st);
     auto k = kvq_attention_kernel<T, D>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem)) != cudaSuccess)
         return GDN_ERR_LAUNCH;

@@ -611,8 +611,8 @@ void gdn_test_stall_next_verify(uint64_t wait_ns);
  * gdn_paged_attention_kvq takes it in the same way.
  *   role  0 softmax and results, 1 copies, 2 scores, 3 values' products,
  *         4 cleaning of values (with the 4-bit cache its conversion; where a call
- *         of that has 16 query rows a head at most, 1 is one of the copying warps
- *         and the others are working warps); any other is ignored */
+ *         of that has 16 query rows a key/value head at most, 8 for d = 256, 1 is
+ *         one of the copying warps and the others are working warps); any other is ignored */
 void gdn_test_stall_next_attention(uint64_t wait_ns, int role);
 
 /* Name of a host or device status code ("GDN_OK", "GDN_DEV_DUP_SLOT", ...);
