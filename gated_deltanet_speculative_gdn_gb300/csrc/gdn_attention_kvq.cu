@@ -50,11 +50,11 @@ __global__ void __launch_bounds__(att::Cfg<D, true>::kThreads, 1) kvq_attention_
 // shared-memory reads, conversions and products; more warps (12 of 152 registers) did not help.
 // (Where it is used stands at its launch: at d = 256 a lane's q and O of 16 rows leave no registers for 32
 // positions at a time.)  Four more warps copy tiles (keys and values of 64 positions, 18 KB at d = 256)
-// into a ring of ~190 KB; two warps take a tile (four for 16 rows), four tiles are under way.
+// into a ring of ~190 KB; two warps take a tile, four tiles are under way.
 template <int D_, int NT_>
 struct Few {
     static constexpr int D = D_, NT = NT_;                  // NT: blocks of 8 rows
-    static constexpr int NS = NT == 1 ? 2 : 1;              // strips of 16 positions that a warp takes at a time
+    static constexpr int NS = 2;                            // strips of 16 positions that a warp takes at a time (1: 126 us for 111)
     static constexpr int kWarps = 8, kOfTile = 4 / NS, kGroups = kWarps / kOfTile, kThreads = 32 * (kWarps + 4);
     static constexpr int kCodeRow = D / 2, kScaleRow = D / 16;
     static constexpr uint32_t kRaw = att::TK * (kCodeRow + kScaleRow), kStage = 2 * kRaw;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
             gdn::mbar_wait_bounded(full_bar + st, phase);
         }
     } else {
-        // ---- 32 positions of every fourth tile (or 16 of every second) --------------------------
+        // ---- 32 positions of every fourth tile ---------------------------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         Walk walk(a, start_s);
         Segment g;
@@ -659,7 +659,7 @@ int launch(const gdn_attn_dims *dims, att::Args a, void *workspace, int ctas, cu
     a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);
     a.stall_ns = gdn::take_attention_stall(&a.stall_role);
     // Few rows (single tokens, 64 at d = 256 and 32 below, over up to 16,384 positions, 8 rows a head: 79 us at d = 256, 84 at 128,
-    // 63 at 64; the other kernel 148, 228, 181.  16 rows: 126 at 128, 95 at 64; the other 230, 181, and at d = 256 149 for 168.)
+    // 63 at 64; the other kernel 148, 228, 181.  16 rows: 111 at 128, 79 at 64; the other 230, 181, and at d = 256 149 for 168.)
     const int64_t rows = int64_t(a.G) * dims->max_seq_tokens;
     if (rows <= 8) return launch_few<T, D, 1>(dims, a, ctas, st);
     if constexpr (D < 256)
