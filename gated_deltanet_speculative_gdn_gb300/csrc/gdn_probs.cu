@@ -697,7 +697,7 @@ __device__ __forceinline__ unsigned long long token_path(const TokenArgs &a, int
     return path;
 }
 
-// A CTA a sequence, as in the commit itself: a round's few nodes or a prompt's many tokens.
+// CTAs of a sequence (y), as in the commit itself: one for a round's few nodes, more for a prompt's many tokens.
 __global__ void __launch_bounds__(256) token_preflight_kernel(const TokenArgs a) {
     __shared__ unsigned long long path_s;
     __shared__ int err_s;
@@ -728,11 +728,11 @@ __global__ void __launch_bounds__(256) token_preflight_kernel(const TokenArgs a)
             err = GDN_DEV_BAD_SLOT;
         } else {
             bool bad = false, dup = false;
-            for (int k = tid; k < ns; k += 256) {
+            for (int k = 256 * blockIdx.y + tid; k < ns; k += 256 * gridDim.y) {
                 const int t = a.tokens[n0 + k];
                 bad |= (!a.accepted || ((path_s >> k) & 1)) && (t < 0 || t >= a.V);
             }
-            for (int s2 = tid; s2 < a.S; s2 += 256) dup |= s2 != s && a.slot_map[s2] == slot && commits(a, s2);
+            for (int s2 = tid; s2 < a.S && blockIdx.y == 0; s2 += 256) dup |= s2 != s && a.slot_map[s2] == slot && commits(a, s2);
             if (__syncthreads_or(bad)) err = GDN_DEV_BAD_TOKEN;
             else if (__syncthreads_or(dup)) err = GDN_DEV_DUP_SLOT;
         }
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(256) token_commit_kernel(const TokenArgs a) {
         __syncthreads();
     }
     uint16_t *row = a.history + int64_t(a.slot_map[s]) * a.h_stride;
-    for (int k = tid; k < ns; k += 256) {
+    for (int k = 256 * blockIdx.y + tid; k < ns; k += 256 * gridDim.y) {
         if (a.accepted && !((path_s >> k) & 1)) continue;
         const int t = a.tokens[n0 + k];
         unsigned int *w = reinterpret_cast<unsigned int *>(row + (t & ~1));
@@ -779,11 +779,13 @@ __global__ void __launch_bounds__(256) token_commit_kernel(const TokenArgs a) {
 template <typename T>
 int launch_probs(const ProbsArgs &args, int64_t rows, int vocab, cudaStream_t st) {
     ProbsArgs a = args;
-    // A cluster whose registers hold the row, of more CTAs while there are few rows to fill the GPU with.
+    // A cluster whose registers hold the row, of more CTAs while there are few rows to fill the GPU with.  (Not all clusters of 16
+    // find their places at once: one row of 131,072 takes 8.2 us with 16 CTAs and 9.9 with 8, 12 rows 10.9 and 12.3, 16 rows
+    // 18.0 and 14.3.)
     const int sms = gdn::sm_count_current();
     if (sms < 1) return GDN_ERR_LAUNCH;
     int C = 1;
-    while (C < kMaxCluster && (int64_t(C) * kSlice < vocab || (rows * 2 * C <= 2 * sms && vocab / (2 * C) >= 2048))) C *= 2;
+    while (C < kMaxCluster && (int64_t(C) * kSlice < vocab || (rows * 2 * C <= 2 * sms && vocab / (2 * C) >= 2048 && (C < 8 || rows <= 12)))) C *= 2;
     a.groups = int((int64_t(vocab) + 7) / 8);
     const bool rest = int64_t(C) * kSlice < vocab;
     auto k = rest ? logits_probs_kernel<T, true> : logits_probs_kernel<T, false>;
@@ -895,6 +897,7 @@ extern "C" int gdn_token_commit(const gdn_dims *dims, int vocab, const int32_t *
     TokenArgs a{tokens, accepted, parents, node_off, slot_map, history, history_stride, status, int(S), int(N), int(P), vocab,
                 dims->max_seq_nodes, prompt};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (gdn::launch_pdl(token_preflight_kernel, dim3(unsigned(S)), dim3(256), 0, st, a) != cudaSuccess) return GDN_ERR_LAUNCH;
-    return gdn::launch_pdl(token_commit_kernel, dim3(unsigned(S)), dim3(256), 0, st, a) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+    const dim3 grid(unsigned(S), unsigned(std::min<int64_t>((N + S * 256 - 1) / (S * 256), 64)));
+    if (gdn::launch_pdl(token_preflight_kernel, grid, dim3(256), 0, st, a) != cudaSuccess) return GDN_ERR_LAUNCH;
+    return gdn::launch_pdl(token_commit_kernel, grid, dim3(256), 0, st, a) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
