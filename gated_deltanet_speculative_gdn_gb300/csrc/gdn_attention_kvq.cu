@@ -695,6 +695,7 @@ extern "C" int gdn_paged_attention_kvq(const gdn_attn_dims *dims, const void *q,
     int rc = gdn::check_kv4_dims(dims);
     if (rc) return rc;
     if (!gdn::good_unit(k_unit) || !gdn::good_unit(v_unit)) return GDN_ERR_ARG;
+    if (!(scale * k_unit < 1.0e38f)) return GDN_ERR_ARG;  // (their product with log2(e) is a factor of the scores)
     bool empty = false;
     rc = check_attention(dims, q, q_stride, k_pool, v_pool, gdn::kv4_pool_bytes(dims), page_table, ctx_len, node_off, parents, scale, o,
                          workspace, workspace_size, gdn_attention_kvq_workspace_bytes(dims), status, &empty);

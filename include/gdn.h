@@ -468,7 +468,7 @@ int gdn_kvq_read(const gdn_attn_dims *dims, int n_layers, int64_t layer_stride, 
  * scaled by a power of two, so that its largest element is in [2^14, 2^15) (what is
  * below 2^-39 of that is lost, and put back afterwards is the factor).
  *   workspace  at least gdn_attention_kvq_workspace_bytes(dims) bytes
- * Host errors: also GDN_ERR_ARG for a unit. */
+ * Host errors: also GDN_ERR_ARG for a unit, and for scale * k_unit from 1e38 on. */
 int gdn_paged_attention_kvq(const gdn_attn_dims *dims, const void *q, int64_t q_stride,
                             const void *k_pool, const void *v_pool, float k_unit, float v_unit,
                             const int32_t *page_table, const int32_t *ctx_len,

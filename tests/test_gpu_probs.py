@@ -462,3 +462,15 @@ def test_token_commit_errors_write_nothing():
     st.zero_()
     commit(dm, V, i32([1, 2, 3, 1 << 30, 5, 6, 7, 8]), i32([2, -1]), i32(good["par"]), i32(good["off"]), i32([1, 99]), 0, h, st)
     assert int(st) == 0 and h.sum() == 3
+
+
+@pytest.mark.parametrize("at", [0, 300, 4000])
+def test_token_commit_errors_anywhere_in_a_prompt(at):
+    """One bad token among several CTAs' shares of a long prompt: nothing of any sequence is written."""
+    V, new = 100, [5, 4001]
+    tokens = np.arange(sum(new)) % V
+    tokens[5 + at] = V
+    dm = G.GdnDims.make(2, sum(new), 2, 1, 1, 128, 1)
+    hist, st = torch.zeros(2, 104, dtype=torch.int16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    commit(dm, V, i32(tokens), None, None, i32(offsets(new)), i32([1, 0]), 1, hist, st)
+    assert int(st) == G.GDN_DEV_BAD_TOKEN and not hist.any()

@@ -142,6 +142,12 @@ def test_arguments():
     assert probs(G.GdnDims.make(2, 8, 4, 1, 1, 16, 65)) == tokens(G.GdnDims.make(2, 8, 4, 1, 1, 16, 0)) == G.GDN_ERR_DIMS
 
 
+def test_scale_times_unit():
+    """The keys' unit multiplies the scale: both in range, their product not."""
+    assert attend(dims(), scale=1e32, ku=2.0 ** 24) == attend(dims(), scale=2e38, ku=1.0) == G.GDN_ERR_ARG
+    assert attend(dims(n_tokens=0), scale=1e32, ku=2.0 ** -24) == attend(dims(n_tokens=0), scale=1e30, ku=2.0 ** 24) == G.GDN_OK
+
+
 def test_nearest_codes_are_nearest():
     """The reference's codes against a plain search over all values, ties to the even code by hand."""
     for grid in (Q.E2M1, Q.E4M3):
