@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "gdn_kv4.h"
@@ -85,7 +86,8 @@ struct Args {
     const void *__restrict__ k_pool, *__restrict__ v_pool;  // of the 16-bit cache read directly only for values that are not finite
     gdn::PagedLayout pl;
     const int32_t *__restrict__ ctx_len, *__restrict__ node_off, *__restrict__ parents;
-    float c;    // scale * log2(e), of the 4-bit cache times the keys' unit
+    float c;    // scale * log2(e), of the 4-bit cache times the keys' unit, FLT_MIN at least
+    double c_wide;  // of the 4-bit cache: that product wherever it lies
     float out;  // the values' unit; 1
     void *o;
     int32_t *status;
@@ -594,6 +596,14 @@ __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned
     }
 }
 
+// The factor of a bf16 row's scores: c times `back`, the power of two that takes back the one its q was scaled by.
+// The product is formed where fp32 does not end and then kept among its normal numbers, since 0 or infinity would make
+// NaN of a masked score (-infinity) or of a score of 0.  It changes no weight: a score is below 2^36, so times 2^-126 it
+// is nothing to an exponent, and two that are not equal are 2^-34 apart at least, so times 2^128 one of them takes all.
+__device__ __forceinline__ float row_factor(const Args &a, float back) {
+    return fminf(fmaxf(float(a.c_wide * double(back)), FLT_MIN), FLT_MAX);
+}
+
 // The 4-bit cache's kernel: a warp's 32 rows of q into its lanes of tensor memory (column `to` on), as fp16; returns what a
 // row's scores are to be multiplied by, to its lane.  fp16 does not hold every bf16: such a row is scaled by a power of
 // two that brings its largest element to 2^14 .. 2^15.  (Infinities and NaN stay what they are.)  Four rows at a time, an
@@ -1040,9 +1050,11 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
         // A segment's Q rows into tensor memory, once every S of the segment before has been formed.
         auto load_q = [&](const Segment &sg) {
             if constexpr (k4) {
-                if (w * 32 < sg.rows)
-                    c_next = a.c * load_q_rows<T, C>(static_cast<const T *>(a.q), a.q_stride, int64_t(sg.q.n0) + sg.i0, sg.h, a.G, sg.rows,
-                                                     tiles + C::kRing + C::kAhead * C::kRawTile + warp * 4096, back[warp], trow + C::kQ);
+                if (w * 32 < sg.rows) {
+                    const float b = load_q_rows<T, C>(static_cast<const T *>(a.q), a.q_stride, int64_t(sg.q.n0) + sg.i0, sg.h, a.G, sg.rows,
+                                                      tiles + C::kRing + C::kAhead * C::kRawTile + warp * 4096, back[warp], trow + C::kQ);
+                    c_next = std::is_same<T, __half>::value ? a.c : row_factor(a, b);
+                }
                 gdn::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) arrive(&q_bar);

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
                     top = max(top, __shfl_xor_sync(full, top, 2));
                     const int e = int(top >> 7), s = e == 255 ? 0 : min(14 + 127 - e, 100);
                     const float f = __uint_as_float(uint32_t(127 + s) << 23);
-                    mine = a.c * __uint_as_float(uint32_t(127 - s) << 23);
+                    mine = row_factor(a, __uint_as_float(uint32_t(127 - s) << 23));
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
                         float y[8];
@@ -704,8 +704,12 @@ extern "C" int gdn_paged_attention_kvq(const gdn_attn_dims *dims, const void *q,
     if (ctas < 1) return GDN_ERR_LAUNCH;
     const int64_t S = dims->n_seqs, N = dims->n_tokens, Hq = dims->h_q;
     const int G = int(Hq / dims->h_kv);
+    // (rounded as fp32 rounds scale * log2(e), wherever the product with the unit lies)
+    int e;
+    const float f = std::frexp(scale, &e) * 1.4426950408889634f;
+    const double c = std::ldexp(double(f), e) * double(k_unit);
     att::Args a{q, q_stride, k_pool, v_pool, gdn::paged_layout(dims, page_table), ctx_len, node_off, parents,
-                scale * k_unit * 1.4426950408889634f, v_unit, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens,
+                std::max(float(c), FLT_MIN), c, v_unit, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens,
                 int(Hq), dims->h_kv, G, att::kRows / G, 0, 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dims->dtype == GDN_BF16 ? launch_d<__nv_bfloat16>(dims, a, workspace, ctas, st)
