@@ -552,9 +552,9 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
                     const float f = l[nt][e] != 0.f ? exp2_approx(m[nt][e] - M[nt][e]) : 0.f;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        // (a warp that has seen nothing of a row has no O of it)
-                        o[j][nt][e] = f != 0.f ? f * o[j][nt][e] : 0.f;
-                        o[j][nt][e + 2] = f != 0.f ? f * o[j][nt][e + 2] : 0.f;
+                        // (of a row that the warp has seen nothing of, O is 0.  An f that underflows leaves a NaN of O one.)
+                        o[j][nt][e] *= f;
+                        o[j][nt][e + 2] *= f;
                     }
                 }
             auto cell = [&](int w, int j, int nt) { return joined + ((w * (D / 16) + j) * NT + nt) * 128 + 4 * lane; };
