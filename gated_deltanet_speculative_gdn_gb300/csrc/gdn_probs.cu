@@ -178,6 +178,14 @@ __device__ __forceinline__ Row read_row(const ProbsArgs &a, int n, int *path_out
     return r;
 }
 
+// A row looks at its own sequence's offsets; the first CTA looks at all of them (threads t of n), those that no row comes to
+// among them.
+__device__ __forceinline__ void check_offsets(const ProbsArgs &a, int t, int n) {
+    if (blockIdx.x != 0) return;
+    const int err = gdn::check_node_off(a.node_off, a.S, a.N, a.max_nodes, t, n);
+    if (err) gdn::record_status(a.status, err);
+}
+
 // touch(token) for the biases, thread t of n; whether its share of them is out of order.
 template <typename Touch>
 __device__ __forceinline__ bool for_biases(const ProbsArgs &a, const Row &row, int t, int n, Touch &&touch) {
@@ -339,6 +347,8 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
     if (warp == 0) {
         const Row r = read_row(a, n, path_s);
         if (lane == 0) row_s = r;
+    } else {
+        check_offsets(a, tid - 32, kThreads - 32);
     }
     __syncthreads();
     const Row row = row_s;
@@ -521,6 +531,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) logits_probs_rows_kernel(const
     }
     cl.sync();  // every CTA's barriers are there before one of another sends to them
     gdn::grid_dep_wait();
+    check_offsets(a, tid, kRowThreads);
 
     auto load = [&](int n, int k) {  // one thread
         const int g = (k * C + rank) * kRowThreads;
