@@ -498,6 +498,16 @@ __device__ __forceinline__ void send(const Part *to, uint64_t *bar, int rank, co
                  : "memory");
 }
 
+// Counts a warp that has read a chunk for the last time (one lane, the warp together before it); whether it is the last of
+// them.  With release and acquire, so that all warps' reads come before what the last one does next: the copy over the chunk
+// and the arrival at its barrier, by which they also come before what is done after a wait for that copy (look_up over the
+// head of the row before).
+__device__ __forceinline__ bool last_reader(int *count) {
+    int before;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(gdn::smem_addr(count)) : "memory");
+    return before == kRowWarps - 1;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads, 1) logits_probs_rows_kernel(const ProbsArgs a) {
     using K = RowChunks<T>;
@@ -639,6 +649,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) logits_probs_rows_kernel(const
             if (lane < C) send(parts[z] + rank * kRowWarps + warp, part_bar + z, lane, mine);
             __syncwarp();
         }
+        // (its place is that of the row before, which no warp reads any more: every chunk of this row has come in)
         if (n + 1 < last && warp == (n & (kRowWarps - 1))) look_up(n + 1);
         if (!row.err) {
             const int z = sent & 1;
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) logits_probs_rows_kernel(const
             float x[8];
             if (there && !greedy) x_of(k, g, x);
             __syncwarp();
-            if (lane == 0 && n + 1 < last && atomicAdd(read_s + k, 1) == kRowWarps - 1) {
+            if (lane == 0 && n + 1 < last && last_reader(read_s + k)) {
                 read_s[k] = 0;
                 load(n + 1, k);
             }
