@@ -164,7 +164,7 @@ extern "C" int gdn_paged_attention(const gdn_attn_dims *dims, const void *q, int
     if (ctas < 1) return GDN_ERR_LAUNCH;
     const int G = int(Hq / dims->h_kv);
     att::Args a{q, q_stride, k_pool, v_pool, gdn::paged_layout(dims, page_table), ctx_len, node_off, parents,
-                scale * 1.4426950408889634f, 0.0, 1.f, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens, int(Hq),
+                scale * 1.4426950408889634f, 1.f, 0, 1.f, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens, int(Hq),
                 dims->h_kv, G, att::kRows / G, 0, 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dims->dtype == GDN_BF16 ? launch_d<__nv_bfloat16>(dims, a, workspace, ctas, st)

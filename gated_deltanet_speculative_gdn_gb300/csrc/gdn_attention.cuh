@@ -87,7 +87,8 @@ struct Args {
     gdn::PagedLayout pl;
     const int32_t *__restrict__ ctx_len, *__restrict__ node_off, *__restrict__ parents;
     float c;    // scale * log2(e), of the 4-bit cache times the keys' unit, FLT_MIN at least
-    double c_wide;  // of the 4-bit cache: that product wherever it lies
+    float c_mant;  // of the 4-bit cache: that product, wherever it lies, is c_mant 2^c_exp, c_mant in [1, 2)
+    int c_exp;
     float out;  // the values' unit; 1
     void *o;
     int32_t *status;
@@ -596,23 +597,23 @@ __device__ __forceinline__ void convert_role(const Args &a, Walk &walk, unsigned
     }
 }
 
-// The factor of a bf16 row's scores: c times `back`, the power of two that takes back the one its q was scaled by.
-// The product is formed where fp32 does not end and then kept among its normal numbers, since 0 or infinity would make
-// NaN of a masked score (-infinity) or of a score of 0.  It changes no weight: a score is below 2^36, so times 2^-126 it
-// is nothing to an exponent, and two that are not equal are 2^-34 apart at least, so times 2^128 one of them takes all.
-__device__ __forceinline__ float row_factor(const Args &a, float back) {
-    return fminf(fmaxf(float(a.c_wide * double(back)), FLT_MIN), FLT_MAX);
+// The factor of a bf16 row's scores: c 2^-s for a row of q that was scaled by 2^s.  Its exponent is kept among fp32's normal
+// numbers, since 0 or infinity would make NaN of a masked score (-infinity) or of a score of 0.  That changes no weight: a
+// score is below 2^36, so times 2^-126 it is nothing to an exponent, and two that are not equal are 2^-34 apart at least, so
+// times 2^127 one of them takes all.
+__device__ __forceinline__ float row_factor(const Args &a, int s) {
+    return a.c_mant * __uint_as_float(uint32_t(127 + min(max(a.c_exp - s, -126), 127)) << 23);
 }
 
-// The 4-bit cache's kernel: a warp's 32 rows of q into its lanes of tensor memory (column `to` on), as fp16; returns what a
-// row's scores are to be multiplied by, to its lane.  fp16 does not hold every bf16: such a row is scaled by a power of
+// The 4-bit cache's kernel: a warp's 32 rows of q into its lanes of tensor memory (column `to` on), as fp16; returns the power of
+// two that a row was scaled by, to its lane.  fp16 does not hold every bf16: such a row is scaled by a power of
 // two that brings its largest element to 2^14 .. 2^15.  (Infinities and NaN stay what they are.)  Four rows at a time, an
 // eighth of a warp to 128 bytes of one, then through shared memory (`turn`, 4 KB) to the rows' own lanes.
 // One copy of little code: unrolled and in line at both places where it is called it is 40 KB, which a CTA runs through
 // once or twice, at the pace at which instructions come in (30,000 cycles each time; so 6,000).
 template <typename T, typename C>
-__device__ __noinline__ float load_q_rows(const T *q, int64_t q_stride, int64_t token, int head, int G, int rows, unsigned char *turn,
-                                          float *back, uint32_t to) {
+__device__ __noinline__ int load_q_rows(const T *q, int64_t q_stride, int64_t token, int head, int G, int rows, unsigned char *turn,
+                                        int *scaled_by, uint32_t to) {
     constexpr bool scaled = !std::is_same<T, __half>::value;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, stream = threadIdx.x >> 7;
     const T *src[8];
@@ -645,7 +646,7 @@ __device__ __noinline__ float load_q_rows(const T *q, int64_t q_stride, int64_t 
             for (int o = 4; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
             const int e = int(x >> 7), s = e == 255 ? 0 : min(14 + 127 - e, 100);
             f[i] = __uint_as_float(uint32_t(127 + s) << 23);
-            if (lane % 8 == 0) back[4 * i + lane / 8] = __uint_as_float(uint32_t(127 - s) << 23);
+            if (lane % 8 == 0) scaled_by[4 * i + lane / 8] = s;
         }
         __syncwarp();
     }
@@ -680,7 +681,7 @@ __device__ __noinline__ float load_q_rows(const T *q, int64_t q_stride, int64_t 
         __syncwarp();
     }
     tmem_wait_st();
-    return scaled ? back[lane] : 1.f;
+    return scaled ? scaled_by[lane] : 0;
 }
 
 }  // namespace att
@@ -703,7 +704,7 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
     __shared__ long long wsum[kThreads / 32];
     __shared__ int tree_par[C::kRowWarps][gdn::kMaxSeqNodes];
     __shared__ float2 ml[2][C::kStreams][kRows];  // by segment: m and l of each stream's rows
-    __shared__ float back[k4 ? C::kRowWarps : 1][32];  // factors of q's rows
+    __shared__ int scaled_by[k4 ? C::kRowWarps : 1][32];  // powers of two of q's rows
     __shared__ uint32_t nf[kNfBufs][4];  // by segment: positions from `safe` on with values that are not finite
     volatile int *abort_flag = &abort_s;
     unsigned char *tiles =
@@ -1051,9 +1052,9 @@ __device__ __forceinline__ void attention_body(const CUtensorMap *kmap, const CU
         auto load_q = [&](const Segment &sg) {
             if constexpr (k4) {
                 if (w * 32 < sg.rows) {
-                    const float b = load_q_rows<T, C>(static_cast<const T *>(a.q), a.q_stride, int64_t(sg.q.n0) + sg.i0, sg.h, a.G, sg.rows,
-                                                      tiles + C::kRing + C::kAhead * C::kRawTile + warp * 4096, back[warp], trow + C::kQ);
-                    c_next = std::is_same<T, __half>::value ? a.c : row_factor(a, b);
+                    const int by = load_q_rows<T, C>(static_cast<const T *>(a.q), a.q_stride, int64_t(sg.q.n0) + sg.i0, sg.h, a.G, sg.rows,
+                                                     tiles + C::kRing + C::kAhead * C::kRawTile + warp * 4096, scaled_by[warp], trow + C::kQ);
+                    c_next = std::is_same<T, __half>::value ? a.c : row_factor(a, by);
                 }
                 gdn::tc_fence_before_sync();
                 __syncwarp();

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Few<D, NT>::kThreads, 1) kvq_few_kernel(const 
                     top = max(top, __shfl_xor_sync(full, top, 2));
                     const int e = int(top >> 7), s = e == 255 ? 0 : min(14 + 127 - e, 100);
                     const float f = __uint_as_float(uint32_t(127 + s) << 23);
-                    mine = row_factor(a, __uint_as_float(uint32_t(127 - s) << 23));
+                    mine = row_factor(a, s);
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
                         float y[8];
@@ -705,12 +705,13 @@ extern "C" int gdn_paged_attention_kvq(const gdn_attn_dims *dims, const void *q,
     const int64_t S = dims->n_seqs, N = dims->n_tokens, Hq = dims->h_q;
     const int G = int(Hq / dims->h_kv);
     // (rounded as fp32 rounds scale * log2(e), wherever the product with the unit lies)
-    int e;
-    const float f = std::frexp(scale, &e) * 1.4426950408889634f;
-    const double c = std::ldexp(double(f), e) * double(k_unit);
+    int e, e2, eu;
+    const float mant = 2.f * std::frexp(std::frexp(scale, &e) * 1.4426950408889634f, &e2);
+    std::frexp(k_unit, &eu);
+    const int c_exp = e + e2 + eu - 2;
     att::Args a{q, q_stride, k_pool, v_pool, gdn::paged_layout(dims, page_table), ctx_len, node_off, parents,
-                std::max(float(c), FLT_MIN), c, v_unit, o, status, nullptr, nullptr, int(S), int(N), dims->max_seq_tokens,
-                int(Hq), dims->h_kv, G, att::kRows / G, 0, 0};
+                std::max(float(std::ldexp(double(mant), c_exp)), FLT_MIN), mant, c_exp, v_unit, o, status, nullptr, nullptr, int(S), int(N),
+                dims->max_seq_tokens, int(Hq), dims->h_kv, G, att::kRows / G, 0, 0};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dims->dtype == GDN_BF16 ? launch_d<__nv_bfloat16>(dims, a, workspace, ctas, st)
                                    : launch_d<__half>(dims, a, workspace, ctas, st);
