@@ -75,3 +75,27 @@ def test_large_scales(d, new):
     g = torch.Generator().manual_seed(d)
     q = (torch.randn((sum(new), 8, d), generator=g) * 2.0 ** 120).to(torch.bfloat16)
     compare(cache, q, new, torch.bfloat16, 2.0 ** 30, d)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [24, 3]])
+def test_far_pages(new):
+    """Pages 2^30 bytes apart, read beyond 2^32."""
+    d, hkv, page, stride, n_pages, dtype = 64, 2, 16, 1 << 30, 7, torch.bfloat16
+    ctx = [40, 3]
+    near = Q.make_cache4(np.random.default_rng(35), [a + b for a, b in zip(ctx, new)], hkv, d, page, extra=0)
+    block = G.gdn_kvq_block_bytes(G.AttnDims.make_kvq(1, 1, 1, 8, hkv, d, G.GDN_BF16, 1, page, 1))
+    q = torch.randn((sum(new), 8, d), generator=torch.Generator().manual_seed(5)).to(dtype)
+    ref, A, big = R.attention(q.double(), near, ctx, new, None, d ** -0.5)
+    assert near.n_pages <= n_pages
+    a = Attn4(near, q, ctx, new, None, dtype, d ** -0.5)
+    far = [torch.empty((n_pages - 1) * stride + hkv * block, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for to, buf in zip(far, (near.k, near.v)):
+        for p in range(near.n_pages):
+            at = (n_pages - 1 - p) * stride                   # the first pages last
+            to[at:at + hkv * block] = buf[p * hkv * block:(p + 1) * hkv * block].cuda()
+    a.k, a.v = far
+    a.table = torch.where(a.table < near.n_pages, n_pages - 1 - a.table, a.table)
+    a.dm = G.AttnDims.make_kvq(2, sum(new), max(new), 8, hkv, d, G.GDN_BF16, n_pages, page, near.table.shape[1], stride, block)
+    o = a.out()
+    assert int(a.status) == 0
+    check(o, ref, A, sum_of_values(near, ctx, new, 8), big, dtype, d)
