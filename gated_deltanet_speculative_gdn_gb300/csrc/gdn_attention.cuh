@@ -27,7 +27,8 @@ template <> struct Reference<__half> {  // up to 65504
 constexpr int TK = 64;       // positions of a tile
 // What an item costs beside its tiles (Q in, results out), in tiles.  Too little makes the CTAs with many
 // short items the last (chunks of up to 701 tokens: 4 289 us, 8 263, 10 266; 64 trees 122.6, 119.5, 120.6),
-// too much those with few long ones (64 single tokens: 186.9, 187.0, 187.2; 24 191.1).  Not measured for D = 64.
+// too much those with few long ones (64 single tokens: 186.9, 187.0, 187.2; 24 191.1).  Not measured for D = 64, nor
+// with the 4-bit cache, whose kernels have it from here though an item costs them something else.
 constexpr int kItemUnits = 10;
 // Flags of values that are not finite, by segment.  The ring holds the values of 12 segments at most (8 with the 4-bit cache),
 // and one may still be going out.
@@ -45,7 +46,8 @@ struct Cfg {
     static constexpr int kRowWarps = 4 * kStreams;
     static constexpr int kTma = kRowWarps, kMmaS = kTma + 1, kMmaO = kTma + 2, kClean = kTma + 3;
     // 8 or 12 warps: two or three to a scheduler; with the 4-bit cache 8 more for its conversion (at D = 128 four took 331 us
-    // for chunks of up to 701 tokens, eight 310, though the rows' warps have 160 registers then for 176)
+    // for chunks of up to 701 tokens, eight 310, though the rows' warps have 160 registers then for 176 and spill 262-278 bytes
+    // a thread for 44-90)
     static constexpr int kConv = kRowWarps + 4, kConvWarps = D == 64 ? 4 : 8, kConvGroup = kConvWarps / 2;
     static constexpr int kThreads = 32 * (kRowWarps + 4 + (k4 ? 8 : 0));
     static constexpr int kChunks = D / 64;                // 128-byte columns of a row

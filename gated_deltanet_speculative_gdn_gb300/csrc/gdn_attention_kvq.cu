@@ -16,11 +16,13 @@
 // memory through registers.  Sequences of few rows take the second kernel.
 //
 // Measured: 64 trees of 16 nodes over up to 8,192 (d = 256) 97-106 us, chunks of up to 701 over up to
-// 3,001 (d = 128) 309 (the 16-bit cache 119-122 and 262-266), 64 single tokens over up to 16,384 79
+// 3,001 (d = 128) 309-311 (the 16-bit cache 119-122 and 262-266), 64 single tokens over up to 16,384 79
 // (184-189).  Why not faster: the trees' 128 items are dealt out over 152 SMs as in the 16-bit form, so
 // each SM has a start, an end and parts to write and join beside its tiles; and a tile passes conversion,
 // scores, softmax and values one after the other, with few tiles under way at once (the rings hold two of
-// fp16 keys and values at d = 256).
+// fp16 keys and values at d = 256).  For d <= 128 the chunks are slower than over the 16-bit cache: every tile
+// is converted for 128 rows only, and the rows' warps, which gave registers to the converting ones, spill 262 (fp16)
+// and 278 bytes (bf16) a thread at d = 128, 182 and 196 at 64 (at 256 none and 8; the 16-bit form 104, 64 and none).
 #include <type_traits>
 
 #include "gdn_attention.cuh"
@@ -45,12 +47,15 @@ __global__ void __launch_bounds__(att::Cfg<D, true>::kThreads, 1) kvq_attention_
 //                               two words put into one byte before the conversion; P^T comes
 //                               out of S^T's layout by movmatrix
 // so a running m and l, and O, are a warp's own until the segment ends.  m moves as in the
-// other kernel.  64 single tokens take 79 us so (heads of 128: 84, of 64: 63), against a floor of 50:
-// HBM at 63 %.  A warp's tile is a chain of
+// other kernel.  64 single tokens take 79 us so (heads of 128: 82-85, of 64: 64), against a floor of 50 of memory
+// (63 % of a copy's rate, by the times).  A warp's tile is a chain of
 // shared-memory reads, conversions and products; more warps (12 of 152 registers) did not help.
 // (Where it is used stands at its launch: at d = 256 a lane's q and O of 16 rows leave no registers for 32
-// positions at a time.)  Four more warps copy tiles (keys and values of 64 positions, 18 KB at d = 256)
-// into a ring of ~190 KB; two warps take a tile, four tiles are under way.
+// positions at a time.)  Four more warps copy tiles (keys and values of 64 positions) into a ring; two warps take a
+// tile, four tiles are under way.  The ring has a multiple of four stages, so that each belongs to one copying warp and
+// to one group: 8 of 18 KB (144 KB) at d = 256, 20 of 9 at 128, 24 of 4.5 at 64.
+// At launch 168 registers a thread.  Spilled, of the working warps: 24 (fp16) and 32 bytes (bf16) at d = 256, 16 for
+// 16 rows at d = 128 in bf16, none otherwise.
 template <int D_, int NT_>
 struct Few {
     static constexpr int D = D_, NT = NT_;                  // NT: blocks of 8 rows
@@ -658,8 +663,8 @@ int launch(const gdn_attn_dims *dims, att::Args a, void *workspace, int ctas, cu
     a.meta = static_cast<int4 *>(workspace);
     a.parts = reinterpret_cast<float *>(a.meta + 2 * ctas);
     a.stall_ns = gdn::take_attention_stall(&a.stall_role);
-    // Few rows (single tokens, 64 at d = 256 and 32 below, over up to 16,384 positions, 8 rows a head: 79 us at d = 256, 84 at 128,
-    // 63 at 64; the other kernel 148, 228, 181.  16 rows: 111 at 128, 79 at 64; the other 230, 181, and at d = 256 149 for 168.)
+    // Few rows (single tokens, 64 at d = 256 and 32 below, over up to 16,384 positions, 8 rows a head: 79 us at d = 256, 82-85 at
+    // 128, 64 at 64; the other kernel 145, 228, 181.  16 rows: 110 at 128, 80 at 64; the other 230, 181, and at d = 256 146 for 168.)
     const int64_t rows = int64_t(a.G) * dims->max_seq_tokens;
     if (rows <= 8) return launch_few<T, D, 1>(dims, a, ctas, st);
     if constexpr (D < 256)

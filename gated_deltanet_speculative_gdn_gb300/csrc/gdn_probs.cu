@@ -11,12 +11,13 @@
 // tie is a tie.
 //
 // Mapping.  Few rows: a cluster of CTAs takes a row, each CTA runs of up to 16384 tokens
-// whose x, then 2^(..), stay in registers (four groups of 8 a thread): the row is
+// whose x, then 2^(..), stay in registers (four groups of 8 a thread; of 64 registers, for two CTAs an SM, 32 bytes
+// spill with 16-bit logits and 104 with fp32): the row is
 // read once and written once, 6 bytes a token with 16-bit logits.  (A larger vocabulary
 // than 16 slices hold reads the rest of each slice again for every pass.)  The logits are
 // requested before the row's sequence is looked up.  Bound by latency: look-ups, loads, one
-// exchange, stores; 16 rows of 131,072 tokens take 14 us, one 8.  More rows than that: the
-// second kernel, below.  Few tokens are touched by a path or a bias: a bitmap of groups of 8 in
+// exchange, stores; 16 rows of 131,072 tokens take 14 us, one 8 (fp32 logits 15; of 151,936 tokens, by clusters of 16,
+// 19 and 21; of 248,320 23 and 26).  More rows than that: the second kernel, below.  Few tokens are touched by a path or a bias: a bitmap of groups of 8 in
 // shared memory says which, and only those look into the lists; the history's 16 bits a token
 // come from L2 for all of a sequence's nodes but the first.
 #include <cooperative_groups.h>
@@ -467,8 +468,10 @@ __global__ void __launch_bounds__(kThreads, 2) logits_probs_kernel(const ProbsAr
 // sums, an exchange, and the probabilities, forming x again.  A chunk of the next row is copied as soon as a chunk of
 // this one has been read for the last time, so loads and stores share the time; the next row is looked up by a warp that
 // waits for the exchange.  1024 rows of 131,072 with penalties, biases and masks take 338-384 us so, without any of them
-// 228, against 124 of memory: bound by instructions (~190 for 8 tokens a lane and pass without them), since x is formed
-// twice; DRAM is at a third.
+// 228-238, against 124 of memory: bound by instructions (~190 for 8 tokens a lane and pass without them), since x is formed
+// twice; DRAM is at a third.  Beyond 131,072 bf16 (65,536 fp32) tokens a row is four CTAs or more, which work in step:
+// 151,936 take 479 us (floor 144), 248,320 643 (235); fp32 logits of 131,072 430-451 (164), of 151,936, by eight CTAs with
+// two or three of their four chunks in use, 830 (190), of 248,320, by eight too, 972 (311).
 struct Head {
     Row row;
     int path[gdn::kMaxSeqNodes];
@@ -501,7 +504,7 @@ __device__ __forceinline__ void send(const Part *to, uint64_t *bar, int rank, co
 // Counts a warp that has read a chunk for the last time (one lane, the warp together before it); whether it is the last of
 // them.  With release and acquire, so that all warps' reads come before what the last one does next: the copy over the chunk
 // and the arrival at its barrier, by which they also come before what is done after a wait for that copy (look_up over the
-// head of the row before).
+// head of the row before).  An mbarrier that says who came last takes 1024 rows without penalties from 238 to 246 us.
 __device__ __forceinline__ bool last_reader(int *count) {
     int before;
     asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(gdn::smem_addr(count)) : "memory");
