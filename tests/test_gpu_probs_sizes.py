@@ -11,6 +11,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # collected on CPU machines, never run there
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
+import gated_deltanet_speculative_gdn_gb300 as G  # noqa: E402
 import probs_ref as P  # noqa: E402
 from test_gpu_probs import Probs  # noqa: E402
 
@@ -102,3 +103,32 @@ def test_extreme_temperatures(t, V, new):
     ok = P.allowed_of(c.mask[0], V)
     want = (np.arange(V) == top).astype(float) if t < 1 else ok / ok.sum()
     assert int(c.status) == 0 and np.allclose(got, want, rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("V,new,far", [(5000, [3, 1], 1 << 30), (16384, [64] * 5, 1 << 24)])
+def test_far_rows(V, new, far):
+    """Rows of logits, probabilities, history and masks whose places pass 2^32 elements: the bits of dense ones."""
+    c = Probs(173, "bf16", V, new, True, slots=len(new))
+    c.biases([9] * c.S).masks()
+    dense = c.call()
+    logits, _, _, _, _, hist, _, _, _, _, _, _, _, mask, _ = c.keep
+    assert int(c.status) == 0
+
+    def spread(x, stride):
+        y = torch.empty((len(x) - 1) * stride + x.shape[1], dtype=x.dtype, device="cuda")
+        y.as_strided(x.shape, (stride, 1)).copy_(x)
+        return y
+
+    masks = far // 8                                              # (words of 32 tokens)
+    p = torch.full(((c.N - 1) * far + c.ps,), 7.0, device="cuda")
+    dm = G.GdnDims.make(c.S, c.N, c.P, 1, 1, 128, max(new))
+    _, tok, par, off, slot, _, rep, freq, pres, temp, b_off, b_tok, b_val, _, _ = c.keep
+    G.gdn_logits_probs(dm, V, c.code, spread(logits, far), far, tok, par, off, slot, spread(hist, far), far, rep, freq, pres, temp, b_off, b_tok, b_val,
+                       b_tok.numel(), spread(mask, masks), masks, None, c.N, p, far, c.status)
+    assert int(c.status) == 0 and torch.equal(p.as_strided(dense.shape, (far, 1)), dense)
+    h = torch.zeros((c.P - 1) * far + c.stride, dtype=torch.int16, device="cuda")
+    G.gdn_token_commit(dm, V, tok, None, None, off, slot, 0, h, far, c.status)
+    assert int(c.status) == 0
+    want = np.zeros((c.P, c.stride), np.int16)
+    np.add.at(want, (c.slot.repeat(new), c.tokens), 1)
+    assert np.array_equal(h.as_strided((c.P, c.stride), (far, 1)).cpu().numpy(), want)
